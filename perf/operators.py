@@ -185,6 +185,7 @@ def _buffers(c, s):
     elif c["op"] == "adamw":
         s["opt"] = steps.AdamW(s["p"], s["m"], s["v"] if c["bits"] == 32 else s["r"], s.get("e"), lr=s["lr"],
                                betas=(s["beta1"], s["beta2"]), eps=s["eps"], weight_decay=s["wd"], t=s["t"] - 1)
+        s["opt"].bind_grads(s["g"])
     else:
         n, m, t = c["rows"], c["cols"], DT[c["dtype"]]
         if c["op"] == "norm_fwd":
@@ -322,7 +323,7 @@ def _own(s, c):
         ops.ionn_layer_norm_bwd(s["dy"], s["x"], s["mean"], s["rstd"], s["dx"], gamma=s["gamma"], dgamma=s["dgamma"],
                                 dbeta=s["dbeta"], workspace=s["ws"])
         return [s["dx"], s["dgamma"], s["dbeta"]]
-    s["opt"].step(s["g"])
+    s["opt"].step()
     return [s["p"], s["m"], s["v"]] if c["bits"] == 32 else [s["p"], s["m"], s["r"], s["e"]]
 
 
