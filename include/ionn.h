@@ -670,6 +670,158 @@ int apt_adjust_mixed(int L, void *const *W, const int32_t *wbytes, const int64_t
                      int32_t *gavg_count, double t_min, double t_max, int k_min,
                      int k_max, int32_t *dk_out, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* The floating-point operations around the integer products ([DFP] section  */
+/* 4: the integer kernels do the products, the operations around them run in */
+/* floating point): a Linear layer on DFP-8 operands with bias, activation   */
+/* and residual in its epilogue, its backward pass, layer norm and AdamW.    */
+/*                                                                          */
+/* A DFP-8 tensor is int8 mantissas I plus one shared exponent E (a device   */
+/* int32 in [-128, 127]): value I * 2^E ([DFP] section 3 with P = 8).        */
+/* Floating tensors are of type `dtype` (one of the IONN_F32 ... values) and */
+/* row-major; arithmetic is in float32 and a value is rounded to its type    */
+/* once, when it is stored.  Every tensor must be aligned to its element     */
+/* size; 16-byte aligned tensors whose rows are multiples of 16 bytes take   */
+/* the vector paths.                                                         */
+/* ------------------------------------------------------------------------ */
+
+enum { IONN_F32 = 0, IONN_BF16 = 1, IONN_F16 = 2 };
+
+/* gelu: z * Phi(z), Phi the normal distribution function; gelu_tanh: its
+ * approximation z / 2 * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))); silu:
+ * z / (1 + exp(-z)). */
+enum {
+    IONN_ACT_NONE = 0,
+    IONN_ACT_RELU = 1,
+    IONN_ACT_GELU = 2,
+    IONN_ACT_GELU_TANH = 3,
+    IONN_ACT_SILU = 4
+};
+
+/* Longest reduction of the DFP-8 products: the int32 sum of this many
+ * products of int8 values cannot overflow. */
+#define IONN_DFP8_MAX_REDUCTION 131071
+
+/* Floating point -> DFP-8: max |x| = f * 2^q (f in [1, 2)) gives E = q - 6
+ * (0 for an all-zero x) and out = sat8(round_to_nearest_even(x / 2^E)).
+ * x: dtype [n]; out: int8 [n]; e_out: device int32; status_out (nullable,
+ * device int32): 0, 1 when E leaves the signed 8-bit range (E still
+ * written), 2 when x holds a NaN or infinity (outputs then unspecified).
+ * absmax (nullable): device uint32 that holds the float32 bits of max |x|,
+ * as the absmax arguments below leave them; the maximum is then not taken
+ * again.  Without it the call takes it, in `workspace` (4-byte aligned,
+ * dfp8_from_float_workspace_bytes() bytes).  n >= 1. */
+size_t dfp8_from_float_workspace_bytes(void);
+int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax,
+                    int8_t *out, int32_t *e_out, int32_t *status_out,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Forward of a Linear layer on DFP-8 operands:
+ *   z[b][o] = fl(sum_i X[b][i] * W[o][i]) * 2^(eX + eW) + bias[o]
+ *   Y[b][o] = act(z[b][o]) + residual[b][o]
+ * with the sum exact in int32.  X: int8 [B][IN]; W: int8 [OUT][IN]; bias
+ * (nullable): float [OUT]; act: IONN_ACT_*; residual (nullable), Y: dtype
+ * [B][OUT] (Y may be the residual itself); Z (nullable): dtype [B][OUT],
+ * receives z for the backward pass.  absmax_Y (nullable): device uint32,
+ * max-combined with the float32 bits of |Y| before its rounding (a NaN counts
+ * above every number), to be rounded by dfp8_from_float.  B, OUT in
+ * [0, 2^30]; 0 <= IN <= IONN_DFP8_MAX_REDUCTION (IN = 0: the sum is 0).
+ * workspace: 16-byte aligned, dfp8_linear_fwd_workspace_bytes(B, IN, OUT)
+ * bytes (may be 0). */
+size_t dfp8_linear_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT);
+int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W,
+                    const int32_t *eW, const float *bias, int act,
+                    const void *residual, void *Z, void *Y, int dtype,
+                    int64_t B, int64_t IN, int64_t OUT, uint32_t *absmax_Y,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of that layer, for the error dY of Y:
+ *   dZ = dY * act'(Z)                       (float32, not stored)
+ *   gb[o] = sum_b dZ[b][o]                  (float32, a fixed order)
+ *   dZ8, edZ = DFP-8 of dZ, as dfp8_from_float converts
+ *   dX = fl(dZ8 . W) * 2^(edZ + eW),  G = fl(dZ8^T . X) * 2^(edZ + eX)
+ * (the residual's gradient is dY itself).  dY: dtype [B][OUT]; Z: dtype
+ * [B][OUT] as the forward stored it (may be NULL for IONN_ACT_NONE); dZ8:
+ * int8 [B][OUT] and edZ: device int32 (written); dX (nullable): dtype
+ * [B][IN]; G (nullable): dtype [OUT][IN]; gb (nullable): float [OUT].
+ * status_out (nullable, device int32): as in dfp8_from_float, for dZ.
+ * B, IN, OUT in [0, 2^30]; OUT <= IONN_DFP8_MAX_REDUCTION with dX, B <= it
+ * with G.
+ * B = 0 writes G = 0 and gb = 0; OUT = 0 writes dX = 0; edZ = 0 either way.
+ * workspace: 16-byte aligned, dfp8_linear_bwd_workspace_bytes(B, IN, OUT)
+ * bytes. */
+size_t dfp8_linear_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT);
+int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype,
+                    const int8_t *X, const int32_t *eX, const int8_t *W,
+                    const int32_t *eW, int8_t *dZ8, int32_t *edZ, void *dX,
+                    void *G, float *gb, int64_t B, int64_t IN, int64_t OUT,
+                    int32_t *status_out, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Layer norm over the rows of x:
+ *   mean[r] = sum_c x[r][c] / cols, rstd[r] = 1 / sqrt(sum_c (x[r][c] -
+ *   mean[r])^2 / cols + eps),
+ *   y[r][c] = (x[r][c] - mean[r]) * rstd[r] * gamma[c] + beta[c].
+ * x, y: dtype [rows][cols] (y may be x); gamma (nullable: 1), beta
+ * (nullable: 0): float [cols]; mean, rstd (nullable): float [rows], written
+ * for the backward pass.  absmax_y as in dfp8_linear_fwd.  rows, cols >= 0
+ * and below 2^31; eps >= 0. */
+int ionn_layer_norm_fwd(const void *x, const float *gamma, const float *beta,
+                        double eps, void *y, float *mean, float *rstd,
+                        int dtype, int64_t rows, int64_t cols,
+                        uint32_t *absmax_y, void *stream);
+
+/* Its gradient, for the error dy of y, with h = (x - mean) * rstd and
+ * d = dy * gamma:
+ *   dx = rstd * (d - mean_c(d) - h * mean_c(d * h)) + dres
+ *   dgamma[c] = sum_r dy[r][c] * h[r][c],  dbeta[c] = sum_r dy[r][c].
+ * dres (nullable): dtype [rows][cols], the gradient that reaches x past the
+ * norm (the residual branch); dx may be dy or dres.  dgamma, dbeta
+ * (nullable): float [cols], summed in an order that the sizes fix (0 for
+ * rows = 0).  workspace: 16-byte aligned,
+ * ionn_layer_norm_bwd_workspace_bytes(rows, cols) bytes (needed where dgamma
+ * or dbeta is asked for). */
+size_t ionn_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
+                        const float *rstd, const float *gamma, const void *dres,
+                        void *dx, float *dgamma, float *dbeta, int dtype,
+                        int64_t rows, int64_t cols, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* One AdamW step of L tensors, in place.  Per element, each operation
+ * rounded to float32 on its own (none fused):
+ *   g = G * grad_scale
+ *   m = beta1 * m + (1 - beta1) * g,  v = beta2 * v + ((1 - beta2) * g) * g
+ *   u = m / (sqrt(v) * (1 / sqrt(1 - beta2^t)) + eps)
+ *   P = P * (1 - lr * weight_decay) - (lr / (1 - beta1^t)) * u
+ * (the scalar factors computed in double and rounded once).  P: float32
+ * [n[l]] master weights; G: [n[l]] of type g_dtype.
+ * state_bits 32: M, V float32 [n[l]] hold m and v; S NULL.
+ * state_bits 8: blocks of IONN_ADAMW_BLOCK elements (the last one shorter).
+ * M and V hold 8-bit floating codes of OCP E4M3 (1-4-3, bias 7, largest
+ * 448), of m and of r = sqrt(v): m = code * 2^S[l][2 b], r = code *
+ * 2^S[l][2 b + 1] in block b, S[l]: int8 [2 * blocks].  The step works on
+ * the float32 m and v and stores both again: for a block's largest finite
+ * magnitude f * 2^q (f in [1, 2)) the exponent is q - 8 where f <= 1.75,
+ * q - 7 otherwise, at least -126 (0 for an all-zero block); codes round to
+ * nearest even, except that a positive r never becomes 0 (the smallest code
+ * takes its place, so that no later step divides by a vanished r).  A value
+ * that is not finite becomes the NaN code 0x7f; the block's others are unaffected.
+ * t: the number of this step, from 1.  For a captured graph, step (nullable,
+ * device int32) gives t and lr_dev (nullable, device float) gives lr when the
+ * kernel runs; the caller advances them.  grad_scale (nullable, device
+ * float): 1.  absmax_P (nullable, device uint32 [L]): max-combined with the
+ * float32 bits of |P| after the step, for dfp8_from_float.
+ * L >= 1; P, G, M, V, S, n are HOST arrays; 1 <= n[l] <= 2^40.
+ * 0 <= beta1, beta2 < 1; eps >= 0; lr and weight_decay finite. */
+#define IONN_ADAMW_BLOCK 256
+int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype,
+                    void *const *M, void *const *V, int8_t *const *S,
+                    int state_bits, const int64_t *n, int64_t t, double lr,
+                    double beta1, double beta2, double eps, double weight_decay,
+                    const int32_t *step, const float *lr_dev,
+                    const float *grad_scale, uint32_t *absmax_P, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,6 +72,17 @@ SIGNATURES = {
     "ionn_relu_mask_i32": (_I, [_P, _P, _I64, _P, _P]),
     "ionn_model_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I64]),
     "ionn_model_forward": (_I, [_P, _I, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "dfp8_from_float_workspace_bytes": (ctypes.c_size_t, []),
+    "dfp8_from_float": (_I, [_P, _I, _I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dfp8_linear_fwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "dfp8_linear_fwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "dfp8_linear_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "dfp8_linear_bwd": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P,
+                             ctypes.c_size_t, _P]),
+    "ionn_layer_norm_fwd": (_I, [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I, _I64, _I64, _P, _P]),
+    "ionn_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "ionn_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "ionn_adamw_step": (_I, [_I, _P, _P, _I, _P, _P, _P, _I, _P, _I64] + [ctypes.c_double] * 5 + [_P, _P, _P, _P, _P]),
     "ionn_model_backward": (_I, [_P, _I, _P, _I64, _P, _P, _P, _I, _I, _I, _P, ctypes.c_size_t, _P, _P]),
 }
 

@@ -1,0 +1,316 @@
+// AdamW over many tensors in one launch per 64 of them, with float32 master
+// weights and the two moments held in float32 or in 8 bits ("Mixed Precision
+// Training of Convolutional Neural Networks using Integer Operations",
+// section 4: the weight update runs in floating point, on FP32 weights).
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   P = P (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Bound by HBM: per weight it reads P, g, m, v and writes P, m, v, 28 bytes
+// with float32 states and a float32 gradient, 12 + 1/32 + the gradient's
+// with 8-bit ones.  A wavefront takes 1024 weights as four chunks of 256, a
+// lane four consecutive ones of each, so that every access is a contiguous
+// run and a chunk is one 8-bit block: its largest magnitude is a reduction
+// inside the wavefront, and no state is read twice.
+//
+// 8-bit states are E4M3 codes with one power-of-two exponent per block of
+// 256.  The second moment is kept as its root r = sqrt(v): E4M3 spans 2^18
+// from its smallest to its largest value, so the root covers 2^36 of v inside
+// a block, and the step needs the root anyway.
+#include "float_ops.h"
+
+namespace ionn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunks = 4;                                   // chunks of 256 weights per wavefront
+constexpr int kWaveElems = kChunks * IONN_ADAMW_BLOCK;
+constexpr int kBlockElems = kWaveElems * (kThreads / 64);    // 4096
+constexpr int kTable = 64;                                   // tensors per launch
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+static_assert(IONN_ADAMW_BLOCK == 256, "a block is 64 lanes of four weights");
+
+struct Table {
+    float *P[kTable];
+    const void *G[kTable];
+    void *M[kTable], *V[kTable];
+    int8_t *S[kTable];
+    int64_t n[kTable];
+    int32_t first[kTable + 1];  // first workgroup of each tensor; first[L] = grid size
+    int32_t L;
+};
+
+// Everything about the step that is the same for every weight.
+struct Hyper {
+    double lr, beta1, beta2, eps, wd;
+    int64_t t;
+    const int32_t *step;
+    const float *lr_dev, *grad_scale;
+    uint32_t *absmax;
+};
+
+struct Factors {
+    float b1, c1, b2, c2, rs2, eps, decay, size, scale;
+};
+
+// b^t by repeated squaring, the same operations on the host and the device.
+__host__ __device__ inline double ipow(double b, uint64_t t) {
+#pragma clang fp contract(off)
+    double r = 1.0;
+    for (; t; t >>= 1, b = b * b)
+        if (t & 1) r = r * b;
+    return r;
+}
+
+__host__ __device__ inline Factors make_factors(const Hyper &h, int64_t t, double lr) {
+#pragma clang fp contract(off)
+    Factors f;
+    f.b1 = float(h.beta1);
+    f.c1 = float(1.0 - h.beta1);
+    f.b2 = float(h.beta2);
+    f.c2 = float(1.0 - h.beta2);
+    f.rs2 = float(1.0 / __builtin_sqrt(1.0 - ipow(h.beta2, uint64_t(t))));
+    f.eps = float(h.eps);
+    f.decay = float(1.0 - lr * h.wd);
+    f.size = float(lr / (1.0 - ipow(h.beta1, uint64_t(t))));
+    f.scale = 1.0f;
+    return f;
+}
+
+// One weight: p, m and v (or, ROOT, r = sqrt(v) on entry in v's place) are
+// updated; r returns sqrt of the new v.  No operation is fused with another.
+__device__ __forceinline__ void step_one(const Factors &f, float g, float &p, float &m, float &v, float &r) {
+#pragma clang fp contract(off)
+    m = f.b1 * m + f.c1 * g;
+    v = f.b2 * v + (f.c2 * g) * g;
+    r = sqrtf(v);
+    const float u = m / (r * f.rs2 + f.eps);
+    p = p * f.decay - f.size * u;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // e in [-126, 127]
+
+// The exponent of a block from the bits of its largest finite magnitude f 2^q.
+__device__ __forceinline__ int block_exponent(uint32_t bits) {
+    const int e = int(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return bits == 0u ? 0 : (e < -126 ? -126 : e);
+}
+
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t b = mag_bits(x);
+    return b < 0x7f800000u ? b : 0u;
+}
+
+// Four E4M3 codes of a dword as floats, and back (to nearest even; the
+// values are within the format's range; a NaN or an infinity becomes code 0x7f).
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+    x[0] = lo.x;
+    x[1] = lo.y;
+    x[2] = hi.x;
+    x[3] = hi.y;
+}
+
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4]) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, mag_bits(x[i]));
+    if (top >= 0x7f800000u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (mag_bits(x[i]) >= 0x7f800000u) w = (w & ~(0xff << (8 * i))) | 0x7f << (8 * i);
+    }
+    return uint32_t(w);
+}
+
+// Four bytes at any address, the first `valid` of them.
+__device__ __forceinline__ uint32_t load4(const uint8_t *p, int valid) {
+    if (valid >= 4) return *reinterpret_cast<const __attribute__((aligned(1))) uint32_t *>(p);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i < valid) w |= uint32_t(p[i]) << (8 * i);
+    return w;
+}
+
+__device__ __forceinline__ void store4(uint8_t *p, uint32_t w, int valid) {
+    if (valid >= 4) {
+        *reinterpret_cast<__attribute__((aligned(1))) uint32_t *>(p) = w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i < valid) p[i] = uint8_t(w >> (8 * i));
+}
+
+template <class T, bool Q8>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Factors f) {
+    int l = 0;
+    while (l + 1 < tab.L && int(blockIdx.x) >= tab.first[l + 1]) ++l;
+    const int64_t n = tab.n[l];
+    const int lane = threadIdx.x & 63;
+    const int64_t w0 = int64_t(int(blockIdx.x) - tab.first[l]) * kBlockElems + int64_t(threadIdx.x >> 6) * kWaveElems;
+    float *__restrict__ P = tab.P[l];
+    const T *__restrict__ G = static_cast<const T *>(tab.G[l]);
+    float *M = static_cast<float *>(tab.M[l]), *V = static_cast<float *>(tab.V[l]);
+    uint8_t *M8 = static_cast<uint8_t *>(tab.M[l]), *V8 = static_cast<uint8_t *>(tab.V[l]);
+    int8_t *S = tab.S[l];
+    typename Vec<float, 4>::type p[kChunks], m[kChunks], v[kChunks];
+    typename Vec<T, 4>::type g[kChunks];
+    uint32_t mw[kChunks], vw[kChunks];
+    int em[kChunks], ev[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int64_t i = w0 + c * 256 + lane * 4;
+        const int valid = i < n ? int(n - i < 4 ? n - i : 4) : 0;
+        p[c] = load_raw<float, 4>(P + i, valid);
+        g[c] = load_raw<T, 4>(G + i, valid);
+        if (Q8) {
+            mw[c] = load4(M8 + i, valid);
+            vw[c] = load4(V8 + i, valid);
+            const int64_t b = w0 / 256 + c;
+            em[c] = valid > 0 ? S[2 * b] : 0;
+            ev[c] = valid > 0 ? S[2 * b + 1] : 0;
+        } else {
+            m[c] = load_raw<float, 4>(M + i, valid);
+            v[c] = load_raw<float, 4>(V + i, valid);
+        }
+    }
+    if (h.step || h.lr_dev) f = make_factors(h, h.step ? int64_t(*h.step) : h.t, h.lr_dev ? double(*h.lr_dev) : h.lr);
+    const float scale = h.grad_scale ? *h.grad_scale : 1.0f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int64_t i = w0 + c * 256 + lane * 4;
+        if (w0 + c * 256 >= n) break;  // the same for the whole wavefront
+        const int valid = i < n ? int(n - i < 4 ? n - i : 4) : 0;
+        float pn[4], mn[4], vn[4], rn[4];
+        if (Q8) {
+            decode4(mw[c], mn);
+            decode4(vw[c], vn);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mn[e] *= pow2f(em[c]);
+                const float r = vn[e] * pow2f(ev[c]);
+                vn[e] = r * r;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            pn[e] = p[c][e];
+            if (!Q8) {
+                mn[e] = m[c][e];
+                vn[e] = v[c][e];
+            }
+            step_one(f, float(g[c][e]) * scale, pn[e], mn[e], vn[e], rn[e]);
+            if (e < valid) top = max(top, mag_bits(pn[e]));
+        }
+        store_vec<float, 4>(P + i, pn, valid);
+        if (Q8) {
+            uint32_t am = 0, av = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                am = max(am, e < valid ? finite_bits(mn[e]) : 0u);
+                av = max(av, e < valid ? finite_bits(rn[e]) : 0u);
+            }
+            const int xm = block_exponent(wave_max_u32(am)), xv = block_exponent(wave_max_u32(av));
+            float sm[4], sv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sm[e] = mn[e] * pow2f(-xm);
+                sv[e] = rn[e] * pow2f(-xv);
+                // a positive root keeps at least the smallest code, 2^-9
+                if (rn[e] > 0.0f && sv[e] < 0x1p-9f) sv[e] = 0x1p-9f;
+            }
+            store4(M8 + i, encode4(sm), valid);
+            store4(V8 + i, encode4(sv), valid);
+            if (lane == 0) {
+                const int64_t b = w0 / 256 + c;
+                S[2 * b] = int8_t(xm);
+                S[2 * b + 1] = int8_t(xv);
+            }
+        } else {
+            store_vec<float, 4>(M + i, mn, valid);
+            store_vec<float, 4>(V + i, vn, valid);
+        }
+    }
+    if (h.absmax) {
+        top = wave_max_u32(top);
+        if (lane == 0) publish_max_u32(h.absmax + l, top);
+    }
+}
+
+}  // namespace
+}  // namespace ionn
+
+using namespace ionn;
+
+extern "C" {
+
+int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype, void *const *M, void *const *V,
+                    int8_t *const *S, int state_bits, const int64_t *n, int64_t t, double lr, double beta1,
+                    double beta2, double eps, double weight_decay, const int32_t *step, const float *lr_dev,
+                    const float *grad_scale, uint32_t *absmax_P, void *stream) {
+    clear_error();
+    IONN_REQUIRE(L >= 1, IONN_ERR_SHAPE, "ionn_adamw_step: L = %d < 1", L);
+    IONN_REQUIRE(dtype_ok(g_dtype), IONN_ERR_ARG, "ionn_adamw_step: g_dtype = %d", g_dtype);
+    IONN_REQUIRE(state_bits == 32 || state_bits == 8, IONN_ERR_ARG, "ionn_adamw_step: state_bits = %d (8 or 32)",
+                 state_bits);
+    IONN_REQUIRE(P && G && M && V && n && (state_bits == 32 || S), IONN_ERR_ARG, "ionn_adamw_step: NULL array");
+    IONN_REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, IONN_ERR_RANGE,
+                 "ionn_adamw_step: beta1 = %g, beta2 = %g outside [0, 1)", beta1, beta2);
+    IONN_REQUIRE(eps >= 0.0 && eps <= 3.0e38 && lr >= -3.0e38 && lr <= 3.0e38 && weight_decay >= -3.0e38 &&
+                     weight_decay <= 3.0e38,
+                 IONN_ERR_RANGE, "ionn_adamw_step: eps = %g, lr = %g, weight_decay = %g", eps, lr, weight_decay);
+    IONN_REQUIRE(step || t >= 1, IONN_ERR_RANGE, "ionn_adamw_step: t = %lld < 1", (long long)t);
+    IONN_REQUIRE(aligned(step, 4) && aligned(lr_dev, 4) && aligned(grad_scale, 4) && aligned(absmax_P, 4),
+                 IONN_ERR_ALIGN, "ionn_adamw_step: device scalars must be 4-byte aligned");
+    const size_t gs = dtype_size(g_dtype), ss = state_bits == 32 ? 4 : 1;
+    for (int l = 0; l < L; ++l) {
+        IONN_REQUIRE(n[l] >= 1 && n[l] <= kMaxElems, IONN_ERR_SHAPE, "ionn_adamw_step: tensor %d has n = %lld", l,
+                     (long long)n[l]);
+        IONN_REQUIRE(P[l] && G[l] && M[l] && V[l] && (state_bits == 32 || S[l]), IONN_ERR_ARG,
+                     "ionn_adamw_step: tensor %d has a NULL pointer", l);
+        IONN_REQUIRE(aligned(P[l], 4) && aligned(G[l], gs) && aligned(M[l], ss) && aligned(V[l], ss), IONN_ERR_ALIGN,
+                     "ionn_adamw_step: tensor %d must be aligned to its element size", l);
+    }
+    Hyper h{lr, beta1, beta2, eps, weight_decay, t, step, lr_dev, grad_scale, nullptr};
+    const Factors f = make_factors(h, t < 1 ? 1 : t, lr);
+    hipStream_t st = as_stream(stream);
+    int l = 0;
+    while (l < L) {
+        Table tab;
+        memset(&tab, 0, sizeof(tab));
+        int64_t blocks = 0;
+        h.absmax = absmax_P ? absmax_P + l : nullptr;
+        int k = 0;
+        for (; k < kTable && l < L; ++k, ++l) {
+            const int64_t b = (n[l] + kBlockElems - 1) / kBlockElems;
+            if (blocks + b > 0x7fffffff) break;  // (a single tensor has at most 2^28)
+            tab.P[k] = P[l];
+            tab.G[k] = G[l];
+            tab.M[k] = M[l];
+            tab.V[k] = V[l];
+            tab.S[k] = state_bits == 8 ? S[l] : nullptr;
+            tab.n[k] = n[l];
+            tab.first[k] = int32_t(blocks);
+            blocks += b;
+        }
+        tab.first[k] = int32_t(blocks);
+        tab.L = k;
+        with_dtype(g_dtype, [&](auto tag) {
+            using T = decltype(tag);
+            if (state_bits == 8)
+                adamw_kernel<T, true><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(tab, h, f);
+            else
+                adamw_kernel<T, false><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(tab, h, f);
+        });
+        if (int rc = check_launch("ionn_adamw_step")) return rc;
+    }
+    return IONN_OK;
+}
+
+}  // extern "C"

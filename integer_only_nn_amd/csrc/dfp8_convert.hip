@@ -1,0 +1,284 @@
+// Conversion of floating tensors to DFP-8 (8-bit mantissas, one shared
+// exponent from the exponent of the largest magnitude: "Mixed Precision
+// Training of Convolutional Neural Networks using Integer Operations", 3.1),
+// and the same behind an activation's derivative, where a Linear layer's
+// error becomes the operand of its gradients.
+//
+// The exponent needs the maximum of the whole tensor before the first value
+// is rounded, so both are two passes, bound by HBM: one that leaves each
+// workgroup's maximum (and the error's column sums), one that rounds.  The
+// second pass computes the derivative again rather than read it back: a
+// float32 copy would cost 8 bytes per element where dY and Z cost 4 in the
+// 16-bit types.  Each workgroup of it reduces the first pass's maxima itself
+// (at most 4 KiB, from L2), which saves the launch, the cleared scalar and
+// the queue of atomics of a shared maximum.
+#include "dfp8_convert.h"
+
+namespace ionn {
+namespace dfp8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    __shared__ uint32_t red[kThreads / 64];
+    v = wave_max_u32(v);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// ---- a floating tensor -------------------------------------------------------
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void max_kernel(const T *__restrict__ x, int64_t n,
+                                                       uint32_t *__restrict__ part) {
+    constexpr int VE = 16 / sizeof(T);
+    uint32_t m = 0;
+    const int64_t step = int64_t(gridDim.x) * kThreads * VE;
+    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE; i < n; i += step) {
+        const auto v = load_raw<T, VE>(x + i, int(n - i < VE ? n - i : VE));
+#pragma unroll
+        for (int e = 0; e < VE; ++e) m = max(m, mag_bits(float(v[e])));
+    }
+    m = block_max(m);
+    if (threadIdx.x == 0) part[blockIdx.x] = m;
+}
+
+__device__ __forceinline__ void store_bytes(int8_t *p, const int32_t *q, int count, int valid) {
+    if (valid >= count) {
+        if (count == 8)
+            *reinterpret_cast<__attribute__((aligned(1))) uint64_t *>(p) =
+                uint64_t(pack4_u8(q[0], q[1], q[2], q[3])) | uint64_t(pack4_u8(q[4], q[5], q[6], q[7])) << 32;
+        else
+            *reinterpret_cast<__attribute__((aligned(1))) uint32_t *>(p) = pack4_u8(q[0], q[1], q[2], q[3]);
+        return;
+    }
+    for (int e = 0; e < valid; ++e) p[e] = int8_t(q[e]);
+}
+
+// The largest of the first pass's maxima.
+__device__ __forceinline__ uint32_t all_max(const uint32_t *__restrict__ part, int nparts) {
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < nparts; i += kThreads) m = max(m, part[i]);
+    return block_max(m);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void round_kernel(const T *__restrict__ x, int64_t n,
+                                                         const uint32_t *__restrict__ part, int nparts,
+                                                         int8_t *__restrict__ out, int32_t *__restrict__ e_out,
+                                                         int32_t *__restrict__ status) {
+    constexpr int VE = 16 / sizeof(T);
+    const uint32_t m = all_max(part, nparts);
+    const int E = dfp8_exponent(m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *e_out = E;
+        if (status) *status = dfp8_status(m, E);
+    }
+    const int64_t step = int64_t(gridDim.x) * kThreads * VE;
+    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE; i < n; i += step) {
+        const int valid = int(n - i < VE ? n - i : VE);
+        const auto v = load_raw<T, VE>(x + i, valid);
+        int32_t q[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) q[e] = dfp8_mantissa(float(v[e]), -E);
+        store_bytes(out + i, q, VE, valid);
+    }
+}
+
+// ---- the error behind an activation ------------------------------------------
+
+// Workgroup (strip, chunk): the strip's columns over the chunk's rows, four
+// wavefronts of 64 / lanes rows each at a time.
+template <class T, int ACT>
+__global__ __launch_bounds__(kThreads) void act_sums_kernel(const T *__restrict__ dY, const T *__restrict__ Z,
+                                                            int64_t B, int OUT, int lanes_log, int64_t chunk_rows,
+                                                            uint32_t *__restrict__ part_max,
+                                                            float *__restrict__ part_sum) {
+    constexpr int VE = 16 / sizeof(T);
+    __shared__ float fold[kThreads / 64][64 * VE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lanes = 1 << lanes_log, per_wave = 64 >> lanes_log;
+    const int c = (int(blockIdx.x) * lanes + (lane & (lanes - 1))) * VE;
+    const int64_t r1 = min(B, int64_t(blockIdx.y + 1) * chunk_rows);
+    float s[VE] = {};
+    uint32_t m = 0;
+    if (c < OUT) {
+        const int valid = OUT - c;
+        for (int64_t r = int64_t(blockIdx.y) * chunk_rows + wave * per_wave + (lane >> lanes_log); r < r1;
+             r += (kThreads / 64) * per_wave) {
+            const auto y = load_raw<T, VE>(dY + r * OUT + c, valid);
+            typename Vec<T, VE>::type z;
+            if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + r * OUT + c, valid);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT>(float(z[e]));
+                s[e] += d;
+                m = max(m, e < valid ? mag_bits(d) : 0u);
+            }
+        }
+    }
+    // the row groups of a wavefront, then the wavefronts
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+        for (int off = lanes; off < 64; off <<= 1) s[e] += __shfl_xor(s[e], off, 64);
+        fold[wave][(lane & (lanes - 1)) * VE + e] = s[e];
+    }
+    m = block_max(m);  // (its barrier orders fold as well)
+    if (threadIdx.x == 0) part_max[blockIdx.y * gridDim.x + blockIdx.x] = m;
+    if (part_sum == nullptr) return;
+    for (int i = threadIdx.x; i < lanes * VE; i += kThreads) {
+        const int col = int(blockIdx.x) * lanes * VE + i;
+        if (col < OUT)
+            part_sum[int64_t(blockIdx.y) * OUT + col] = (fold[0][i] + fold[1][i]) + (fold[2][i] + fold[3][i]);
+    }
+}
+
+// Workgroups below n_round round the errors; those from it on add up the
+// chunks' column sums, 64 columns each, every fourth chunk per wavefront.
+template <class T, int ACT>
+__global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict__ dY, const T *__restrict__ Z,
+                                                             int64_t n, int OUT, const uint32_t *__restrict__ part_max,
+                                                             int nparts, int n_round, const float *__restrict__ part_sum,
+                                                             int chunks, int8_t *__restrict__ dZ8,
+                                                             int32_t *__restrict__ edZ, float *__restrict__ gb,
+                                                             int32_t *__restrict__ status) {
+    constexpr int VE = 16 / sizeof(T);
+    if (int(blockIdx.x) >= n_round) {
+        __shared__ float red[kThreads / 64][64];
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int64_t c = int64_t(int(blockIdx.x) - n_round) * 64 + lane;
+        float s = 0.0f;
+        if (c < OUT) {
+#pragma unroll 8
+            for (int k = wave; k < chunks; k += kThreads / 64) s += part_sum[int64_t(k) * OUT + c];
+        }
+        red[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && c < OUT) gb[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        return;
+    }
+    const uint32_t m = all_max(part_max, nparts);
+    const int E = dfp8_exponent(m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *edZ = E;
+        if (status) *status = dfp8_status(m, E);
+    }
+    const int64_t step = int64_t(n_round) * kThreads * VE;
+    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE; i < n; i += step) {
+        const int valid = int(n - i < VE ? n - i : VE);
+        const auto y = load_raw<T, VE>(dY + i, valid);
+        typename Vec<T, VE>::type z;
+        if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + i, valid);
+        int32_t q[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT>(float(z[e]));
+            q[e] = dfp8_mantissa(d, -E);
+        }
+        store_bytes(dZ8 + i, q, VE, valid);
+    }
+}
+
+// Workgroups for a pass over n values of es bytes, 16 bytes per thread.
+unsigned pass_groups(int64_t n, size_t es, int64_t most) {
+    const int64_t per = kThreads * int64_t(16 / es);
+    const int64_t b = (n + per - 1) / per;
+    return unsigned(b < most ? b : most);
+}
+
+}  // namespace
+
+ActLayout act_layout(int64_t B, int64_t OUT, size_t es) {
+    const int64_t ve = int64_t(16 / es);
+    ActLayout a;
+    a.lanes = 1;
+    while (a.lanes < 64 && a.lanes * ve < OUT) a.lanes *= 2;
+    const int64_t strips = (OUT + a.lanes * ve - 1) / (a.lanes * ve);
+    a.strips = int(strips);
+    // at least four rows per lane in a range, and about kMaxParts workgroups
+    const int64_t least = int64_t(4) * (kThreads / a.lanes);
+    int64_t chunks = kMaxParts / strips;
+    if (chunks > (B + least - 1) / least) chunks = (B + least - 1) / least;
+    if (chunks < 1) chunks = 1;
+    a.rows = (B + chunks - 1) / chunks;
+    a.chunks = int((B + a.rows - 1) / a.rows);
+    return a;
+}
+
+size_t act_workspace_bytes(int64_t B, int64_t OUT) {
+    size_t most = 0;
+    for (size_t es : {size_t(2), size_t(4)}) {
+        const ActLayout a = act_layout(B, OUT, es);
+        const size_t maxima = (size_t(a.strips) * a.chunks * sizeof(uint32_t) + 15) & ~size_t(15);
+        const size_t b = maxima + size_t(a.chunks) * OUT * sizeof(float);
+        most = b > most ? b : most;
+    }
+    return (most + 15) & ~size_t(15);
+}
+
+int launch_act_bwd(const void *dY, const void *Z, int act, int dtype, int64_t B, int64_t OUT, int8_t *dZ8,
+                   int32_t *edZ, float *gb, int32_t *status, void *workspace, hipStream_t st) {
+    const ActLayout a = act_layout(B, OUT, dtype_size(dtype));
+    const int nparts = a.strips * a.chunks;
+    uint32_t *maxima = static_cast<uint32_t *>(workspace);
+    float *sums = gb ? reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                                 ((size_t(nparts) * sizeof(uint32_t) + 15) & ~size_t(15)))
+                     : nullptr;
+    int lanes_log = 0;
+    while ((1 << lanes_log) < a.lanes) ++lanes_log;
+    const unsigned n_round = pass_groups(B * OUT, dtype_size(dtype), 2048);
+    const unsigned n_sum = gb ? unsigned((OUT + 63) / 64) : 0u;
+    with_dtype(dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const T *y = static_cast<const T *>(dY), *z = static_cast<const T *>(Z);
+        with_act(act, [&](auto ac) {
+            constexpr int ACT = decltype(ac)::value;
+            act_sums_kernel<T, ACT><<<dim3(unsigned(a.strips), unsigned(a.chunks)), dim3(kThreads), 0, st>>>(
+                y, z, B, int(OUT), lanes_log, a.rows, maxima, sums);
+            act_round_kernel<T, ACT><<<dim3(n_round + n_sum), dim3(kThreads), 0, st>>>(
+                y, z, B * OUT, int(OUT), maxima, nparts, int(n_round), sums, a.chunks, dZ8, edZ, gb, status);
+        });
+    });
+    return check_launch("dfp8_linear_bwd");
+}
+
+}  // namespace dfp8
+}  // namespace ionn
+
+using namespace ionn;
+using namespace ionn::dfp8;
+
+extern "C" {
+
+size_t dfp8_from_float_workspace_bytes(void) { return kMaxParts * sizeof(uint32_t); }
+
+int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax, int8_t *out, int32_t *e_out,
+                    int32_t *status_out, void *workspace, size_t workspace_bytes, void *stream) {
+    clear_error();
+    IONN_REQUIRE(dtype_ok(dtype), IONN_ERR_ARG, "dfp8_from_float: dtype = %d", dtype);
+    IONN_REQUIRE(n >= 1 && n <= (int64_t(1) << 40), IONN_ERR_SHAPE, "dfp8_from_float: n = %lld", (long long)n);
+    IONN_REQUIRE(x && out && e_out, IONN_ERR_ARG, "dfp8_from_float: NULL argument");
+    IONN_REQUIRE(aligned(x, dtype_size(dtype)) && aligned(e_out, 4) && aligned(status_out, 4) && aligned(absmax, 4),
+                 IONN_ERR_ALIGN, "dfp8_from_float: x must be aligned to its element size, the scalars to 4 bytes");
+    IONN_REQUIRE(absmax || (workspace && aligned(workspace, 4) && workspace_bytes >= dfp8_from_float_workspace_bytes()),
+                 IONN_ERR_WORKSPACE, "dfp8_from_float: needs a 4-byte aligned workspace of %zu bytes",
+                 dfp8_from_float_workspace_bytes());
+    hipStream_t st = as_stream(stream);
+    uint32_t *part = static_cast<uint32_t *>(workspace);
+    int nparts = 1;
+    with_dtype(dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const T *p = static_cast<const T *>(x);
+        if (!absmax) {
+            nparts = int(pass_groups(n, sizeof(T), kMaxParts));
+            max_kernel<T><<<dim3(unsigned(nparts)), dim3(kThreads), 0, st>>>(p, n, part);
+        }
+        round_kernel<T><<<dim3(pass_groups(n, sizeof(T), 2048)), dim3(kThreads), 0, st>>>(
+            p, n, absmax ? absmax : part, nparts, out, e_out, status_out);
+    });
+    return check_launch("dfp8_from_float");
+}
+
+}  // extern "C"

@@ -525,3 +525,136 @@ def apt_adjust(Ws, k, e_w, gavg_sum, gavg_count, t_min, t_max, k_min=2, k_max=16
                            _p(gavg_sum, torch.float64, L, "gavg_sum"), _p(gavg_count, i32, L, "gavg_count"),
                            float(t_min), float(t_max), int(k_min), int(k_max), _p(dk_out, i32, L, "dk_out"),
                            _stream(stream)), "apt_adjust")
+
+
+# ---- floating-point operations around the DFP-8 products ---------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ADAMW_BLOCK = 256  # elements of an 8-bit optimiser state that share an exponent
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _dtype(t, name):
+    """The library's number of a floating tensor's type."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+        raise TypeError(f"{name}: expected a float32, bfloat16 or float16 tensor")
+    return _FLOATS[t.dtype]
+
+
+def _act(act):
+    """The library's number of an activation, given by number or name."""
+    return ACTIVATIONS[act] if isinstance(act, str) else int(act)
+
+
+def _same(cond, what):
+    if not cond:
+        raise ValueError(f"shape mismatch: {what}")
+
+
+def dfp8_from_float_workspace_bytes():
+    return int(lib().dfp8_from_float_workspace_bytes())
+
+
+def dfp8_from_float(x, out, e_out, absmax=None, workspace=None, status_out=None, stream=None):
+    _same(x.numel() == out.numel(), "x and out")
+    check(lib().dfp8_from_float(_p(x, name="x"), _dtype(x, "x"), x.numel(), _p(absmax, u32, 1, "absmax"),
+                                _p(out, i8, name="out"), _p(e_out, i32, 1, "e_out"),
+                                _p(status_out, i32, 1, "status_out"), *_ws(workspace), _stream(stream)),
+          "dfp8_from_float")
+
+
+def dfp8_linear_fwd_workspace_bytes(B, IN, OUT):
+    return int(lib().dfp8_linear_fwd_workspace_bytes(int(B), int(IN), int(OUT)))
+
+
+def dfp8_linear_fwd(X, eX, W, eW, Y, bias=None, act=0, residual=None, Z=None, absmax_Y=None, workspace=None,
+                    stream=None):
+    B, IN = X.shape
+    OUT = W.shape[0]
+    dt = Y.dtype
+    _same(W.shape == (OUT, IN) and Y.shape == (B, OUT), "X, W and Y")
+    _same((residual is None or residual.shape == (B, OUT)) and (Z is None or Z.shape == (B, OUT)) and
+          (bias is None or bias.numel() == OUT), "bias, residual and Z")
+    check(lib().dfp8_linear_fwd(_p(X, i8, name="X"), _p(eX, i32, 1, "eX"), _p(W, i8, name="W"), _p(eW, i32, 1, "eW"),
+                                _p(bias, f32, name="bias"), _act(act), _p(residual, dt, name="residual"),
+                                _p(Z, dt, name="Z"), _p(Y, name="Y"), _dtype(Y, "Y"), B, IN, OUT,
+                                _p(absmax_Y, u32, 1, "absmax_Y"), *_ws(workspace), _stream(stream)),
+          "dfp8_linear_fwd")
+
+
+def dfp8_linear_bwd_workspace_bytes(B, IN, OUT):
+    return int(lib().dfp8_linear_bwd_workspace_bytes(int(B), int(IN), int(OUT)))
+
+
+def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None, workspace=None, status_out=None,
+                    stream=None):
+    """Z may be None for no activation; X and eX are read for G, W and eW for dX."""
+    B, OUT = dY.shape
+    IN = (X if X is not None else W).shape[1]
+    dt = dY.dtype
+    _same((Z is None or Z.shape == (B, OUT)) and dZ8.shape == (B, OUT), "dY, Z and dZ8")
+    _same((X is None or X.shape == (B, IN)) and (W is None or W.shape == (OUT, IN)), "X and W")
+    _same((dX is None or dX.shape == (B, IN)) and (G is None or G.shape == (OUT, IN)) and
+          (gb is None or gb.numel() == OUT), "dX, G and gb")
+    check(lib().dfp8_linear_bwd(_p(dY, name="dY"), _p(Z, dt, name="Z"), _act(act), _dtype(dY, "dY"),
+                                _p(X, i8, name="X"), _p(eX, i32, 1, "eX"), _p(W, i8, name="W"), _p(eW, i32, 1, "eW"),
+                                _p(dZ8, i8, name="dZ8"), _p(edZ, i32, 1, "edZ"), _p(dX, dt, name="dX"),
+                                _p(G, dt, name="G"), _p(gb, f32, name="gb"), B, IN, OUT,
+                                _p(status_out, i32, 1, "status_out"), *_ws(workspace), _stream(stream)),
+          "dfp8_linear_bwd")
+
+
+def ionn_layer_norm_fwd(x, y, gamma=None, beta=None, eps=1e-5, mean=None, rstd=None, absmax_y=None, stream=None):
+    rows, cols = x.shape
+    _same(y.shape == (rows, cols) and (gamma is None or gamma.numel() == cols) and
+          (beta is None or beta.numel() == cols), "x, y, gamma and beta")
+    _same((mean is None or mean.numel() == rows) and (rstd is None or rstd.numel() == rows), "mean and rstd")
+    check(lib().ionn_layer_norm_fwd(_p(x, name="x"), _p(gamma, f32, name="gamma"), _p(beta, f32, name="beta"),
+                                    float(eps), _p(y, x.dtype, name="y"), _p(mean, f32, name="mean"),
+                                    _p(rstd, f32, name="rstd"), _dtype(x, "x"), rows, cols,
+                                    _p(absmax_y, u32, 1, "absmax_y"), _stream(stream)), "ionn_layer_norm_fwd")
+
+
+def ionn_layer_norm_bwd_workspace_bytes(rows, cols):
+    return int(lib().ionn_layer_norm_bwd_workspace_bytes(int(rows), int(cols)))
+
+
+def ionn_layer_norm_bwd(dy, x, mean, rstd, dx, gamma=None, dres=None, dgamma=None, dbeta=None, workspace=None,
+                        stream=None):
+    rows, cols = x.shape
+    dt = x.dtype
+    _same(dy.shape == x.shape and dx.shape == x.shape and (dres is None or dres.shape == x.shape), "dy, x, dx and dres")
+    _same(mean.numel() == rows and rstd.numel() == rows, "mean and rstd")
+    _same(all(t is None or t.numel() == cols for t in (gamma, dgamma, dbeta)), "gamma, dgamma and dbeta")
+    check(lib().ionn_layer_norm_bwd(_p(dy, dt, name="dy"), _p(x, name="x"), _p(mean, f32, name="mean"),
+                                    _p(rstd, f32, name="rstd"), _p(gamma, f32, name="gamma"), _p(dres, dt, name="dres"),
+                                    _p(dx, dt, name="dx"), _p(dgamma, f32, name="dgamma"), _p(dbeta, f32, name="dbeta"),
+                                    _dtype(x, "x"), rows, cols, *_ws(workspace), _stream(stream)),
+          "ionn_layer_norm_bwd")
+
+
+def _state_ptrs(ts, bits, name):
+    """Pointers of optimiser states: float32, or one byte per element (uint8,
+    int8 or float8_e4m3fn tensors of codes)."""
+    if bits == 8 and any(t.element_size() != 1 for t in ts):
+        raise TypeError(f"{name}: 8-bit states are held in tensors of one byte per element")
+    return _ptr_array(ts, f32 if bits == 32 else None, name)
+
+
+def ionn_adamw_step(Ps, Gs, Ms, Vs, t, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, Ss=None, step=None,
+                    lr_dev=None, grad_scale=None, absmax_P=None, stream=None):
+    """One step of every tensor (lists of device tensors); 8-bit states where
+    Ss (int8 [blocks][2] per tensor) is given."""
+    L = len(Ps)
+    bits = 32 if Ss is None else 8
+    _same(len(Gs) == L and len(Ms) == L and len(Vs) == L and (Ss is None or len(Ss) == L), "lists of tensors")
+    _same(all(p.numel() == x.numel() for xs in (Gs, Ms, Vs) for p, x in zip(Ps, xs)), "P, G, M and V of a tensor")
+    _same(Ss is None or all(s.numel() == 2 * -(-p.numel() // ADAMW_BLOCK) for p, s in zip(Ps, Ss)), "S of a tensor")
+    if L == 0:
+        return
+    check(lib().ionn_adamw_step(L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
+                                _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"),
+                                None if Ss is None else _ptr_array(Ss, i8, "S"), bits, _sizes(Ps), int(t), float(lr),
+                                float(beta1), float(beta2), float(eps), float(weight_decay), _p(step, i32, 1, "step"),
+                                _p(lr_dev, f32, 1, "lr_dev"), _p(grad_scale, f32, 1, "grad_scale"),
+                                _p(absmax_P, u32, L, "absmax_P"), _stream(stream)), "ionn_adamw_step")

@@ -434,3 +434,83 @@ class AptLayers:
             ops.check(ops.lib().apt_adjust_mixed(L, self._Wp, self._wb, *args), "apt_adjust_mixed")
         else:
             ops.check(ops.lib().apt_adjust(L, self._Wp, *args), "apt_adjust")
+
+
+# ---------------------------------------------------------------------------
+# AdamW over a model's tensors (ionn_adamw_step).
+# ---------------------------------------------------------------------------
+
+class AdamW:
+    """The optimiser of a list of float32 master weights, updated in place.
+    Ms and Vs: the moments, float32 tensors; or, with Ss (int8 [blocks][2] per
+    tensor), codes of one byte of m and of sqrt(v) (make() allocates either
+    kind, cleared).  The ctypes arrays are built once (bind_grads for the
+    gradient buffers), so a step costs one library call.
+
+    t counts the steps taken.  With on_device the count and the learning rate
+    live in device scalars (self.step_dev, advanced by each step, and
+    self.lr_dev), so that steps can be captured in a graph and replayed."""
+
+    def __init__(self, Ps, Ms, Vs, Ss=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, t=0,
+                 on_device=False):
+        self.P, self.M, self.V, self.S = list(Ps), list(Ms), list(Vs), None if Ss is None else list(Ss)
+        self.lr, self.betas, self.eps, self.weight_decay, self.t = lr, betas, eps, weight_decay, int(t)
+        bits = 32 if Ss is None else 8
+        for xs in (self.M, self.V):
+            ops._same(len(xs) == len(self.P) and all(x.numel() == p.numel() for x, p in zip(xs, self.P)),
+                      "weights and states")
+        if Ss is not None:
+            ops._same(len(self.S) == len(self.P) and
+                      all(s.numel() == 2 * -(-p.numel() // ops.ADAMW_BLOCK) for s, p in zip(self.S, self.P)),
+                      "weights and state exponents")
+        self._bits = bits
+        self._Pp = ops._ptr_array(self.P, torch.float32, "P")
+        self._Mp, self._Vp = ops._state_ptrs(self.M, bits, "M"), ops._state_ptrs(self.V, bits, "V")
+        self._Sp = None if Ss is None else ops._ptr_array(self.S, torch.int8, "S")
+        self._n = ops._sizes(self.P)
+        self._G = None
+        self.step_dev = self.lr_dev = None
+        if on_device:
+            dev = self.P[0].device
+            self.step_dev = torch.tensor([self.t], dtype=torch.int32, device=dev)
+            self.lr_dev = torch.tensor([lr], dtype=torch.float32, device=dev)
+
+    @staticmethod
+    def make(Ps, bits=32, **kw):
+        """Cleared states of 32 or 8 bits for these weights."""
+        if bits == 32:
+            return AdamW(Ps, [torch.zeros_like(p) for p in Ps], [torch.zeros_like(p) for p in Ps], **kw)
+        if bits != 8:
+            raise ValueError(f"bits = {bits} (8 or 32)")
+        codes = lambda: [torch.zeros(p.shape, dtype=torch.uint8, device=p.device) for p in Ps]  # noqa: E731
+        blocks = [torch.zeros(-(-p.numel() // ops.ADAMW_BLOCK), 2, dtype=torch.int8, device=p.device) for p in Ps]
+        return AdamW(Ps, codes(), codes(), blocks, **kw)
+
+    def bind_grads(self, Gs):
+        """Fix the gradient buffers (device tensors of one floating type, one
+        per weight) that step() reads when it is given none."""
+        if len(Gs) != len(self.P) or any(g.numel() != p.numel() for g, p in zip(Gs, self.P)):
+            raise ValueError("one gradient per weight tensor, of its size")
+        if self.P:
+            self._G = (list(Gs), ops._ptr_array(Gs, Gs[0].dtype, "G"), ops._dtype(Gs[0], "G"))
+
+    def step(self, Gs=None, grad_scale=None, absmax_P=None, stream=None):
+        """One step with gradients Gs (None: the bound buffers)."""
+        if not self.P:
+            return
+        if Gs is not None:
+            self.bind_grads(Gs)
+        if self._G is None:
+            raise ValueError("no gradient buffers")
+        if self.step_dev is not None:
+            if stream is None:
+                self.step_dev.add_(1)
+            else:
+                with torch.cuda.stream(stream):
+                    self.step_dev.add_(1)
+        self.t += 1
+        ops.check(ops.lib().ionn_adamw_step(
+            len(self.P), self._Pp, self._G[1], self._G[2], self._Mp, self._Vp, self._Sp, self._bits, self._n, self.t,
+            float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps), float(self.weight_decay),
+            ops._p(self.step_dev), ops._p(self.lr_dev), ops._p(grad_scale, torch.float32, 1, "grad_scale"),
+            ops._p(absmax_P, torch.int32, len(self.P), "absmax_P"), ops._stream(stream)), "ionn_adamw_step")

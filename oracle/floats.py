@@ -1,0 +1,176 @@
+"""CPU oracle of the floating-point operations around the DFP-8 products:
+the Linear layer's epilogue and its backward pass, layer norm, AdamW and the
+DFP-8 and E4M3 conversions, each the definition written out in numpy.  Test
+infrastructure only.
+
+Everything is in float64 except AdamW, whose definition fixes the rounding of
+every operation to float32 and is therefore reproduced bit for bit.
+"""
+import math
+
+import numpy as np
+
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+ADAMW_BLOCK = 256
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+_K = math.sqrt(2.0 / math.pi)
+
+
+def _sigmoid(w):
+    return 1.0 / (1.0 + np.exp(-np.clip(w, -700.0, 700.0)))
+
+
+def act(z, kind):
+    z = np.asarray(z, np.float64)
+    if kind == "relu":
+        return np.maximum(z, 0.0)
+    if kind == "gelu":
+        return 0.5 * z * _erfc(-z / math.sqrt(2.0))
+    if kind == "gelu_tanh":
+        return 0.5 * z * (1.0 + np.tanh(_K * (z + 0.044715 * z ** 3)))
+    if kind == "silu":
+        return z * _sigmoid(z)
+    assert kind == "none"
+    return z.copy()
+
+
+def act_grad(z, kind):
+    z = np.asarray(z, np.float64)
+    if kind == "relu":
+        return (z > 0).astype(np.float64)
+    if kind == "gelu":
+        return 0.5 * _erfc(-z / math.sqrt(2.0)) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    if kind == "gelu_tanh":
+        t = np.tanh(_K * (z + 0.044715 * z ** 3))
+        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * _K * (1.0 + 3 * 0.044715 * z * z)
+    if kind == "silu":
+        p = _sigmoid(z)
+        return p * (1.0 + z * (1.0 - p))
+    assert kind == "none"
+    return np.ones_like(z)
+
+
+def dfp8(x):
+    """(mantissas, exponent) of a tensor: max |x| = f 2^q, E = q - 6."""
+    x = np.asarray(x, np.float64)
+    top = float(np.max(np.abs(x))) if x.size else 0.0
+    e = math.frexp(top)[1] - 7 if top else 0
+    return np.clip(np.rint(np.ldexp(x, -e)), -128, 127).astype(np.int8), e
+
+
+def product(A, B):
+    """sum_k A[m][k] B[n][k], exact in int64."""
+    return A.astype(np.int64) @ B.astype(np.int64).T
+
+
+def linear_fwd(X, eX, W, eW, bias, kind, residual):
+    """(y, z) in float64."""
+    z = np.ldexp(product(X, W).astype(np.float64), eX + eW)
+    if bias is not None:
+        z = z + bias.astype(np.float64)
+    y = act(z, kind)
+    if residual is not None:
+        y = y + residual.astype(np.float64)
+    return y, z
+
+
+def layer_norm_fwd(x, gamma, beta, eps):
+    """(y, mean, rstd) in float64."""
+    x = np.asarray(x, np.float64)
+    mean = x.mean(1)
+    rstd = 1.0 / np.sqrt(np.square(x - mean[:, None]).mean(1) + eps)
+    y = (x - mean[:, None]) * rstd[:, None]
+    if gamma is not None:
+        y = y * gamma.astype(np.float64)
+    if beta is not None:
+        y = y + beta.astype(np.float64)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, gamma, dres):
+    """(dx, dgamma, dbeta) in float64."""
+    dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
+    rstd = np.asarray(rstd, np.float64)[:, None]
+    h = (x - np.asarray(mean, np.float64)[:, None]) * rstd
+    d = dy if gamma is None else dy * gamma.astype(np.float64)
+    dx = rstd * (d - d.mean(1, keepdims=True) - h * (d * h).mean(1, keepdims=True))
+    if dres is not None:
+        dx = dx + np.asarray(dres, np.float64)
+    return dx, (dy * h).sum(0), dy.sum(0)
+
+
+# ---- 8-bit optimiser states --------------------------------------------------
+
+def e4m3_table():
+    """The value of each E4M3 code (sign 1, exponent 4 with bias 7, mantissa 3; 0x7f and 0xff: NaN)."""
+    c = np.arange(256)
+    ex, m = (c >> 3) & 15, c & 7
+    v = np.where(ex == 0, m * 2.0 ** -9, (8 + m) * np.exp2(ex - 10.0))
+    v[(c & 0x7f) == 0x7f] = np.nan
+    return np.where(c & 0x80, -v, v)
+
+
+_TABLE = e4m3_table()
+
+
+def e4m3_encode(x):
+    """Codes of the nearest values, ties to the even code; not finite: NaN (0x7f).  |x| <= 448 or not finite."""
+    x = np.asarray(x, np.float64)
+    a = np.abs(np.where(np.isfinite(x), x, 0.0))
+    pos = _TABLE[:0x7f]
+    hi = np.searchsorted(pos, a).clip(0, 0x7e)
+    lo = np.maximum(hi - 1, 0)
+    d = (a - pos[lo]) - (pos[hi] - a)
+    c = np.where(d > 0, hi, np.where(d < 0, lo, np.where(lo % 2 == 0, lo, hi)))
+    c = np.where(np.isfinite(x), c | np.where(np.signbit(x), 0x80, 0), 0x7f)
+    return c.astype(np.uint8)
+
+
+def block_exponents(x):
+    """One exponent per block of 256 (float32 x): of the largest finite magnitude."""
+    n = x.size
+    a = np.zeros(-(-n // ADAMW_BLOCK) * ADAMW_BLOCK)
+    a[:n] = np.where(np.isfinite(x), np.abs(x.astype(np.float64)), 0.0)
+    top = a.reshape(-1, ADAMW_BLOCK).max(1)
+    f, q = np.frexp(top)  # f in [0.5, 1)
+    e = np.where(top > 0, np.maximum(q - 1 - 8 + (2 * f > 1.75), -126), 0)
+    return e.astype(np.int8)
+
+
+def state_encode(x, positive):
+    """(codes, exponents) of a float32 state; positive: a value above 0 keeps at least code 1."""
+    e = block_exponents(x)
+    c = e4m3_encode(np.ldexp(x.astype(np.float64), -e.astype(np.int64).repeat(ADAMW_BLOCK)[:x.size]))
+    if positive:
+        c = np.where((c == 0) & (x > 0), 1, c).astype(np.uint8)
+    return c, e
+
+
+def state_decode(c, e):
+    """float32 values (exact)."""
+    return np.ldexp(_TABLE[c], e.astype(np.int64).repeat(ADAMW_BLOCK)[:c.size]).astype(np.float32)
+
+
+def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.0, exps=None):
+    """(p, m, v[, exps]) after one step of one tensor.  v: the second moment
+    (float32), or with exps (int8 [blocks][2]) m and v are E4M3 codes of m
+    and of the root of the second moment."""
+    f = np.float32
+    b1, c1, b2, c2 = f(beta1), f(1.0 - beta1), f(beta2), f(1.0 - beta2)
+    rs2 = f(1.0 / math.sqrt(1.0 - beta2 ** t))
+    decay, size = f(1.0 - lr * weight_decay), f(lr / (1.0 - beta1 ** t))
+    with np.errstate(all="ignore"):
+        g = g.astype(f) * f(grad_scale)
+        if exps is not None:
+            m, r = state_decode(m, exps[:, 0]), state_decode(v, exps[:, 1])
+            v = r * r
+        m = b1 * m + c1 * g
+        v = b2 * v + (c2 * g) * g
+        r = np.sqrt(v)
+        u = m / (r * rs2 + f(eps))
+        p = p * decay - size * u
+    assert p.dtype == m.dtype == v.dtype == f
+    if exps is None:
+        return p, m, v
+    (cm, em), (cr, er) = state_encode(m, False), state_encode(r, True)
+    return p, cm, cr, np.stack([em, er], 1)
