@@ -8,7 +8,7 @@
 //   dZ = dY act'(Z) -> dZ8, edZ;  dX = fl(dZ8 W) 2^(edZ + eW),
 //   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
 #include "dfp8_convert.h"
-#include "dfp8_tile.h"
+#include "dfp8_tile256.h"
 
 namespace ionn {
 namespace {
@@ -26,8 +26,14 @@ template <bool A_KM, bool B_KM, bool LINEAR>
 void launch_product(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, const Epi &ep, int dtype, int M,
                     int N, int K, hipStream_t st) {
     const int64_t tiles = int64_t((M + 63) / 64) * ((N + 63) / 64);
+    const int64_t tiles256 = int64_t((M + 255) / 256) * ((N + 255) / 256);
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
+        if (tiles256 >= 64 && tile256_fits<A_KM, B_KM>(A, lda, B, ldb, M, N, K)) {
+            tile256_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles256)), dim3(g256::NT), 0, st>>>(
+                A, lda, B, ldb, uint32_t((A_KM ? M : K) * lda), uint32_t((B_KM ? N : K) * ldb), ep, M, N, K);
+            return;
+        }
         tile_kernel<T, 64, 64, A_KM, B_KM, LINEAR>
             <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
     });

@@ -236,7 +236,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(const int8_t *__restrict__ A, 
     // lane: row lane % 32, columns 8 q + 4 (lane / 32) .. + 3 of each block
     const int e2 = *ep.ea + *ep.eb;
     uint32_t top = 0;
-    with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) {
+    with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll

@@ -1,0 +1,250 @@
+// The large-product path of the DFP-8 Linear layer: 256 x 256 output tiles,
+// 128-deep K steps, loads straight into LDS, on the operand layouts, fragment
+// reads and issue order of gemm256.h, with a floating epilogue and with edges:
+// any M and N, any K of the K-major pair that is a multiple of 16 (row pitches
+// are, so that 16-byte pieces stay aligned), any K of the others.
+//
+// Edges cost no branch.  Rows past a K-major operand's end and k past an
+// M-major one's lie past its buffer resource and come back as zeros; what a
+// row's or column's end lets in of the next row feeds outputs that are not
+// stored.  Only where both operands are K-major does k past the end meet the
+// next row on both sides: there A's pieces past K are sent out of range.  An
+// address is a per-lane offset alone (no scalar offset): the hardware's range
+// check subtracts a scalar offset from the resource's size, which wraps when
+// a whole instruction lies past the end.
+#pragma once
+
+#include "dfp8_tile.h"
+
+namespace ionn {
+namespace dfp8 {
+
+constexpr uint32_t kOut = 0x80000000u;  // past every resource, whatever is added
+
+// The per-lane offsets of one operand (TileSrc holds the resource, the pitch
+// and the wavefront's and lanes' positions).
+template <bool KMAJOR>
+struct EdgeSrc : g256::TileSrc<KMAJOR> {
+    int col[2];  // K-major: the piece's first k within a step
+    __device__ __forceinline__ void init_edge(const int8_t *b, int ld, uint32_t bytes, int r0, int wave, int lane) {
+        this->init(b, ld, bytes, r0, wave, lane);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) col[p] = 16 * ((lane & 7) ^ g256::fK(8 * p + (lane >> 3)));
+    }
+    // lane offsets of a step whose first k is K - left (MASK: pieces past K out of range)
+    template <bool MASK>
+    __device__ __forceinline__ void offsets(int left, uint32_t (&v)[2]) const {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) v[p] = !MASK || col[p] < left ? this->lane_off[p] : kOut;
+    }
+    __device__ __forceinline__ void one(const uint32_t (&v)[2], int k0, int8_t *dst, int wave, int qq) const {
+        g256::dma16(this->rsrc, v[qq & 1] + this->soff_of(k0, qq), 0u, this->lds_of(dst, wave, qq));
+    }
+    __device__ __forceinline__ void two(const uint32_t (&v)[2], int k0, int8_t *dst, int wave, int qq) const {
+        g256::dma16x2(this->rsrc, v[0] + this->soff_of(k0, qq), 0u, v[1] + (this->soff_of(k0, qq + 1) - 1024u), 0u,
+                      this->lds_of(dst, wave, qq));
+    }
+};
+
+// Row m, columns n .. n + 7 through the epilogue; b: the columns' bias.
+template <class T, int ACT, bool LINEAR>
+__device__ __forceinline__ uint32_t finish8(const int32_t (&s)[8], const Epi &ep, int e2, const float (&b)[8],
+                                            int64_t m, int n, int M, int N) {
+    if (m >= M || n >= N) return 0u;
+    const int valid = N - n;
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __builtin_amdgcn_ldexpf(float(s[i]), e2);
+    const int64_t at = m * N + n;
+    T *y = static_cast<T *>(ep.y) + at;
+    if (LINEAR) {
+        store_vec<T, 8>(y, z, valid);
+        return 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += b[i];
+    if (ep.z) store_vec<T, 8>(static_cast<T *>(ep.z) + at, z, valid);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = act_value<ACT>(z[i]);
+    if (ep.residual) {
+        const auto r = load_raw<T, 8>(static_cast<const T *>(ep.residual) + at, valid);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += float(r[i]);
+    }
+    store_vec<T, 8>(y, o, valid);
+    uint32_t top = 0;
+    if (ep.absmax) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) top = max(top, mag_bits(o[i]));
+    }
+    return top;
+}
+
+template <class T, bool A_KM, bool B_KM, bool LINEAR>
+__global__ __launch_bounds__(g256::NT, 1) void tile256_kernel(const int8_t *__restrict__ A, int64_t lda,
+                                                              const int8_t *__restrict__ B, int64_t ldb,
+                                                              uint32_t a_bytes, uint32_t b_bytes, Epi ep, int M, int N,
+                                                              int K) {
+    using namespace g256;
+    __shared__ __attribute__((aligned(1024))) int8_t sA0[TILE_BYTES];
+    __shared__ __attribute__((aligned(1024))) int8_t sB0[TILE_BYTES];
+    __shared__ __attribute__((aligned(1024))) int8_t sA1[TILE_BYTES];
+    __shared__ __attribute__((aligned(1024))) int8_t sB1[TILE_BYTES];
+    constexpr bool MASK = A_KM && B_KM;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    int tm, tn;
+    gemm::tile_coords(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+
+    EdgeSrc<A_KM> ta;
+    EdgeSrc<B_KM> tb;
+    ta.init_edge(A, int(lda), a_bytes, m0, wave, lane);
+    tb.init_edge(B, int(ldb), b_bytes, n0, wave, lane);
+    FragSrc<A_KM> fa;
+    FragSrc<B_KM> fb;
+    fa.init(wm * 128, lane);
+    fb.init(wn * 128, lane);
+    const int e2 = *ep.ea + *ep.eb;
+
+    v16i acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = v16i{};
+    Frags<A_KM, B_KM> F[2];
+    const int nk = 2 * ((K + 2 * g256::BK - 1) / (2 * g256::BK));  // the two stages take turns: an even count
+
+    // va: A's lane offsets of the step being loaded
+    uint32_t va[2];
+    const uint32_t(&vb)[2] = tb.lane_off;
+    auto dma1 = [&](int q, int k0, int8_t *Ad, int8_t *Bd) __attribute__((always_inline)) {
+        if (q < 8) ta.one(va, k0, Ad, wave, q);
+        else tb.one(vb, k0, Bd, wave, q - 8);
+    };
+    auto dma2 = [&](int q, int k0, int8_t *Ad, int8_t *Bd) __attribute__((always_inline)) {
+        if (q < 8) ta.two(va, k0, Ad, wave, q);
+        else tb.two(vb, k0, Bd, wave, q - 8);
+    };
+    ta.template offsets<MASK>(K, va);
+#pragma unroll
+    for (int q = 0; q < 16; q += 2) dma2(q, 0, sA0, sB0);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    ta.template offsets<MASK>(K - g256::BK, va);
+    dma2(0, g256::BK, sA1, sB1);
+    dma2(2, g256::BK, sA1, sB1);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) F[0].read(RO[r], sA0, sB0, fa, fb, 0);
+
+    // One K step, in the issue order of gemm256_kernel: one memory
+    // instruction between consecutive MFMAs, the step's stage read while the
+    // other stage receives the next step, whose first four loads went out at
+    // the end of the step before.
+    auto step = [&](const int8_t *Ac, const int8_t *Bc, const int8_t *An, const int8_t *Bn, int8_t *Adst, int8_t *Bdst,
+                    int kt) __attribute__((always_inline)) {
+        int8_t *Anw = const_cast<int8_t *>(An), *Bnw = const_cast<int8_t *>(Bn);
+        const bool more1 = kt + 1 < nk, more2 = kt + 2 < nk;
+#pragma unroll
+        for (int sl = 0; sl < 3; ++sl) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = 4 * sl + g;
+                mfma_gt(F[sl & 1], g, 0, acc);
+                IONN_SCHED_FENCE();
+                F[(sl + 1) & 1].read(RO[2 * g], Ac, Bc, fa, fb, sl + 1);
+                IONN_SCHED_FENCE();
+                mfma_gt(F[sl & 1], g, 1, acc);
+                IONN_SCHED_FENCE();
+                if (c < 8 && more1) {
+                    if (c < 4) dma2(4 + 2 * c, (kt + 1) * g256::BK, Anw, Bnw);
+                    else dma1(12 + (c - 4), (kt + 1) * g256::BK, Anw, Bnw);
+                }
+                IONN_SCHED_FENCE();
+                mfma_gt(F[sl & 1], g, 2, acc);
+                IONN_SCHED_FENCE();
+                F[(sl + 1) & 1].read(RO[2 * g + 1], Ac, Bc, fa, fb, sl + 1);
+                IONN_SCHED_FENCE();
+                mfma_gt(F[sl & 1], g, 3, acc);
+                IONN_SCHED_FENCE();
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mfma_gt(F[1], t >> 2, t & 3, acc);
+        IONN_SCHED_FENCE();
+        ta.template offsets<MASK>(K - (kt + 2) * g256::BK, va);
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        IONN_SCHED_FENCE();
+#pragma unroll
+        for (int g = 2; g < 4; ++g) {
+            if (more2) dma2(2 * (g - 2), (kt + 2) * g256::BK, Adst, Bdst);
+            IONN_SCHED_FENCE();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                mfma_gt(F[1], g, t, acc);
+                IONN_SCHED_FENCE();
+                F[0].read(RO[4 * (g - 2) + t], An, Bn, fa, fb, 0);
+                IONN_SCHED_FENCE();
+            }
+        }
+    };
+    for (int kt = 0; kt < nk; kt += 2) {
+        step(sA0, sB0, sA1, sB1, sA0, sB0, kt);
+        step(sA1, sB1, sA0, sB0, sA1, sB1, kt + 1);
+    }
+
+    // Epilogue: block (i, j) leaves row lane % 32, columns 8 q + 4 (lane / 32)
+    // .. + 3.  Swapping the upper half of q with the lower half of q + 1
+    // gives every lane eight consecutive columns, one 16-byte store of a
+    // 16-bit type, 32 bytes of a row per instruction.
+    const int half = lane >> 5;
+    uint32_t top = 0;
+    with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int qp = 0; qp < 2; ++qp) {
+                const int n = n0 + wn * 128 + 32 * j + 16 * qp + 8 * half;
+                float b[8] = {};
+                if (!LINEAR && ep.bias) {
+                    const auto raw = load_raw<float, 8>(ep.bias + n, N - n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) b[i] = raw[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int32_t s[8];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const v2u w = __builtin_amdgcn_permlane32_swap(uint32_t(acc[i][j][8 * qp + c]),
+                                                                       uint32_t(acc[i][j][8 * qp + 4 + c]), false, false);
+                        s[c] = int32_t(w.x);
+                        s[4 + c] = int32_t(w.y);
+                    }
+                    top = max(top, finish8<T, decltype(ac)::value, LINEAR>(
+                                       s, ep, e2, b, int64_t(m0) + wm * 128 + i * 32 + (lane & 31), n, M, N));
+                }
+            }
+    });
+    if (!LINEAR && ep.absmax) {
+        top = wave_max_u32(top);
+        if (lane == 0) publish_max_u32(ep.absmax, top);
+    }
+}
+
+// Whether tile256_kernel takes the product: 16-byte pieces that stay aligned,
+// and offsets that stay below 2^32 past a ragged tile's end.
+template <bool A_KM, bool B_KM>
+inline bool tile256_fits(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, int64_t M, int64_t N, int64_t K) {
+    const int64_t ab = (A_KM ? M : K) * lda, bb = (B_KM ? N : K) * ldb, lim = int64_t(1) << 31;
+    return K >= 1 && aligned(A, 16) && aligned(B, 16) && lda % 16 == 0 && ldb % 16 == 0 && ab < lim && bb < lim &&
+           512 * lda < lim && 512 * ldb < lim && lda >= 256 && ldb >= 256;
+}
+
+}  // namespace dfp8
+}  // namespace ionn

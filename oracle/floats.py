@@ -59,8 +59,9 @@ def dfp8(x):
 
 
 def product(A, B):
-    """sum_k A[m][k] B[n][k], exact in int64."""
-    return A.astype(np.int64) @ B.astype(np.int64).T
+    """sum_k A[m][k] B[n][k], exact (every partial sum is below 2^53)."""
+    assert A.shape[1] * 2 ** 14 < 2 ** 53
+    return (A.astype(np.float64) @ B.astype(np.float64).T).astype(np.int64)
 
 
 def linear_fwd(X, eX, W, eW, bias, kind, residual):

@@ -108,7 +108,9 @@ def test_forward(B, IN, OUT, name):
 # whole tiles of 256, their edges, few rows against many columns, few tiles over a long reduction
 @pytest.mark.parametrize("B,IN,OUT", [(512, 512, 768), (256, 4096, 256), (1000, 1023, 1025), (513, 1280, 769),
                                       (1024, 272, 1040), (2, 4096, 4096), (8, 1000, 2049), (33, 2048, 1024),
-                                      (64, 8192, 64), (5, 20000, 40), (4096, 64, 96)])
+                                      (64, 8192, 64), (5, 20000, 40), (4096, 64, 96),
+                                      # many whole and cut tiles of 256, reductions that end inside a step
+                                      (2048, 512, 2304), (2100, 272, 2064), (2060, 400, 2321), (2049, 1168, 2050)])
 @pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "gelu"), ("f16", "silu")])
 def test_forward_larger(B, IN, OUT, name, kind):
     _check_forward(_case(B, IN, OUT, name, bias=name != "f16", residual=name != "f32"), kind, name)
@@ -229,7 +231,8 @@ def test_backward(B, IN, OUT, name):
 
 @pytest.mark.parametrize("B,IN,OUT", [(512, 768, 512), (256, 256, 256), (1000, 1023, 513), (513, 1281, 769),
                                       (1040, 272, 1024), (4000, 70, 130), (8192, 64, 48), (2, 2048, 4096),
-                                      (64, 512, 8192), (768, 512, 1536)])
+                                      (64, 512, 8192), (768, 512, 1536), (2048, 2304, 2048), (2060, 2064, 2320),
+                                      (2051, 2320, 2080), (2305, 2048, 272)])
 @pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "gelu"), ("f16", "silu")])
 def test_backward_larger(B, IN, OUT, name, kind):
     _check_backward(_backward(B, IN, OUT, kind, name), kind, name)
