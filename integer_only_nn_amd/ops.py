@@ -541,6 +541,31 @@ def _dtype(t, name):
     return _FLOATS[t.dtype]
 
 
+# The calls below serve single tokens too, where the host's share of a call
+# counts: a tensor that is in order costs _a three attribute reads (_p, with a
+# message for what is not, the rest), and the current stream is read without
+# building a Stream object (0.1 against 1 us).
+
+def _a(t, dtype=None, numel=0, name="tensor"):
+    """Address of a contiguous device tensor (None -> NULL)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype == dtype) and t.is_contiguous() and \
+            (numel == 0 or t.numel() >= numel):
+        return t.data_ptr()
+    return _p(t, dtype, numel, name).value
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, t):
+    """The stream's handle: by default the current one of t's device."""
+    if stream is None and _raw_stream is not None and t.is_cuda:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _act(act):
     """The library's number of an activation, given by number or name."""
     return ACTIVATIONS[act] if isinstance(act, str) else int(act)
@@ -551,15 +576,22 @@ def _same(cond, what):
         raise ValueError(f"shape mismatch: {what}")
 
 
+def _space(workspace):
+    """Address and bytes of a workspace (None: NULL and 0)."""
+    if workspace is None:
+        return None, 0
+    return _a(workspace, name="workspace"), workspace.numel() * workspace.element_size()
+
+
 def dfp8_from_float_workspace_bytes():
     return int(lib().dfp8_from_float_workspace_bytes())
 
 
 def dfp8_from_float(x, out, e_out, absmax=None, workspace=None, status_out=None, stream=None):
     _same(x.numel() == out.numel(), "x and out")
-    check(lib().dfp8_from_float(_p(x, name="x"), _dtype(x, "x"), x.numel(), _p(absmax, u32, 1, "absmax"),
-                                _p(out, i8, name="out"), _p(e_out, i32, 1, "e_out"),
-                                _p(status_out, i32, 1, "status_out"), *_ws(workspace), _stream(stream)),
+    check(lib().dfp8_from_float(_a(x, name="x"), _dtype(x, "x"), x.numel(), _a(absmax, u32, 1, "absmax"),
+                                _a(out, i8, name="out"), _a(e_out, i32, 1, "e_out"),
+                                _a(status_out, i32, 1, "status_out"), *_space(workspace), _on(stream, x)),
           "dfp8_from_float")
 
 
@@ -575,10 +607,10 @@ def dfp8_linear_fwd(X, eX, W, eW, Y, bias=None, act=0, residual=None, Z=None, ab
     _same(W.shape == (OUT, IN) and Y.shape == (B, OUT), "X, W and Y")
     _same((residual is None or residual.shape == (B, OUT)) and (Z is None or Z.shape == (B, OUT)) and
           (bias is None or bias.numel() == OUT), "bias, residual and Z")
-    check(lib().dfp8_linear_fwd(_p(X, i8, name="X"), _p(eX, i32, 1, "eX"), _p(W, i8, name="W"), _p(eW, i32, 1, "eW"),
-                                _p(bias, f32, name="bias"), _act(act), _p(residual, dt, name="residual"),
-                                _p(Z, dt, name="Z"), _p(Y, name="Y"), _dtype(Y, "Y"), B, IN, OUT,
-                                _p(absmax_Y, u32, 1, "absmax_Y"), *_ws(workspace), _stream(stream)),
+    check(lib().dfp8_linear_fwd(_a(X, i8, name="X"), _a(eX, i32, 1, "eX"), _a(W, i8, name="W"), _a(eW, i32, 1, "eW"),
+                                _a(bias, f32, name="bias"), _act(act), _a(residual, dt, name="residual"),
+                                _a(Z, dt, name="Z"), _a(Y, name="Y"), _dtype(Y, "Y"), B, IN, OUT,
+                                _a(absmax_Y, u32, 1, "absmax_Y"), *_space(workspace), _on(stream, Y)),
           "dfp8_linear_fwd")
 
 
@@ -596,11 +628,11 @@ def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None
     _same((X is None or X.shape == (B, IN)) and (W is None or W.shape == (OUT, IN)), "X and W")
     _same((dX is None or dX.shape == (B, IN)) and (G is None or G.shape == (OUT, IN)) and
           (gb is None or gb.numel() == OUT), "dX, G and gb")
-    check(lib().dfp8_linear_bwd(_p(dY, name="dY"), _p(Z, dt, name="Z"), _act(act), _dtype(dY, "dY"),
-                                _p(X, i8, name="X"), _p(eX, i32, 1, "eX"), _p(W, i8, name="W"), _p(eW, i32, 1, "eW"),
-                                _p(dZ8, i8, name="dZ8"), _p(edZ, i32, 1, "edZ"), _p(dX, dt, name="dX"),
-                                _p(G, dt, name="G"), _p(gb, f32, name="gb"), B, IN, OUT,
-                                _p(status_out, i32, 1, "status_out"), *_ws(workspace), _stream(stream)),
+    check(lib().dfp8_linear_bwd(_a(dY, name="dY"), _a(Z, dt, name="Z"), _act(act), _dtype(dY, "dY"),
+                                _a(X, i8, name="X"), _a(eX, i32, 1, "eX"), _a(W, i8, name="W"), _a(eW, i32, 1, "eW"),
+                                _a(dZ8, i8, name="dZ8"), _a(edZ, i32, 1, "edZ"), _a(dX, dt, name="dX"),
+                                _a(G, dt, name="G"), _a(gb, f32, name="gb"), B, IN, OUT,
+                                _a(status_out, i32, 1, "status_out"), *_space(workspace), _on(stream, dY)),
           "dfp8_linear_bwd")
 
 
@@ -609,10 +641,10 @@ def ionn_layer_norm_fwd(x, y, gamma=None, beta=None, eps=1e-5, mean=None, rstd=N
     _same(y.shape == (rows, cols) and (gamma is None or gamma.numel() == cols) and
           (beta is None or beta.numel() == cols), "x, y, gamma and beta")
     _same((mean is None or mean.numel() == rows) and (rstd is None or rstd.numel() == rows), "mean and rstd")
-    check(lib().ionn_layer_norm_fwd(_p(x, name="x"), _p(gamma, f32, name="gamma"), _p(beta, f32, name="beta"),
-                                    float(eps), _p(y, x.dtype, name="y"), _p(mean, f32, name="mean"),
-                                    _p(rstd, f32, name="rstd"), _dtype(x, "x"), rows, cols,
-                                    _p(absmax_y, u32, 1, "absmax_y"), _stream(stream)), "ionn_layer_norm_fwd")
+    check(lib().ionn_layer_norm_fwd(_a(x, name="x"), _a(gamma, f32, name="gamma"), _a(beta, f32, name="beta"),
+                                    float(eps), _a(y, x.dtype, name="y"), _a(mean, f32, name="mean"),
+                                    _a(rstd, f32, name="rstd"), _dtype(x, "x"), rows, cols,
+                                    _a(absmax_y, u32, 1, "absmax_y"), _on(stream, x)), "ionn_layer_norm_fwd")
 
 
 def ionn_layer_norm_bwd_workspace_bytes(rows, cols):
@@ -626,10 +658,10 @@ def ionn_layer_norm_bwd(dy, x, mean, rstd, dx, gamma=None, dres=None, dgamma=Non
     _same(dy.shape == x.shape and dx.shape == x.shape and (dres is None or dres.shape == x.shape), "dy, x, dx and dres")
     _same(mean.numel() == rows and rstd.numel() == rows, "mean and rstd")
     _same(all(t is None or t.numel() == cols for t in (gamma, dgamma, dbeta)), "gamma, dgamma and dbeta")
-    check(lib().ionn_layer_norm_bwd(_p(dy, dt, name="dy"), _p(x, name="x"), _p(mean, f32, name="mean"),
-                                    _p(rstd, f32, name="rstd"), _p(gamma, f32, name="gamma"), _p(dres, dt, name="dres"),
-                                    _p(dx, dt, name="dx"), _p(dgamma, f32, name="dgamma"), _p(dbeta, f32, name="dbeta"),
-                                    _dtype(x, "x"), rows, cols, *_ws(workspace), _stream(stream)),
+    check(lib().ionn_layer_norm_bwd(_a(dy, dt, name="dy"), _a(x, name="x"), _a(mean, f32, name="mean"),
+                                    _a(rstd, f32, name="rstd"), _a(gamma, f32, name="gamma"), _a(dres, dt, name="dres"),
+                                    _a(dx, dt, name="dx"), _a(dgamma, f32, name="dgamma"), _a(dbeta, f32, name="dbeta"),
+                                    _dtype(x, "x"), rows, cols, *_space(workspace), _on(stream, x)),
           "ionn_layer_norm_bwd")
 
 
@@ -655,6 +687,6 @@ def ionn_adamw_step(Ps, Gs, Ms, Vs, t, lr, beta1=0.9, beta2=0.999, eps=1e-8, wei
     check(lib().ionn_adamw_step(L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
                                 _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"),
                                 None if Ss is None else _ptr_array(Ss, i8, "S"), bits, _sizes(Ps), int(t), float(lr),
-                                float(beta1), float(beta2), float(eps), float(weight_decay), _p(step, i32, 1, "step"),
-                                _p(lr_dev, f32, 1, "lr_dev"), _p(grad_scale, f32, 1, "grad_scale"),
-                                _p(absmax_P, u32, L, "absmax_P"), _stream(stream)), "ionn_adamw_step")
+                                float(beta1), float(beta2), float(eps), float(weight_decay), _a(step, i32, 1, "step"),
+                                _a(lr_dev, f32, 1, "lr_dev"), _a(grad_scale, f32, 1, "grad_scale"),
+                                _a(absmax_P, u32, L, "absmax_P"), _on(stream, Ps[0])), "ionn_adamw_step")

@@ -512,5 +512,5 @@ class AdamW:
         ops.check(ops.lib().ionn_adamw_step(
             len(self.P), self._Pp, self._G[1], self._G[2], self._Mp, self._Vp, self._Sp, self._bits, self._n, self.t,
             float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps), float(self.weight_decay),
-            ops._p(self.step_dev), ops._p(self.lr_dev), ops._p(grad_scale, torch.float32, 1, "grad_scale"),
-            ops._p(absmax_P, torch.int32, len(self.P), "absmax_P"), ops._stream(stream)), "ionn_adamw_step")
+            ops._a(self.step_dev), ops._a(self.lr_dev), ops._a(grad_scale, torch.float32, 1, "grad_scale"),
+            ops._a(absmax_P, torch.int32, len(self.P), "absmax_P"), ops._on(stream, self.P[0])), "ionn_adamw_step")
