@@ -8,6 +8,7 @@
 //   dZ = dY act'(Z) -> dZ8, edZ;  dX = fl(dZ8 W) 2^(edZ + eW),
 //   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
 #include "dfp8_convert.h"
+#include "dfp8_rows.h"
 #include "dfp8_tile256.h"
 
 namespace ionn {
@@ -29,6 +30,15 @@ void launch_product(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, 
     const int64_t tiles256 = int64_t((M + 255) / 256) * ((N + 255) / 256);
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
+        if constexpr (!LINEAR) {
+            if (M <= kRowsMax && K >= kRowsMinK) {
+                const dim3 grid(unsigned((N + 15) / 16)), block(kRowWaves * 64);
+                if (M <= 16) rows_kernel<T, 1><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
+                else if (M <= 32) rows_kernel<T, 2><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
+                else rows_kernel<T, 4><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
+                return;
+            }
+        }
         if (tiles256 >= 64 && tile256_fits<A_KM, B_KM>(A, lda, B, ldb, M, N, K)) {
             tile256_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles256)), dim3(g256::NT), 0, st>>>(
                 A, lda, B, ldb, uint32_t((A_KM ? M : K) * lda), uint32_t((B_KM ? N : K) * ldb), ep, M, N, K);
