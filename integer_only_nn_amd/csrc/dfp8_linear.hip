@@ -44,8 +44,13 @@ void launch_product(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, 
                 A, lda, B, ldb, uint32_t((A_KM ? M : K) * lda), uint32_t((B_KM ? N : K) * ldb), ep, M, N, K);
             return;
         }
-        tile_kernel<T, 64, 64, A_KM, B_KM, LINEAR>
-            <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
+        const int a_side = A_KM ? K : M, b_side = B_KM ? K : N;  // contiguous
+        if (a_side < 16 || b_side < 16)
+            tile_kernel<T, 64, 64, 2, A_KM, B_KM, LINEAR, true>
+                <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
+        else
+            tile_kernel<T, 64, 64, 4, A_KM, B_KM, LINEAR, false>
+                <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
     });
 }
 

@@ -9,11 +9,14 @@
 //   wgrad A = dZ8 [B][OUT], B = X [B][IN]     (both M-major)
 //
 // A workgroup of four wavefronts (2 x 2) takes a BM x BN tile in 128-deep K
-// steps, double-buffered in LDS; the next step's 16-byte pieces are loaded
-// into registers while the current step is contracted.  Pieces are loaded at
-// whatever byte they start on, and a piece that a row's (or the tensor's) end
-// cuts is loaded so that it ends there and shifted down, so odd sizes cost a
-// shift in the last piece and no byte-wise path.
+// steps, double-buffered in LDS.  A step's arithmetic is far shorter than a
+// trip to memory, so DEPTH steps of 16-byte pieces are in flight in registers.
+// Their loads are unconditional (a lane-dependent branch around a load makes
+// the compiler wait for everything in flight) and in bounds: a piece that a
+// row's or the tensor's end cuts is loaded so that it ends there and shifted
+// down on its way to LDS, a row or k past the end repeats the last one, and
+// A's values past K become 0.  Pieces start at whatever byte they start on,
+// so odd sizes cost a shift in the last piece and no byte-wise path.
 //
 // LDS layouts, without bank conflicts in either direction:
 //   K-major [rows][128 B]: 16-byte piece c of row r at position c ^ fK(r & 15)
@@ -75,31 +78,69 @@ __device__ __forceinline__ v4i load_piece(const int8_t *base, int64_t off, int v
     return v;
 }
 
+// v shifted down by sh bytes (zeros from above), sh >= 0.
+__device__ __forceinline__ v4i shift_piece(const v4i &v, int sh) {
+    uint32_t w[5] = {uint32_t(v.x), uint32_t(v.y), uint32_t(v.z), uint32_t(v.w), 0u};
+    if (sh & 8) {
+        w[0] = w[2];
+        w[1] = w[3];
+        w[2] = w[3] = 0u;
+    }
+    if (sh & 4) {
+        w[0] = w[1];
+        w[1] = w[2];
+        w[2] = w[3];
+        w[3] = 0u;
+    }
+    v4i o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = sh >= 16 ? 0 : int(__builtin_amdgcn_alignbyte(w[i + 1], w[i], uint32_t(sh & 3)));
+    return o;
+}
+
 template <int R>
 __device__ __forceinline__ int fT(int k) {
     return R == 128 ? 2 * ((k >> 1) & 3) : 2 * ((k >> 2) & 1);
 }
 
-// One operand's tile of R rows: pieces to registers, then to LDS.
-template <int R, bool KMAJOR>
+// One operand's tile of R rows: a step's pieces to registers, then to LDS.
+// TINY: the contiguous side is shorter than a piece.
+template <int R, bool KMAJOR, bool TINY>
 struct Stage {
     static constexpr int kPer = R * BK / 16 / NT;
     static_assert(R * BK / 16 % NT == 0, "whole pieces per thread");
     v4i reg[kPer];
     __device__ __forceinline__ void load(const int8_t *base, int64_t ld, int rows, int kdim, int r0, int k0) {
+        typedef v4i loose __attribute__((aligned(1)));
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int id = j * NT + int(threadIdx.x);
-            if (KMAJOR) {
-                const int r = r0 + id / (BK / 16), k = k0 + 16 * (id % (BK / 16));
+            const int r = r0 + (KMAJOR ? id / (BK / 16) : 16 * (id % (R / 16)));
+            const int k = k0 + (KMAJOR ? 16 * (id % (BK / 16)) : id / (R / 16));
+            if (TINY && KMAJOR)
                 reg[j] = load_piece(base, r * ld + k, r < rows ? kdim - k : 0);
-            } else {
-                const int k = k0 + id / (R / 16), r = r0 + 16 * (id % (R / 16));
+            else if (TINY)
                 reg[j] = load_piece(base, k * ld + r, k < kdim ? rows - r : 0);
-            }
+            else if (KMAJOR)
+                reg[j] = *reinterpret_cast<const loose *>(base + min(r, rows - 1) * ld + min(k, kdim - 16));
+            else
+                reg[j] = *reinterpret_cast<const loose *>(base + min(k, kdim - 1) * ld + min(r, rows - 16));
         }
     }
-    __device__ __forceinline__ void store(int8_t *lds) const {
+    // r0, k0: of the step in the registers
+    __device__ __forceinline__ void store(int8_t *lds, int rows, int kdim, int r0, int k0) {
+        if (!TINY && (k0 + BK > kdim || (!KMAJOR && r0 + R > rows))) {  // a step or a tile that an end cuts
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int id = j * NT + int(threadIdx.x);
+                if (KMAJOR) {
+                    reg[j] = shift_piece(reg[j], max(0, k0 + 16 * (id % (BK / 16)) - (kdim - 16)));
+                } else {
+                    const bool past = k0 + id / (R / 16) >= kdim;
+                    reg[j] = shift_piece(reg[j], past ? 16 : max(0, r0 + 16 * (id % (R / 16)) - (rows - 16)));
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int id = j * NT + int(threadIdx.x);
@@ -179,12 +220,70 @@ __device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2,
     return top;
 }
 
-template <class T, int BM, int BN, bool A_KM, bool B_KM, bool LINEAR>
+// The sums of one tile over k in [k_begin, k_end) (k_begin and, but for the
+// last range, k_end multiples of BK).  lds: 2 stages of (BM + BN) * BK bytes.
+template <int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool TINY>
+__device__ __forceinline__ void tile_sums(const int8_t *__restrict__ A, int64_t lda, const int8_t *__restrict__ B,
+                                          int64_t ldb, int M, int N, int m0, int n0, int k_begin, int k_end, int8_t *lds,
+                                          int wm, int wn, int lane, v16i (&acc)[BM / 64][BN / 64]) {
+    constexpr int FM = BM / 64, FN = BN / 64;  // 32 x 32 blocks of a wavefront
+    constexpr int kStage = (BM + BN) * BK;
+    static_assert(DEPTH % 2 == 0, "two LDS stages: DEPTH steps unrolled keep every index static");
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = v16i{};
+    const int nk = (k_end - k_begin + BK - 1) / BK;
+    if (nk <= 0) return;
+    Stage<BM, A_KM, TINY> sa[DEPTH];
+    Stage<BN, B_KM, TINY> sb[DEPTH];
+    auto load = [&](int s, int kt) __attribute__((always_inline)) {
+        sa[s].load(A, lda, M, k_end, m0, k_begin + kt * BK);
+        sb[s].load(B, ldb, N, k_end, n0, k_begin + kt * BK);
+    };
+    auto store = [&](int s, int kt, int8_t *to) __attribute__((always_inline)) {
+        sa[s].store(to, M, k_end, m0, k_begin + kt * BK);
+        sb[s].store(to + BM * BK, N, k_end, n0, k_begin + kt * BK);
+    };
+    // (a load past the last step would repeat its pieces: skipped, for all lanes)
+#pragma unroll
+    for (int s = 0; s < DEPTH; ++s)
+        if (s < nk) load(s, s);
+    store(0, 0, lds);
+    if (DEPTH < nk) load(0, DEPTH);
+    __syncthreads();
+    for (int k4 = 0; k4 < nk; k4 += DEPTH) {
+#pragma unroll
+        for (int s = 0; s < DEPTH; ++s) {
+            const int kt = k4 + s;
+            if (kt >= nk) break;
+            const int8_t *As = lds + (s & 1) * kStage, *Bs = As + BM * BK;
+#pragma unroll
+            for (int sl = 0; sl < BK / 32; ++sl) {
+                v4i a[FM], b[FN];
+#pragma unroll
+                for (int i = 0; i < FM; ++i) a[i] = read_frag<BM, A_KM>(As, wm + 32 * i, sl, lane);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) b[j] = read_frag<BN, B_KM>(Bs, wn + 32 * j, sl, lane);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+            }
+            if (kt + 1 < nk) store((s + 1) % DEPTH, kt + 1, lds + ((s + 1) & 1) * kStage);
+            if (kt + 1 + DEPTH < nk) load((s + 1) % DEPTH, kt + 1 + DEPTH);
+            __syncthreads();
+        }
+    }
+}
+
+template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
 __global__ __launch_bounds__(NT) void tile_kernel(const int8_t *__restrict__ A, int64_t lda,
                                                   const int8_t *__restrict__ B, int64_t ldb, Epi ep, int M, int N,
                                                   int K) {
-    constexpr int FM = BM / 64, FN = BN / 64;  // 32 x 32 blocks of a wavefront
-    __shared__ __attribute__((aligned(256))) int8_t lds[2][(BM + BN) * BK];
+    constexpr int FM = BM / 64, FN = BN / 64;
+    __shared__ __attribute__((aligned(256))) int8_t lds[2 * (BM + BN) * BK];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
@@ -192,47 +291,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(const int8_t *__restrict__ A, 
     gemm::tile_coords(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     v16i acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = v16i{};
-    Stage<BM, A_KM> sa;
-    Stage<BN, B_KM> sb;
-    const int nk = (K + BK - 1) / BK;
-    if (nk > 0) {
-        sa.load(A, lda, M, K, m0, 0);
-        sb.load(B, ldb, N, K, n0, 0);
-        sa.store(lds[0]);
-        sb.store(lds[0] + BM * BK);
-    }
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        const int8_t *As = lds[kt & 1], *Bs = As + BM * BK;
-        const bool more = kt + 1 < nk;
-        if (more) {
-            sa.load(A, lda, M, K, m0, (kt + 1) * BK);
-            sb.load(B, ldb, N, K, n0, (kt + 1) * BK);
-        }
-#pragma unroll
-        for (int sl = 0; sl < BK / 32; ++sl) {
-            v4i a[FM], b[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) a[i] = read_frag<BM, A_KM>(As, wm + 32 * i, sl, lane);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) b[j] = read_frag<BN, B_KM>(Bs, wn + 32 * j, sl, lane);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
-        }
-        if (more) {
-            int8_t *nx = lds[(kt + 1) & 1];
-            sa.store(nx);
-            sb.store(nx + BM * BK);
-        }
-        __syncthreads();
-    }
+    tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(A, lda, B, ldb, M, N, m0, n0, 0, K, lds, wm, wn, lane, acc);
     // lane: row lane % 32, columns 8 q + 4 (lane / 32) .. + 3 of each block
     const int e2 = *ep.ea + *ep.eb;
     uint32_t top = 0;
