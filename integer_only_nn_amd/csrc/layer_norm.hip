@@ -48,21 +48,43 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void norm_fwd_kern
     uint32_t *absmax) {
     __shared__ float buf[2][TPR / 64 + 1];
     constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;  // rows a workgroup takes at once
+    constexpr bool kHold = NV * VE <= 16;                       // gamma and beta stay in registers
     const int t = threadIdx.x % TPR;
+    const int64_t step = int64_t(gridDim.x) * kRows;
+    int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
     int ph = 0;
     uint32_t top = 0;
-    for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR; r < rows; r += int64_t(gridDim.x) * kRows) {
-        const T *xr = x + r * cols;
-        float v[NV][VE];
-        float s = 0.0f;
+    // the next row's loads go out before this row's sums are taken
+    typename Vec<T, VE>::type raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VE;
+        raw[i] = load_raw<T, VE>(x + r * cols + c, r < rows ? cols - c : 0);
+    }
+    typename Vec<float, VE>::type gh[kHold ? NV : 1], bh[kHold ? NV : 1];
+    if (kHold) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VE;
-            const auto raw = load_raw<T, VE>(xr + c, cols - c);
+            gh[i] = gamma ? load_raw<float, VE>(gamma + c, cols - c) : typename Vec<float, VE>::type(1.0f);
+            bh[i] = load_raw<float, VE>(beta + c, beta ? cols - c : 0);
+        }
+    }
+    for (; r < rows; r += step) {
+        float v[NV][VE];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                v[i][e] = float(raw[e]);
+                v[i][e] = float(raw[i][e]);
                 s += v[i][e];
+            }
+        if (r + step < rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * VE;
+                raw[i] = load_raw<T, VE>(x + (r + step) * cols + c, cols - c);
             }
         }
         const float mean = row_sum<TPR>(s, buf, ph) / n_cols;
@@ -85,19 +107,17 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void norm_fwd_kern
             const int c = (i * TPR + t) * VE;
             const int valid = cols - c;
             if (valid <= 0) continue;
+            typename Vec<float, VE>::type g, b;
+            if (kHold) {
+                g = gh[i];
+                b = bh[i];
+            } else {
+                g = gamma ? load_raw<float, VE>(gamma + c, valid) : typename Vec<float, VE>::type(1.0f);
+                b = load_raw<float, VE>(beta + c, beta ? valid : 0);
+            }
             float o[VE];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) o[e] = v[i][e] * rstd;
-            if (gamma) {
-                const auto g = load_raw<float, VE>(gamma + c, valid);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o[e] *= g[e];
-            }
-            if (beta) {
-                const auto b = load_raw<float, VE>(beta + c, valid);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o[e] += b[e];
-            }
+            for (int e = 0; e < VE; ++e) o[e] = v[i][e] * rstd * g[e] + b[e];
             if (absmax) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
@@ -188,20 +208,33 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void norm_bwd_kern
             sg[i][e] = sb[i][e] = 0.0f;
         }
     }
-    for (int64_t r = int64_t(blockIdx.x) * kRows + rg; r < rows; r += int64_t(gridDim.x) * kRows) {
-        const float mu = mean[r], rs = rstd[r];
+    // the next row's loads go out before this row's sums are taken
+    const int64_t step = int64_t(gridDim.x) * kRows;
+    int64_t r = int64_t(blockIdx.x) * kRows + rg;
+    typename Vec<T, VE>::type rx[NV], ry[NV];
+    float mu_next = 0.0f, rs_next = 0.0f;
+    auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+        mu_next = mean[row];
+        rs_next = rstd[row];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE;
+            rx[i] = load_raw<T, VE>(x + row * cols + c, cols - c);
+            ry[i] = load_raw<T, VE>(dy + row * cols + c, cols - c);
+        }
+    };
+    if (r < rows) load_row(r);
+    for (; r < rows; r += step) {
+        const float mu = mu_next, rs = rs_next;
         float h[NV][VE], d[NV][VE];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VE;
-            const auto rx = load_raw<T, VE>(x + r * cols + c, cols - c);
-            const auto ry = load_raw<T, VE>(dy + r * cols + c, cols - c);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 // (past the row's end dy is 0, and so is every sum's term)
-                h[i][e] = (float(rx[e]) - mu) * rs;
-                const float a = float(ry[e]);
+                h[i][e] = (float(rx[i][e]) - mu) * rs;
+                const float a = float(ry[i][e]);
                 sg[i][e] += a * h[i][e];
                 sb[i][e] += a;
                 d[i][e] = a * g[i][e];
@@ -209,6 +242,7 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void norm_bwd_kern
                 s2 += d[i][e] * h[i][e];
             }
         }
+        if (r + step < rows) load_row(r + step);
         const float c1 = row_sum<TPR>(s1, buf, ph) / n_cols;
         const float c2 = row_sum<TPR>(s2, buf, ph) / n_cols;
 #pragma unroll
