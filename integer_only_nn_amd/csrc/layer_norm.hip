@@ -187,13 +187,17 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(const T *x, const f
     }
 }
 
+// Threads of a workgroup of the backward pass: short rows, one wavefront
+// each, go eight to a workgroup, so that few partial rows leave it.
+constexpr int bwd_threads(int tpr) { return tpr == 64 ? 512 : tpr; }
+
 // part: [gridDim.x][2][cols], the workgroups' sums of dy h and dy (NULL: not asked for).
 template <class T, int VE, int TPR, int NV>
-__global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void norm_bwd_kernel(
+__global__ __launch_bounds__(bwd_threads(TPR)) void norm_bwd_kernel(
     const T *dy, const T *__restrict__ x, const float *__restrict__ mean, const float *__restrict__ rstd,
     const float *__restrict__ gamma, const T *dres, T *dx, float *__restrict__ part, int64_t rows, int cols,
     float n_cols) {
-    constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;
+    constexpr int kRows = bwd_threads(TPR) / TPR;
     __shared__ float buf[2][TPR / 64 + 1];
     __shared__ float fold[kRows > 1 ? kRows * NV * VE * TPR : 1];
     const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
@@ -373,7 +377,7 @@ __global__ __launch_bounds__(64 * kSumGroups) void norm_sum_kernel(const float *
     const int64_t c = int64_t(blockIdx.x) * 64 + lane;
     float s = 0.0f;
     if (c < 2 * cols) {
-#pragma unroll 8
+#pragma unroll 16
         for (int p = grp; p < nparts; p += kSumGroups) s += part[int64_t(p) * 2 * cols + c];
     }
     red[grp][lane] = s;
@@ -406,10 +410,16 @@ bool with_shape(int64_t cols, F &&f) {
     return false;
 }
 
-// Workgroups of the backward pass (and partial rows): at most kMaxParts.
-int64_t bwd_groups(int64_t rows, int rows_per_group) {
+// Workgroups of the backward pass, and partial rows: two of 256 threads per
+// compute unit or one of more.  More keep more loads in flight, but leave more
+// partial rows and deal the rows out less evenly: at 8192 x 4096 (bf16) two
+// per unit took 44 us, one 53, three 50 and four 53; at 8192 x 1024 one of
+// 512 threads took as long as two of 256 with half the partial rows.
+int64_t bwd_groups(int64_t rows, int rows_per_group, int threads) {
     const int64_t b = (rows + rows_per_group - 1) / rows_per_group;
-    return b < kMaxParts ? b : kMaxParts;
+    int64_t most = int64_t(device_cus()) * (threads == 256 ? 2 : 1);
+    if (most > kMaxParts) most = kMaxParts;
+    return b < most ? b : most;
 }
 
 bool overlaps(const void *a, const void *b, size_t bytes) {
@@ -448,8 +458,9 @@ int ionn_layer_norm_fwd(const void *x, const float *gamma, const float *beta, do
             constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
             constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;
             constexpr int kBlock = TPR < kThreads ? kThreads : TPR;
+            // as many workgroups as are resident at once: rows are dealt out evenly
             int64_t blocks = (rows + kRows - 1) / kRows;
-            const int64_t most = int64_t(device_cus()) * (2048 / kBlock);
+            const int64_t most = int64_t(device_cus()) * ((NV * VE > 8 ? 1024 : 2048) / kBlock);
             if (blocks > most) blocks = most;
             norm_fwd_kernel<T, VE, TPR, NV><<<dim3(unsigned(blocks)), dim3(kBlock), 0, st>>>(
                 static_cast<const T *>(x), gamma, beta, float(eps), static_cast<T *>(y), mean, rstd, rows, int(cols), n,
@@ -503,15 +514,14 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean, const 
             T *tdx = static_cast<T *>(dx);
             const bool done = with_shape<VE, true>(cols, [&](auto tpr, auto nv) {
                 constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-                constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;
-                constexpr int kBlock = TPR < kThreads ? kThreads : TPR;
-                groups = bwd_groups(rows, kRows);
+                constexpr int kBlock = bwd_threads(TPR), kRows = kBlock / TPR;
+                groups = bwd_groups(rows, kRows, kBlock);
                 norm_bwd_kernel<T, VE, TPR, NV><<<dim3(unsigned(groups)), dim3(kBlock), 0, st>>>(
                     tdy, tx, mean, rstd, gamma, tdr, tdx, part, rows, int(cols), n);
             });
             if (!done) {
                 if (sums) {
-                    groups = bwd_groups(rows, 1);
+                    groups = bwd_groups(rows, 1, kThreads);
                     const dim3 grid(unsigned((cols + kThreads * VE - 1) / (kThreads * VE)), unsigned(groups));
                     norm_bwd_cols_kernel<T, VE><<<grid, dim3(kThreads), 0, st>>>(tdy, tx, mean, rstd, part, rows,
                                                                                  int(cols));
