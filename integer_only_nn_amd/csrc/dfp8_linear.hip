@@ -22,39 +22,128 @@ bool sizes_ok(int64_t B, int64_t IN, int64_t OUT) {
     return B >= 0 && IN >= 0 && OUT >= 0 && B <= kMaxSide && IN <= kMaxSide && OUT <= kMaxSide;
 }
 
-// C [M][N] of type `dtype` from the product over K; M, N >= 1.
-template <bool A_KM, bool B_KM, bool LINEAR>
-void launch_product(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, const Epi &ep, int dtype, int M,
-                    int N, int K, hipStream_t st) {
-    const int64_t tiles = int64_t((M + 63) / 64) * ((N + 63) / 64);
-    const int64_t tiles256 = int64_t((M + 255) / 256) * ((N + 255) / 256);
-    with_dtype(dtype, [&](auto tag) {
-        using T = decltype(tag);
-        if constexpr (!LINEAR) {
-            if (M <= kRowsMax && K >= kRowsMinK) {
-                const dim3 grid(unsigned((N + 15) / 16)), block(kRowWaves * 64);
-                if (M <= 16) rows_kernel<T, 1><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
-                else if (M <= 32) rows_kernel<T, 2><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
-                else rows_kernel<T, 4><<<grid, block, 0, st>>>(A, B, ep, M, N, K);
-                return;
-            }
-        }
-        if (tiles256 >= 64 && tile256_fits<A_KM, B_KM>(A, lda, B, ldb, M, N, K)) {
-            tile256_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles256)), dim3(g256::NT), 0, st>>>(
-                A, lda, B, ldb, uint32_t((A_KM ? M : K) * lda), uint32_t((B_KM ? N : K) * ldb), ep, M, N, K);
-            return;
-        }
-        const int a_side = A_KM ? K : M, b_side = B_KM ? K : N;  // contiguous
-        if (a_side < 16 || b_side < 16)
-            tile_kernel<T, 64, 64, 2, A_KM, B_KM, LINEAR, true>
-                <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
-        else
-            tile_kernel<T, 64, 64, 4, A_KM, B_KM, LINEAR, false>
-                <<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(A, lda, B, ldb, ep, M, N, K);
-    });
+// ---- how a product is cut ------------------------------------------------------
+
+enum Path { ROWS, TILE256, TILE, TINY };
+
+struct Plan {
+    Path path;
+    int64_t tiles;
+    int split;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// By the sizes alone (the workspace query knows no addresses); operands whose
+// address does not suit TILE256 take TILE.
+template <bool A_KM, bool B_KM>
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
+    Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1};
+    const int64_t a_side = A_KM ? K : M, b_side = B_KM ? K : N;  // contiguous
+    if (forward && M <= kRowsMax && K >= kRowsMinK) {
+        p.path = ROWS;
+        return p;
+    }
+    if (a_side < 16 || b_side < 16) {
+        p.path = TINY;
+        return p;
+    }
+    const int64_t lda = A_KM ? K : M, ldb = B_KM ? K : N;
+    const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256);
+    if (tiles256 >= 64 && tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
+        p.path = TILE256;
+        p.tiles = tiles256;
+        return p;
+    }
+    // few tiles over a long reduction: ranges of at least four steps, about
+    // two workgroups per compute unit
+    const int64_t steps = ceil_div(K, BK);
+    if (p.tiles < 256 && steps >= 16) {
+        int64_t split = ceil_div(512, p.tiles);
+        if (split > steps / 4) split = steps / 4;
+        if (split > 32) split = 32;
+        p.split = int(split);
+    }
+    return p;
 }
 
-bool tiles_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) <= 0x7fffffff; }
+size_t part_bytes(const Plan &p, int64_t M, int64_t N) {
+    return p.split > 1 ? (size_t(p.split) * M * N * sizeof(int32_t) + 15) & ~size_t(15) : 0;
+}
+
+Product make_product(const Plan &pl, const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, const Epi &ep,
+                     int64_t M, int64_t N, int64_t K, void *part) {
+    return Product{A,      B,      lda,      ldb, ep, int(M), int(N), int(K), pl.split, static_cast<int32_t *>(part),
+                   int(pl.tiles * pl.split)};
+}
+
+template <class T, bool A_KM, bool B_KM, bool LINEAR>
+void launch_tile256(const Product &p, hipStream_t st) {
+    const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+    tile256_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles)), dim3(g256::NT), 0, st>>>(
+        p.A, p.lda, p.B, p.ldb, uint32_t((A_KM ? p.M : p.K) * p.lda), uint32_t((B_KM ? p.N : p.K) * p.ldb), p.ep, p.M, p.N,
+        p.K);
+}
+
+// The path a planned product takes with these operands.
+Path path_of(const Plan &pl, const int8_t *A, const int8_t *B) {
+    return pl.path == TILE256 && !(aligned(A, 16) && aligned(B, 16)) ? TILE : pl.path;
+}
+
+// (a TILE256 plan that falls back to 64 x 64 tiles has that many of them)
+void as_tiles(Product &p) { p.blocks = int(ceil_div(p.M, 64) * ceil_div(p.N, 64) * p.split); }
+
+unsigned sum_groups(const Product &p) { return unsigned(ceil_div(int64_t(p.M) * ceil_div(p.N, 4), NT)); }
+
+template <class T>
+void launch_forward(const Plan &pl, Product p, hipStream_t st) {
+    const Path path = path_of(pl, p.A, p.B);
+    if (path == ROWS) {
+        const dim3 grid(unsigned(ceil_div(p.N, 16))), block(kRowWaves * 64);
+        if (p.M <= 16) rows_kernel<T, 1><<<grid, block, 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
+        else if (p.M <= 32) rows_kernel<T, 2><<<grid, block, 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
+        else rows_kernel<T, 4><<<grid, block, 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
+    } else if (path == TILE256) {
+        launch_tile256<T, true, true, false>(p, st);
+    } else {
+        as_tiles(p);
+        const dim3 grid(unsigned(p.blocks)), block(NT);
+        if (path == TINY) tile_kernel<T, 64, 64, 2, true, true, false, true><<<grid, block, 0, st>>>(p);
+        else tile_kernel<T, 64, 64, 4, true, true, false, false><<<grid, block, 0, st>>>(p);
+        if (p.split > 1) sum_kernel<T, false><<<dim3(sum_groups(p)), block, 0, st>>>(p);
+    }
+}
+
+// dX's product d and G's g; one of blocks = 0 is not asked for.
+template <class T>
+void launch_backward(const Plan &pd, Product d, const Plan &pg, Product g, hipStream_t st) {
+    if (d.blocks && path_of(pd, d.A, d.B) == TILE256) {
+        launch_tile256<T, true, false, true>(d, st);
+        d.blocks = 0;
+    }
+    if (g.blocks && path_of(pg, g.A, g.B) == TILE256) {
+        launch_tile256<T, false, false, true>(g, st);
+        g.blocks = 0;
+    }
+    const dim3 block(NT);
+    if (d.blocks && pd.path == TINY) {
+        tile_kernel<T, 64, 64, 2, true, false, true, true><<<dim3(unsigned(d.blocks)), block, 0, st>>>(d);
+        d.blocks = 0;
+    }
+    if (g.blocks && pg.path == TINY) {
+        tile_kernel<T, 64, 64, 2, false, false, true, true><<<dim3(unsigned(g.blocks)), block, 0, st>>>(g);
+        g.blocks = 0;
+    }
+    if (d.blocks) as_tiles(d);
+    if (g.blocks) as_tiles(g);
+    if (d.blocks + g.blocks == 0) return;
+    tile_pair_kernel<T, 64, 64, 4><<<dim3(unsigned(d.blocks) + unsigned(g.blocks)), block, 0, st>>>(d, g);
+    const unsigned sd = d.blocks && d.split > 1 ? sum_groups(d) : 0u, sg = g.blocks && g.split > 1 ? sum_groups(g) : 0u;
+    if (sd + sg) sum_pair_kernel<T><<<dim3(sd + sg), block, 0, st>>>(d, g, int(sd));
+}
+
+// (twice: the two products of a backward pass share a grid)
+bool tiles_ok(int64_t M, int64_t N) { return 2 * ceil_div(M, 64) * ceil_div(N, 64) <= 0x7fffffff; }
 
 // edZ = 0 (and status 0) for an empty error; G and gb of an empty batch, dX
 // of an empty layer.
@@ -77,8 +166,8 @@ using namespace ionn;
 extern "C" {
 
 size_t dfp8_linear_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT) {
-    if (!sizes_ok(B, IN, OUT)) return 0;
-    return 0;
+    if (!sizes_ok(B, IN, OUT) || B == 0 || OUT == 0) return 0;
+    return part_bytes(make_plan<true, true>(B, OUT, IN, true), B, OUT);
 }
 
 int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const int32_t *eW, const float *bias, int act,
@@ -102,13 +191,19 @@ int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const i
     IONN_REQUIRE(need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need), IONN_ERR_WORKSPACE,
                  "dfp8_linear_fwd: needs a 16-byte aligned workspace of %zu bytes", need);
     const Epi ep{eX, eW, bias, residual, Z, Y, absmax_Y, act};
-    launch_product<true, true, false>(X, IN, W, IN, ep, dtype, int(B), int(OUT), int(IN), as_stream(stream));
+    const Plan plan = make_plan<true, true>(B, OUT, IN, true);
+    const Product p = make_product(plan, X, IN, W, IN, ep, B, OUT, IN, workspace);
+    with_dtype(dtype, [&](auto tag) { launch_forward<decltype(tag)>(plan, p, as_stream(stream)); });
     return check_launch("dfp8_linear_fwd");
 }
 
 size_t dfp8_linear_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT) {
     if (!sizes_ok(B, IN, OUT) || B == 0 || OUT == 0) return 0;
-    return act_workspace_bytes(B, OUT);
+    size_t n = act_workspace_bytes(B, OUT);
+    if (IN > 0)
+        n += part_bytes(make_plan<true, false>(B, IN, OUT, false), B, IN) +
+             part_bytes(make_plan<false, false>(OUT, IN, B, false), OUT, IN);
+    return n;
 }
 
 int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype, const int8_t *X, const int32_t *eX,
@@ -146,14 +241,15 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype, const int
     }
     if (int rc = launch_act_bwd(dY, Z, act, dtype, B, OUT, dZ8, edZ, gb, status_out, workspace, st)) return rc;
     if (IN == 0) return IONN_OK;
-    if (dX) {
-        const Epi ep{edZ, eW, nullptr, nullptr, nullptr, dX, nullptr, IONN_ACT_NONE};
-        launch_product<true, false, true>(dZ8, OUT, W, IN, ep, dtype, int(B), int(IN), int(OUT), st);
-    }
-    if (G) {
-        const Epi ep{edZ, eX, nullptr, nullptr, nullptr, G, nullptr, IONN_ACT_NONE};
-        launch_product<false, false, true>(dZ8, OUT, X, IN, ep, dtype, int(OUT), int(IN), int(B), st);
-    }
+    char *parts = static_cast<char *>(workspace) + act_workspace_bytes(B, OUT);
+    const Plan pd = make_plan<true, false>(B, IN, OUT, false), pg = make_plan<false, false>(OUT, IN, B, false);
+    const Epi ed{edZ, eW, nullptr, nullptr, nullptr, dX, nullptr, IONN_ACT_NONE};
+    const Epi eg{edZ, eX, nullptr, nullptr, nullptr, G, nullptr, IONN_ACT_NONE};
+    Product d = make_product(pd, dZ8, OUT, W, IN, ed, B, IN, OUT, parts);
+    Product g = make_product(pg, dZ8, OUT, X, IN, eg, OUT, IN, B, parts + part_bytes(pd, B, IN));
+    if (!dX) d.blocks = 0;
+    if (!G) g.blocks = 0;
+    with_dtype(dtype, [&](auto tag) { launch_backward<decltype(tag)>(pd, d, pg, g, st); });
     return check_launch("dfp8_linear_bwd");
 }
 

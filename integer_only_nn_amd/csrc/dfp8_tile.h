@@ -278,21 +278,65 @@ __device__ __forceinline__ void tile_sums(const int8_t *__restrict__ A, int64_t 
     }
 }
 
+// A product C [M][N] over K with its epilogue, cut into tiles and, where
+// there are few of them over a long reduction, into `split` ranges of K: each
+// range leaves its int32 sums in part [split][M][N], and sum_kernel adds them
+// (exactly, so in any order) and applies the epilogue.
+struct Product {
+    const int8_t *A, *B;
+    int64_t lda, ldb;
+    Epi ep;
+    int M, N, K;
+    int split;      // 1: the tiles apply the epilogue themselves
+    int32_t *part;  // nullable when split is 1
+    int blocks;     // workgroups: tiles * split
+};
+
+// Workgroup `id` of a product: the tile id % tiles over range id / tiles.
 template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
-__global__ __launch_bounds__(NT) void tile_kernel(const int8_t *__restrict__ A, int64_t lda,
-                                                  const int8_t *__restrict__ B, int64_t ldb, Epi ep, int M, int N,
-                                                  int K) {
+__device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) {
     constexpr int FM = BM / 64, FN = BN / 64;
-    __shared__ __attribute__((aligned(256))) int8_t lds[2 * (BM + BN) * BK];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
+    const int M = p.M, N = p.N;
+    const int tiles = p.blocks / p.split, range = id / tiles;
     int tm, tn;
-    gemm::tile_coords(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+    gemm::tile_coords(id - range * tiles, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
+    const int steps = (p.K + BK - 1) / BK;
+    const int k_begin = int(int64_t(steps) * range / p.split) * BK;
+    const int k_end = min(p.K, int(int64_t(steps) * (range + 1) / p.split) * BK);
     v16i acc[FM][FN];
-    tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(A, lda, B, ldb, M, N, m0, n0, 0, K, lds, wm, wn, lane, acc);
+    tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(p.A, p.lda, p.B, p.ldb, M, N, m0, n0, k_begin, k_end, lds, wm, wn, lane,
+                                               acc);
     // lane: row lane % 32, columns 8 q + 4 (lane / 32) .. + 3 of each block
+    const int64_t mr = int64_t(m0) + wm + (lane & 31);
+    const int nc = n0 + wn + 4 * (lane >> 5);
+    if (p.split > 1) {
+        typedef v4i loose __attribute__((aligned(4)));
+        int32_t *part = p.part + int64_t(range) * M * N;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v4i s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    const int64_t m = mr + 32 * i;
+                    const int n = nc + 32 * j + 8 * q;
+                    if (m >= M) continue;
+                    if (n + 4 <= N) {
+                        *reinterpret_cast<loose *>(part + m * N + n) = s;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (n + e < N) part[m * N + n + e] = s[e];
+                    }
+                }
+        return;
+    }
+    const Epi &ep = p.ep;
     const int e2 = *ep.ea + *ep.eb;
     uint32_t top = 0;
     with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
@@ -303,15 +347,80 @@ __global__ __launch_bounds__(NT) void tile_kernel(const int8_t *__restrict__ A, 
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const v4i s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                    top = max(top, finish4<T, decltype(ac)::value, LINEAR>(
-                                       s, ep, e2, int64_t(m0) + wm + 32 * i + (lane & 31),
-                                       n0 + wn + 32 * j + 8 * q + 4 * (lane >> 5), M, N));
+                    top = max(top, finish4<T, decltype(ac)::value, LINEAR>(s, ep, e2, mr + 32 * i, nc + 32 * j + 8 * q,
+                                                                           M, N));
                 }
     });
     if (!LINEAR && ep.absmax) {
         top = wave_max_u32(top);
         if (lane == 0) publish_max_u32(ep.absmax, top);
     }
+}
+
+template <int BM, int BN>
+constexpr int kTileLds = 2 * (BM + BN) * BK;
+
+template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
+__global__ __launch_bounds__(NT) void tile_kernel(Product p) {
+    __shared__ __attribute__((aligned(256))) int8_t lds[kTileLds<BM, BN>];
+    run_tile<T, BM, BN, DEPTH, A_KM, B_KM, LINEAR, TINY>(p, int(blockIdx.x), lds);
+}
+
+// The two products of a backward pass in one launch: dX's workgroups, then
+// G's (a product that is not asked for has none).
+template <class T, int BM, int BN, int DEPTH>
+__global__ __launch_bounds__(NT) void tile_pair_kernel(Product d, Product g) {
+    __shared__ __attribute__((aligned(256))) int8_t lds[kTileLds<BM, BN>];
+    if (int(blockIdx.x) < d.blocks)
+        run_tile<T, BM, BN, DEPTH, true, false, true, false>(d, int(blockIdx.x), lds);
+    else
+        run_tile<T, BM, BN, DEPTH, false, false, true, false>(g, int(blockIdx.x) - d.blocks, lds);
+}
+
+// The sums of the ranges through the epilogue, four columns of a row per
+// thread; element `id` of the product's M * ceil(N / 4).
+template <class T, bool LINEAR>
+__device__ __forceinline__ void sum_ranges(const Product &p, int64_t id) {
+    typedef v4i loose __attribute__((aligned(4)));
+    const int n4 = (p.N + 3) / 4;
+    const int64_t m = id / n4;
+    const int n = 4 * int(id - m * n4);
+    uint32_t top = 0;
+    if (m < p.M) {
+        const int32_t *at = p.part + m * p.N + n;
+        const int64_t step = int64_t(p.M) * p.N;
+        v4i s = {0, 0, 0, 0};
+        if (n + 4 <= p.N) {
+#pragma unroll 4
+            for (int r = 0; r < p.split; ++r) s += *reinterpret_cast<const loose *>(at + r * step);
+        } else {
+            for (int r = 0; r < p.split; ++r)
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (n + e < p.N) s[e] += at[r * step + e];
+        }
+        const int e2 = *p.ep.ea + *p.ep.eb;
+        with_act(LINEAR ? int(IONN_ACT_NONE) : p.ep.act, [&](auto ac) __attribute__((always_inline)) {
+            top = finish4<T, decltype(ac)::value, LINEAR>(s, p.ep, e2, m, n, p.M, p.N);
+        });
+    }
+    if (!LINEAR && p.ep.absmax) {
+        top = wave_max_u32(top);
+        if ((threadIdx.x & 63) == 0) publish_max_u32(p.ep.absmax, top);
+    }
+}
+
+template <class T, bool LINEAR>
+__global__ __launch_bounds__(NT) void sum_kernel(Product p) {
+    sum_ranges<T, LINEAR>(p, int64_t(blockIdx.x) * NT + threadIdx.x);
+}
+
+// The same for the two products of a backward pass (workgroups of the first,
+// d_groups of them, then the second's).
+template <class T>
+__global__ __launch_bounds__(NT) void sum_pair_kernel(Product d, Product g, int d_groups) {
+    if (int(blockIdx.x) < d_groups) sum_ranges<T, true>(d, int64_t(blockIdx.x) * NT + threadIdx.x);
+    else sum_ranges<T, true>(g, int64_t(int(blockIdx.x) - d_groups) * NT + threadIdx.x);
 }
 
 }  // namespace dfp8
