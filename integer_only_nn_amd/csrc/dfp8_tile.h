@@ -220,6 +220,46 @@ __device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2,
     return top;
 }
 
+// Row m, columns n .. n + 7 of the sums through the epilogue; b: the columns'
+// bias.
+template <class T, int ACT, bool LINEAR>
+__device__ __forceinline__ uint32_t finish8(const v4i &lo, const v4i &hi, const Epi &ep, int e2, const float (&b)[8],
+                                            int64_t m, int n, int M, int N) {
+    if (m >= M || n >= N) return 0u;
+    const int valid = N - n;
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        z[i] = __builtin_amdgcn_ldexpf(float(lo[i]), e2);
+        z[4 + i] = __builtin_amdgcn_ldexpf(float(hi[i]), e2);
+    }
+    const int64_t at = m * N + n;
+    T *y = static_cast<T *>(ep.y) + at;
+    if (LINEAR) {
+        store_vec<T, 8>(y, z, valid);
+        return 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += b[i];
+    if (ep.z) store_vec<T, 8>(static_cast<T *>(ep.z) + at, z, valid);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = act_value<ACT>(z[i]);
+    if (ep.residual) {
+        const auto r = load_raw<T, 8>(static_cast<const T *>(ep.residual) + at, valid);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += float(r[i]);
+    }
+    store_vec<T, 8>(y, o, valid);
+    uint32_t top = 0;
+    if (ep.absmax) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) top = max(top, mag_bits(o[i]));
+    }
+    return top;
+}
+
 // The sums of one tile over k in [k_begin, k_end) (k_begin and, but for the
 // last range, k_end multiples of BK).  lds: 2 stages of (BM + BN) * BK bytes.
 template <int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool TINY>
@@ -292,6 +332,9 @@ struct Product {
     int blocks;     // workgroups: tiles * split
 };
 
+template <int BM, int BN>
+constexpr int kTileLds = 2 * (BM + BN) * BK;
+
 // Workgroup `id` of a product: the tile id % tiles over range id / tiles.
 template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
 __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) {
@@ -310,55 +353,71 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
     v16i acc[FM][FN];
     tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(p.A, p.lda, p.B, p.ldb, M, N, m0, n0, k_begin, k_end, lds, wm, wn, lane,
                                                acc);
-    // lane: row lane % 32, columns 8 q + 4 (lane / 32) .. + 3 of each block
-    const int64_t mr = int64_t(m0) + wm + (lane & 31);
-    const int nc = n0 + wn + 4 * (lane >> 5);
+    // The tile through LDS (lane: row lane % 32, columns 8 q + 4 (lane / 32)
+    // .. + 3 of each 32 x 32 block; 16-byte piece c of row r at position c ^ (r
+    // & 15), free of bank conflicts), so that a thread finishes eight columns
+    // and a row's run of 128 bytes or more leaves together.
+    static_assert(BM * BN * 4 <= kTileLds<BM, BN>, "the sums fit where the stages were");
+    constexpr int kPieces = BN / 4;  // of a row
+    v4i *buf = reinterpret_cast<v4i *>(lds);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = wm + 32 * i + (lane & 31), c = (wn + 32 * j) / 4 + 2 * q + (lane >> 5);
+                buf[r * kPieces + (c ^ (r & 15))] =
+                    v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            }
+    __syncthreads();
+    const int c = 2 * (int(threadIdx.x) % (BN / 8)), n = n0 + 4 * c;
+    constexpr int kRows = NT / (BN / 8);  // rows finished at once
     if (p.split > 1) {
         typedef v4i loose __attribute__((aligned(4)));
         int32_t *part = p.part + int64_t(range) * M * N;
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int k = 0; k < BM / kRows; ++k) {
+            const int r = kRows * k + int(threadIdx.x) / (BN / 8);
+            const int64_t m = int64_t(m0) + r;
+            if (m >= M) continue;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int h = 0; h < 2; ++h) {
+                const v4i s = buf[r * kPieces + ((c + h) ^ (r & 15))];
+                const int nh = n + 4 * h;
+                if (nh + 4 <= N) {
+                    *reinterpret_cast<loose *>(part + m * N + nh) = s;
+                } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const v4i s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                    const int64_t m = mr + 32 * i;
-                    const int n = nc + 32 * j + 8 * q;
-                    if (m >= M) continue;
-                    if (n + 4 <= N) {
-                        *reinterpret_cast<loose *>(part + m * N + n) = s;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 3; ++e)
-                            if (n + e < N) part[m * N + n + e] = s[e];
-                    }
+                    for (int e = 0; e < 3; ++e)
+                        if (nh + e < N) part[m * N + nh + e] = s[e];
                 }
+            }
+        }
         return;
     }
     const Epi &ep = p.ep;
     const int e2 = *ep.ea + *ep.eb;
+    float bias[8] = {};
+    if (!LINEAR && ep.bias) {
+        const auto raw = load_raw<float, 8>(ep.bias + n, N - n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = raw[i];
+    }
     uint32_t top = 0;
     with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const v4i s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                    top = max(top, finish4<T, decltype(ac)::value, LINEAR>(s, ep, e2, mr + 32 * i, nc + 32 * j + 8 * q,
-                                                                           M, N));
-                }
+        for (int k = 0; k < BM / kRows; ++k) {
+            const int r = kRows * k + int(threadIdx.x) / (BN / 8);
+            const v4i lo = buf[r * kPieces + (c ^ (r & 15))], hi = buf[r * kPieces + ((c + 1) ^ (r & 15))];
+            top = max(top, finish8<T, decltype(ac)::value, LINEAR>(lo, hi, ep, e2, bias, int64_t(m0) + r, n, M, N));
+        }
     });
     if (!LINEAR && ep.absmax) {
         top = wave_max_u32(top);
         if (lane == 0) publish_max_u32(ep.absmax, top);
     }
 }
-
-template <int BM, int BN>
-constexpr int kTileLds = 2 * (BM + BN) * BK;
 
 template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
 __global__ __launch_bounds__(NT) void tile_kernel(Product p) {

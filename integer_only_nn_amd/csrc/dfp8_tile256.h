@@ -46,46 +46,6 @@ struct EdgeSrc : g256::TileSrc<KMAJOR> {
     }
 };
 
-// Row m, columns n .. n + 7 of the sums through the epilogue; b: the columns'
-// bias.
-template <class T, int ACT, bool LINEAR>
-__device__ __forceinline__ uint32_t finish8(const v4i &lo, const v4i &hi, const Epi &ep, int e2, const float (&b)[8],
-                                            int64_t m, int n, int M, int N) {
-    if (m >= M || n >= N) return 0u;
-    const int valid = N - n;
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        z[i] = __builtin_amdgcn_ldexpf(float(lo[i]), e2);
-        z[4 + i] = __builtin_amdgcn_ldexpf(float(hi[i]), e2);
-    }
-    const int64_t at = m * N + n;
-    T *y = static_cast<T *>(ep.y) + at;
-    if (LINEAR) {
-        store_vec<T, 8>(y, z, valid);
-        return 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += b[i];
-    if (ep.z) store_vec<T, 8>(static_cast<T *>(ep.z) + at, z, valid);
-    float o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = act_value<ACT>(z[i]);
-    if (ep.residual) {
-        const auto r = load_raw<T, 8>(static_cast<const T *>(ep.residual) + at, valid);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += float(r[i]);
-    }
-    store_vec<T, 8>(y, o, valid);
-    uint32_t top = 0;
-    if (ep.absmax) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < valid) top = max(top, mag_bits(o[i]));
-    }
-    return top;
-}
-
 // The epilogue of a wavefront's 128 x 128 sums, 64 columns at a time through
 // 32 KiB of LDS: the accumulators are written as they lie (lane: row lane %
 // 32, columns 8 q + 4 (lane / 32) .. + 3 of each 32 x 32 block; 16-byte piece
