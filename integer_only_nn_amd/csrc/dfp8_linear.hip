@@ -49,8 +49,15 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
         return p;
     }
     const int64_t lda = A_KM ? K : M, ldb = B_KM ? K : N;
+    // 256 x 256 tiles where their rounds of one per compute unit are expected
+    // to end first.  In us, fitted to measurements: a round takes 20 (12
+    // without an activation) and K / 120, the 64 x 64 kernel 8 and its share of
+    // M N K.  64 tiles of 256 at K = 2048: 37 against 23 us forward; 128 at K =
+    // 4096: 55 against 67; 64 at K = 8192, no activation: 80 against 88.
     const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256);
-    if (tiles256 >= 64 && tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
+    const double rounds = double(ceil_div(tiles256, 256)), work = double(M) * double(N) * double(K) / 65536.0;
+    const bool large = rounds * ((forward ? 20.0 : 12.0) + double(K) / 120.0) < 8.0 + work / (forward ? 8850.0 : 6900.0);
+    if (large && tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
         p.path = TILE256;
         p.tiles = tiles256;
         return p;
