@@ -506,7 +506,8 @@ class AdamW:
             if stream is None:
                 self.step_dev.add_(1)
             else:
-                with torch.cuda.stream(stream):
+                on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+                with torch.cuda.stream(on):
                     self.step_dev.add_(1)
         self.t += 1
         ops.check(ops.lib().ionn_adamw_step(
@@ -514,3 +515,87 @@ class AdamW:
             float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps), float(self.weight_decay),
             ops._a(self.step_dev), ops._a(self.lr_dev), ops._a(grad_scale, torch.float32, 1, "grad_scale"),
             ops._a(absmax_P, torch.int32, len(self.P), "absmax_P"), ops._on(stream, self.P[0])), "ionn_adamw_step")
+
+
+# ---------------------------------------------------------------------------
+# The residual MLP block of a transformer on DFP-8 products.
+# ---------------------------------------------------------------------------
+
+class ResidualMlp:
+    """y = x + W2 act(W1 norm(x) + b1) + b2 over a batch of B rows, trained as
+    "Mixed Precision Training of Convolutional Neural Networks using Integer
+    Operations" (section 4) lays out: integer products on DFP-8 copies of
+    activations, weights and errors, everything around them in floating
+    point, FP32 master weights.
+
+    Activations and their gradients are of type dtype.  Weights decay, gains
+    and biases do not; both groups keep their moments in state_bits bits.  All
+    buffers are allocated here, so a step only enqueues kernels (and can be
+    captured in a graph with on_device)."""
+
+    def __init__(self, W1, b1, W2, b2, gamma, beta, B, dtype=torch.bfloat16, act="gelu", eps=1e-5, state_bits=8,
+                 lr=1e-3, betas=(0.9, 0.999), weight_decay=0.01, on_device=False):
+        """W1: [H][D], b1: [H], W2: [D][H], b2, gamma, beta: [D], float32 device tensors, updated in place."""
+        H, D = W1.shape
+        ops._same(W2.shape == (D, H) and b1.numel() == H and all(t.numel() == D for t in (b2, gamma, beta)),
+                  "the block's weights")
+        dev = W1.device
+        new = lambda *shape, dt=dtype: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+        f32, i8, i32 = torch.float32, torch.int8, torch.int32
+        self.B, self.act, self.eps = B, act, eps
+        self.W1, self.b1, self.W2, self.b2, self.gamma, self.beta = W1, b1, W2, b2, gamma, beta
+        self.W1_8, self.W2_8 = new(H, D, dt=i8), new(D, H, dt=i8)
+        # exponents: norm output, hidden activation, W1, W2, the two errors
+        self.e = torch.zeros(6, dtype=i32, device=dev)
+        # largest magnitudes: norm output, hidden activation, W1, W2 (float32 bits)
+        self.top = torch.zeros(4, dtype=i32, device=dev)
+        self.status = torch.zeros(2, dtype=i32, device=dev)  # of the last backward's errors
+        self.h, self.h8, self.mean, self.rstd = new(B, D), new(B, D, dt=i8), new(B, dt=f32), new(B, dt=f32)
+        self.z, self.a, self.a8, self.y = new(B, H), new(B, H), new(B, H, dt=i8), new(B, D)
+        self.da, self.dh, self.dx = new(B, H), new(B, D), new(B, D)
+        self.d2_8, self.d1_8 = new(B, D, dt=i8), new(B, H, dt=i8)
+        self.gW1, self.gW2 = new(H, D), new(D, H)
+        self.gb1, self.gb2, self.ggamma, self.gbeta = new(H, dt=f32), new(D, dt=f32), new(D, dt=f32), new(D, dt=f32)
+        need = max(ops.dfp8_linear_fwd_workspace_bytes(B, D, H), ops.dfp8_linear_fwd_workspace_bytes(B, H, D),
+                   ops.dfp8_linear_bwd_workspace_bytes(B, D, H), ops.dfp8_linear_bwd_workspace_bytes(B, H, D),
+                   ops.ionn_layer_norm_bwd_workspace_bytes(B, D), ops.dfp8_from_float_workspace_bytes())
+        self.ws = new(need, dt=torch.uint8)
+        kw = dict(bits=state_bits, lr=lr, betas=betas, on_device=on_device)
+        self.opt = AdamW.make([W1, W2], weight_decay=weight_decay, **kw)
+        self.opt.bind_grads([self.gW1, self.gW2])
+        self.opt_vectors = AdamW.make([b1, b2, gamma, beta], weight_decay=0.0, **kw)
+        self.opt_vectors.bind_grads([self.gb1, self.gb2, self.ggamma, self.gbeta])
+        ops.dfp8_from_float(W1, self.W1_8, self.e[2:3], workspace=self.ws)
+        ops.dfp8_from_float(W2, self.W2_8, self.e[3:4], workspace=self.ws)
+
+    def forward(self, x, stream=None):
+        """y of a batch x [B][D]; keeps what backward() reads."""
+        e, top, kw = self.e, self.top, dict(stream=stream)
+        ops.ionn_fill_u32(top, 0, **kw)
+        ops.ionn_layer_norm_fwd(x, self.h, gamma=self.gamma, beta=self.beta, eps=self.eps, mean=self.mean,
+                                rstd=self.rstd, absmax_y=top[0:1], **kw)
+        ops.dfp8_from_float(self.h, self.h8, e[0:1], absmax=top[0:1], **kw)
+        ops.dfp8_linear_fwd(self.h8, e[0:1], self.W1_8, e[2:3], self.a, bias=self.b1, act=self.act, Z=self.z,
+                            absmax_Y=top[1:2], workspace=self.ws, **kw)
+        ops.dfp8_from_float(self.a, self.a8, e[1:2], absmax=top[1:2], **kw)
+        ops.dfp8_linear_fwd(self.a8, e[1:2], self.W2_8, e[3:4], self.y, bias=self.b2, residual=x, workspace=self.ws,
+                            **kw)
+        return self.y
+
+    def backward(self, x, dy, stream=None):
+        """dx, and every parameter's gradient, for the error dy of the last forward(x)."""
+        e, kw = self.e, dict(workspace=self.ws, stream=stream)
+        ops.dfp8_linear_bwd(dy, None, "none", self.a8, e[1:2], self.W2_8, e[3:4], self.d2_8, e[4:5], dX=self.da,
+                            G=self.gW2, gb=self.gb2, status_out=self.status[0:1], **kw)
+        ops.dfp8_linear_bwd(self.da, self.z, self.act, self.h8, e[0:1], self.W1_8, e[2:3], self.d1_8, e[5:6],
+                            dX=self.dh, G=self.gW1, gb=self.gb1, status_out=self.status[1:2], **kw)
+        ops.ionn_layer_norm_bwd(self.dh, x, self.mean, self.rstd, self.dx, gamma=self.gamma, dres=dy,
+                                dgamma=self.ggamma, dbeta=self.gbeta, **kw)
+        return self.dx
+
+    def update(self, stream=None):
+        """The optimiser step on the last backward's gradients, and the new DFP-8 weights."""
+        self.opt.step(absmax_P=self.top[2:4], stream=stream)
+        self.opt_vectors.step(stream=stream)
+        ops.dfp8_from_float(self.W1, self.W1_8, self.e[2:3], absmax=self.top[2:3], stream=stream)
+        ops.dfp8_from_float(self.W2, self.W2_8, self.e[3:4], absmax=self.top[3:4], stream=stream)
