@@ -26,7 +26,7 @@ ActLayout act_layout(int64_t B, int64_t OUT, size_t es);
 size_t act_workspace_bytes(int64_t B, int64_t OUT);
 
 // dZ = dY act'(Z): its column sums gb (nullable), its DFP-8 form and status
-// (nullable).  B, OUT >= 1.  Two launches.
+// (nullable).  B, OUT >= 1.  One launch for small errors, else two.
 int launch_act_bwd(const void *dY, const void *Z, int act, int dtype, int64_t B, int64_t OUT, int8_t *dZ8,
                    int32_t *edZ, float *gb, int32_t *status, void *workspace, hipStream_t st);
 

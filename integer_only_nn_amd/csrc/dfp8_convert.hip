@@ -181,6 +181,109 @@ __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict
     }
 }
 
+// Both passes in one workgroup, for an error of at most 16 values a thread:
+// read once, no second launch.  Piece k of kOneValues / VE is strip k / groups
+// of the columns, rows group k % groups: 16 wavefronts of 64 / lanes rows
+// each.  One compute unit takes 4.2 us for 64 x 64 errors and 6.3 for 64 x 256
+// (gelu, bfloat16) where the two launches take 7.7; past that it is the slower
+// (11 us at 128 x 256).
+constexpr int kOneThreads = 1024, kOneValues = 16;
+
+template <class T, int ACT>
+__global__ __launch_bounds__(kOneThreads) void act_one_kernel(const T *__restrict__ dY, const T *__restrict__ Z,
+                                                              int B, int OUT, int lanes_log, int strips, int groups,
+                                                              int8_t *__restrict__ dZ8, int32_t *__restrict__ edZ,
+                                                              float *__restrict__ gb, int32_t *__restrict__ status) {
+    constexpr int VE = 16 / sizeof(T), K = kOneValues / VE, kWaves = kOneThreads / 64;
+    __shared__ float fold[kWaves][64 * VE];
+    __shared__ uint32_t red[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lanes = 1 << lanes_log, per_wave = 64 >> lanes_log;
+    const int row0 = wave * per_wave + (lane >> lanes_log), col0 = (lane & (lanes - 1)) * VE;
+    const int pieces = strips * groups;
+    const int64_t last = int64_t(B) * OUT - VE;  // >= 0: the caller checks
+    float d[K][VE];
+    uint32_t m = 0;
+    // all loads in flight, none behind a lane's own condition: what lies past a
+    // row's end is dropped below, and the tensor's last piece is read again
+    // where its end cuts it
+    typename Vec<T, VE>::type y[K], z[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k < pieces) {
+            const int c = (k / groups) * lanes * VE + col0, r = (k % groups) * kWaves * per_wave + row0;
+            const int64_t at = min(int64_t(min(r, B - 1)) * OUT + c, last);
+            y[k] = load_raw<T, VE>(dY + at);
+            if (ACT != IONN_ACT_NONE) z[k] = load_raw<T, VE>(Z + at);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k < pieces) {
+            const int c = (k / groups) * lanes * VE + col0, r = (k % groups) * kWaves * per_wave + row0;
+            const int valid = r < B ? OUT - c : 0;
+            const int64_t at = int64_t(r) * OUT + c;
+            if (valid > 0 && at > last) {
+                y[k] = load_raw<T, VE>(dY + at, valid);
+                if (ACT != IONN_ACT_NONE) z[k] = load_raw<T, VE>(Z + at, valid);
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                d[k][e] = ACT == IONN_ACT_NONE ? float(y[k][e]) : float(y[k][e]) * act_grad<ACT>(float(z[k][e]));
+                if (e >= valid) d[k][e] = 0.0f;
+                m = max(m, mag_bits(d[k][e]));
+            }
+        }
+    }
+    m = wave_max_u32(m);
+    if (lane == 0) red[wave] = m;
+    __syncthreads();
+    m = red[lane & (kWaves - 1)];
+    m = wave_max_u32(m);
+    const int E = dfp8_exponent(m);
+    if (threadIdx.x == 0) {
+        *edZ = E;
+        if (status) *status = dfp8_status(m, E);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k < pieces) {
+            const int c = (k / groups) * lanes * VE + col0, r = (k % groups) * kWaves * per_wave + row0;
+            int32_t q[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) q[e] = dfp8_mantissa(d[k][e], -E);
+            store_bytes(dZ8 + int64_t(r) * OUT + c, q, VE, r < B ? OUT - c : 0);
+        }
+    }
+    if (gb == nullptr) return;
+    // a strip's rows in a thread, then the row groups of a wavefront, then the wavefronts
+    float s[VE] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k < pieces) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) s[e] += d[k][e];
+            if (k % groups == groups - 1) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    for (int off = lanes; off < 64; off <<= 1) s[e] += __shfl_xor(s[e], off, 64);
+                    fold[wave][col0 + e] = s[e];
+                    s[e] = 0.0f;
+                }
+                __syncthreads();
+                const int i = threadIdx.x, col = (k / groups) * lanes * VE + i;
+                if (i < lanes * VE && col < OUT) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) v += fold[w][i];
+                    gb[col] = v;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
 // Workgroups for a pass over n values of es bytes, 16 bytes per thread.
 unsigned pass_groups(int64_t n, size_t es, int64_t most) {
     const int64_t per = kThreads * int64_t(16 / es);
@@ -228,6 +331,9 @@ int launch_act_bwd(const void *dY, const void *Z, int act, int dtype, int64_t B,
                      : nullptr;
     int lanes_log = 0;
     while ((1 << lanes_log) < a.lanes) ++lanes_log;
+    const int64_t groups = (B + 16 * (64 / a.lanes) - 1) / (16 * (64 / a.lanes));
+    const bool one = a.strips * groups <= kOneValues / int64_t(16 / dtype_size(dtype)) &&
+                     B * OUT >= int64_t(16 / dtype_size(dtype));
     const unsigned n_round = pass_groups(B * OUT, dtype_size(dtype), 2048);
     const unsigned n_sum = gb ? unsigned((OUT + 63) / 64) : 0u;
     with_dtype(dtype, [&](auto tag) {
@@ -235,6 +341,11 @@ int launch_act_bwd(const void *dY, const void *Z, int act, int dtype, int64_t B,
         const T *y = static_cast<const T *>(dY), *z = static_cast<const T *>(Z);
         with_act(act, [&](auto ac) {
             constexpr int ACT = decltype(ac)::value;
+            if (one) {
+                act_one_kernel<T, ACT><<<dim3(1), dim3(kOneThreads), 0, st>>>(
+                    y, z, int(B), int(OUT), lanes_log, a.strips, int(groups), dZ8, edZ, gb, status);
+                return;
+            }
             act_sums_kernel<T, ACT><<<dim3(unsigned(a.strips), unsigned(a.chunks)), dim3(kThreads), 0, st>>>(
                 y, z, B, int(OUT), lanes_log, a.rows, maxima, sums);
             act_round_kernel<T, ACT><<<dim3(n_round + n_sum), dim3(kThreads), 0, st>>>(
