@@ -45,7 +45,7 @@ __global__ __launch_bounds__(kThreads) void max_kernel(const T *__restrict__ x, 
     if (threadIdx.x == 0) part[blockIdx.x] = m;
 }
 
-__device__ __forceinline__ void store_bytes(int8_t *p, const int32_t *q, int count, int valid) {
+__device__ __forceinline__ void store_bytes(int8_t *p, const uint32_t *q, int count, int valid) {
     if (valid >= count) {
         if (count == 8)
             *reinterpret_cast<__attribute__((aligned(1))) uint64_t *>(p) =
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void round_kernel(const T *__restrict__ x
     for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE; i < n; i += step) {
         const int valid = int(n - i < VE ? n - i : VE);
         const auto v = load_raw<T, VE>(x + i, valid);
-        int32_t q[VE];
+        uint32_t q[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) q[e] = dfp8_mantissa(float(v[e]), -E);
         store_bytes(out + i, q, VE, valid);
@@ -106,17 +106,32 @@ __global__ __launch_bounds__(kThreads) void act_sums_kernel(const T *__restrict_
     uint32_t m = 0;
     if (c < OUT) {
         const int valid = OUT - c;
-        for (int64_t r = int64_t(blockIdx.y) * chunk_rows + wave * per_wave + (lane >> lanes_log); r < r1;
-             r += (kThreads / 64) * per_wave) {
-            const auto y = load_raw<T, VE>(dY + r * OUT + c, valid);
-            typename Vec<T, VE>::type z;
-            if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + r * OUT + c, valid);
+        const int step = (kThreads / 64) * per_wave;
+        auto add = [&](const typename Vec<T, VE>::type &y, const typename Vec<T, VE>::type &z) __attribute__((always_inline)) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT>(float(z[e]));
+                const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[e]));
                 s[e] += d;
-                m = max(m, e < valid ? mag_bits(d) : 0u);
+                m = max(m, mag_bits(d));  // (past a row's end dY, and so d, is 0)
             }
+        };
+        int64_t r = int64_t(blockIdx.y) * chunk_rows + wave * per_wave + (lane >> lanes_log);
+        // four rows' loads in flight
+        for (; r + 3 * step < r1; r += 4 * step) {
+            typename Vec<T, VE>::type y[4], z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                y[u] = load_raw<T, VE>(dY + (r + u * step) * OUT + c, valid);
+                if (ACT != IONN_ACT_NONE) z[u] = load_raw<T, VE>(Z + (r + u * step) * OUT + c, valid);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(y[u], z[u]);
+        }
+        for (; r < r1; r += step) {
+            const auto y = load_raw<T, VE>(dY + r * OUT + c, valid);
+            typename Vec<T, VE>::type z = y;
+            if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + r * OUT + c, valid);
+            add(y, z);
         }
     }
     // the row groups of a wavefront, then the wavefronts
@@ -166,18 +181,33 @@ __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict
         if (status) *status = dfp8_status(m, E);
     }
     const int64_t step = int64_t(n_round) * kThreads * VE;
-    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE; i < n; i += step) {
-        const int valid = int(n - i < VE ? n - i : VE);
-        const auto y = load_raw<T, VE>(dY + i, valid);
-        typename Vec<T, VE>::type z;
-        if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + i, valid);
-        int32_t q[VE];
+    auto put = [&](int64_t i, const typename Vec<T, VE>::type &y, const typename Vec<T, VE>::type &z,
+                   int valid) __attribute__((always_inline)) {
+        uint32_t q[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT>(float(z[e]));
+            const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[e]));
             q[e] = dfp8_mantissa(d, -E);
         }
         store_bytes(dZ8 + i, q, VE, valid);
+    };
+    int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VE;
+    for (; i + step + VE <= n; i += 2 * step) {  // two pieces' loads in flight
+        typename Vec<T, VE>::type y[2], z[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            y[u] = load_raw<T, VE>(dY + i + u * step);
+            if (ACT != IONN_ACT_NONE) z[u] = load_raw<T, VE>(Z + i + u * step);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) put(i + u * step, y[u], z[u], VE);
+    }
+    for (; i < n; i += step) {
+        const int valid = int(n - i < VE ? n - i : VE);
+        const auto y = load_raw<T, VE>(dY + i, valid);
+        typename Vec<T, VE>::type z = y;
+        if (ACT != IONN_ACT_NONE) z = load_raw<T, VE>(Z + i, valid);
+        put(i, y, z, valid);
     }
 }
 
@@ -229,7 +259,7 @@ __global__ __launch_bounds__(kOneThreads) void act_one_kernel(const T *__restric
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                d[k][e] = ACT == IONN_ACT_NONE ? float(y[k][e]) : float(y[k][e]) * act_grad<ACT>(float(z[k][e]));
+                d[k][e] = ACT == IONN_ACT_NONE ? float(y[k][e]) : float(y[k][e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[k][e]));
                 if (e >= valid) d[k][e] = 0.0f;
                 m = max(m, mag_bits(d[k][e]));
             }
@@ -249,7 +279,7 @@ __global__ __launch_bounds__(kOneThreads) void act_one_kernel(const T *__restric
     for (int k = 0; k < K; ++k) {
         if (k < pieces) {
             const int c = (k / groups) * lanes * VE + col0, r = (k % groups) * kWaves * per_wave + row0;
-            int32_t q[VE];
+            uint32_t q[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e) q[e] = dfp8_mantissa(d[k][e], -E);
             store_bytes(dZ8 + int64_t(r) * OUT + c, q, VE, r < B ? OUT - c : 0);

@@ -67,64 +67,74 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[VE], int valid 
 // distribution function Phi; gelu_tanh is z * sigmoid(2 k (z + c z^3)), k =
 // sqrt(2 / pi), c = 0.044715 (0.5 (1 + tanh w) = sigmoid(2 w)).
 //
-// Phi(z) = sigmoid(z Q(z^2)) with Q the polynomial of degree 7 that comes
-// nearest to logit(Phi(z)) / z (a least-maximum fit, weighted by z Phi (1 -
-// Phi), over z in (0, 6.5]; it stays positive and grows beyond).  Phi is off by
-// at most 1.2e-7, two half steps of float32 at 1, which the rounding of the
-// argument leaves anyway, and keeps the negative tail's scale, where 1 + erf
-// cancels.  It takes 13 instructions, two of them quarter-rate, where erfc
-// takes about 40 (the epilogue of an 8192 x 4096 output is bound by them).
+// Phi(z) = sigmoid(z Q(z^2)) with Q the polynomial that comes nearest to
+// logit(Phi(z)) / z (a least-maximum fit, weighted by z Phi (1 - Phi), over z
+// in (0, 6.5]; it stays positive and grows beyond).  It keeps the negative
+// tail's scale, where 1 + erf cancels, and takes 10 or 13 instructions, two of
+// them quarter-rate, where erfc takes about 40; the passes over 8192 x 4096
+// values are bound by them.
+//   8 terms: off by at most 1.2e-7, two half steps of float32 at 1, which the
+//     rounding of the argument leaves anyway;
+//   5 terms: 1.5e-6, a hundredth of half a step of bfloat16 at 1, where the
+//     result is rounded to 16 bits.  In the backward pass only where it is
+//     rounded to bfloat16: there an error of 1.5e-6 moves one 8-bit mantissa
+//     of dZ in 10^4 by a step, which bfloat16 gradients hide and half
+//     precision ones do not.
+template <class T>
+constexpr int phi_terms(bool backward) {
+    return sizeof(T) == 4 || (backward && __is_same(T, f16)) ? 8 : 5;
+}
 
-constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluK = 1.59576912160573071f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLog2InvSqrt2Pi = -1.32574806473616f;  // log2(1 / sqrt(2 pi))
 
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// 1 / (1 + 2^x): the logistic function of -x ln 2
+__device__ __forceinline__ float logistic2(float x) { return __builtin_amdgcn_rcpf(1.0f + exp2_fast(x)); }
 // The factor z of a product with a vanishing one, kept finite: the limits at
 // z = -inf (0) and, in the derivatives, at +inf (1) come out instead of
 // inf * 0.  A NaN passes through the other factor.
 __device__ __forceinline__ float above(float z) { return fmaxf(z, -200.0f); }
 __device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -30.0f, 30.0f); }
 
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float sigmoid(float w) { return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2e * w)); }
-
-__device__ __forceinline__ float normal_cdf(float z) {
-    constexpr float c[8] = {1.5957697844099097e+00f * -kLog2e,  7.266674921058917e-02f * -kLog2e,
-                            -6.60603328097877e-05f * -kLog2e,   -1.1009835059468343e-04f * -kLog2e,
-                            7.788852044459863e-06f * -kLog2e,   -2.45761265691951e-07f * -kLog2e,
-                            2.3421368291093768e-09f * -kLog2e,  2.696477063689756e-11f * -kLog2e};
-    const float u = z * z;
-    float q = c[7];
+// Phi(z), u = z^2.
+template <int TERMS>
+__device__ __forceinline__ float normal_cdf(float z, float u) {
+    constexpr float c8[8] = {1.5957697844099097e+00f, 7.266674921058917e-02f,  -6.60603328097877e-05f, -1.1009835059468343e-04f,
+                             7.788852044459863e-06f,  -2.45761265691951e-07f, 2.3421368291093768e-09f, 2.696477063689756e-11f};
+    constexpr float c5[5] = {1.59573911e+00f, 7.27856189e-02f, -1.76439094e-04f, -7.32000513e-05f, 2.83706209e-06f};
+    float q = -kLog2e * (TERMS == 8 ? c8[7] : c5[4]);
 #pragma unroll
-    for (int i = 6; i >= 0; --i) q = fmaf(q, u, c[i]);
-    return __builtin_amdgcn_rcpf(1.0f + exp2_fast(z * q));
+    for (int i = TERMS - 2; i >= 0; --i) q = fmaf(q, u, -kLog2e * (TERMS == 8 ? c8[i] : c5[i < 5 ? i : 4]));
+    return logistic2(z * q);
 }
 
-template <int ACT>
+template <int ACT, int TERMS>
 __device__ __forceinline__ float act_value(float z) {
     if (ACT == IONN_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if (ACT == IONN_ACT_GELU) return above(z) * normal_cdf(z);
-    if (ACT == IONN_ACT_GELU_TANH) return above(z) * sigmoid(kGeluK * (z + kGeluC * z * z * z));
-    if (ACT == IONN_ACT_SILU) return above(z) * sigmoid(z);
+    if (ACT == IONN_ACT_GELU) return above(z) * normal_cdf<TERMS>(z, z * z);
+    if (ACT == IONN_ACT_GELU_TANH)
+        return above(z) * logistic2(z * fmaf(z * z, -kLog2e * kGeluK * kGeluC, -kLog2e * kGeluK));
+    if (ACT == IONN_ACT_SILU) return above(z) * logistic2(-kLog2e * z);
     return z;
 }
 
-template <int ACT>
+template <int ACT, int TERMS>
 __device__ __forceinline__ float act_grad(float z) {
     if (ACT == IONN_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    if (ACT == IONN_ACT_GELU) {
-        const float y = within(z);
-        return normal_cdf(z) + y * kInvSqrt2Pi * exp2_fast(-0.5f * kLog2e * (y * y));
+    if (ACT == IONN_ACT_GELU) {  // Phi + z phi
+        const float u = z * z;
+        return fmaf(within(z), exp2_fast(fmaf(u, -0.5f * kLog2e, kLog2InvSqrt2Pi)), normal_cdf<TERMS>(z, u));
     }
     if (ACT == IONN_ACT_GELU_TANH) {
-        const float y = within(z);
-        const float p = sigmoid(kGeluK * (z + kGeluC * z * z * z));
-        return p + y * p * (1.0f - p) * (kGeluK * (1.0f + 3.0f * kGeluC * y * y));
+        const float p = logistic2(z * fmaf(z * z, -kLog2e * kGeluK * kGeluC, -kLog2e * kGeluK)), y = within(z);
+        return fmaf(y * fmaf(y * y, 3.0f * kGeluK * kGeluC, kGeluK), p * (1.0f - p), p);
     }
     if (ACT == IONN_ACT_SILU) {
-        const float p = sigmoid(z);
-        return p * (1.0f + within(z) * (1.0f - p));
+        const float p = logistic2(-kLog2e * z);
+        return p * fmaf(within(z), 1.0f - p, 1.0f);
     }
     return 1.0f;
 }
@@ -158,11 +168,12 @@ __device__ __forceinline__ int dfp8_exponent(uint32_t m) {
     return (ex > 0 ? ex - 127 : -150 + bitlen_u32(m & 0x7fffffu)) - 6;
 }
 
-// sat8(rne(x / 2^E)), given -E in [-121, 155].  ldexp is exact here unless
-// its result is below 2^-126, which rounds to 0 as the exact one does.
-__device__ __forceinline__ int32_t dfp8_mantissa(float x, int negE) {
-    const float r = __builtin_rintf(__builtin_amdgcn_ldexpf(x, negE));
-    return int32_t(fminf(fmaxf(r, -128.0f), 127.0f));
+// sat8(rne(x / 2^E)) in the low byte, given -E in [-121, 155]: ldexp is exact
+// here unless its result is below 2^-126, which rounds to 0 as the exact one
+// does, and adding 1.5 * 2^23 rounds to an integer and leaves it in the low
+// bits.
+__device__ __forceinline__ uint32_t dfp8_mantissa(float x, int negE) {
+    return __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(x, negE), -128.0f, 127.0f) + 12582912.0f);
 }
 
 // 0, 1 (exponent outside the signed 8-bit range), 2 (not finite).
