@@ -1,14 +1,14 @@
-// Forward product of a few rows (tokens being generated, small batches):
-// bound by reading W once, so W goes straight from memory into matrix-core
-// operands and nothing of it through LDS (gfx950, v_mfma_i32_16x16x64_i8).
+// Forward product of up to 16 rows (tokens being generated): bound by reading
+// W once, so W goes straight from memory into matrix-core operands and nothing
+// of it through LDS (gfx950, v_mfma_i32_16x16x64_i8).
 //
 // A workgroup takes 16 outputs; its eight wavefronts split the reduction, each
 // with kDeep pieces of 16 rows x 64 bytes of W in flight, and their sums meet
 // in LDS.  At 1 x 4096 x 4096 that is 256 workgroups whose wavefronts load
-// all they need of W in one go: one trip to memory.  The weights are the
-// first operand, so a lane ends with four consecutive outputs of one row.
-// X is read by every workgroup, from L2: B bytes for each 16 of W, which is
-// what ends the path's advantage with growing B.
+// all they need of W in one go, one trip to memory: 5.9 us, of which a launch
+// in a graph is 3.3 and W's 16.8 MB at the rate of a copy 3.2; 1 x 4096 x 32768
+// reads W at 4.6 TB/s.  The weights are the first operand, so a lane ends with
+// four consecutive outputs of one row.
 #pragma once
 
 #include "dfp8_tile.h"
@@ -17,15 +17,15 @@ namespace ionn {
 namespace dfp8 {
 
 constexpr int kRowWaves = 8;
-constexpr int kRowsMax = 64;  // rows of X
+constexpr int kRowsMax = 16;  // rows of X
 constexpr int kRowsMinK = 16;
 
-// RB: groups of 16 rows of X (1, 2 or 4).  K >= 16.
-template <class T, int RB>
+// K >= 16.
+template <class T>
 __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__restrict__ X, const int8_t *__restrict__ W,
                                                               Epi ep, int M, int N, int K) {
-    constexpr int kDeep = RB == 4 ? 4 : 8;
-    __shared__ v4i sums[kRowWaves][RB][64];
+    constexpr int kDeep = 8;
+    __shared__ v4i sums[kRowWaves][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int n0 = int(blockIdx.x) * 16;
@@ -39,21 +39,14 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
     // only those no piece before it has counted.
     typedef v4i loose __attribute__((aligned(1)));
     const int8_t *w = W + int64_t(min(n0 + r, N - 1)) * K;
-    const int8_t *x[RB];
-#pragma unroll
-    for (int g = 0; g < RB; ++g) x[g] = X + int64_t(min(16 * g + r, M - 1)) * K;
-    v4i acc[RB];
-#pragma unroll
-    for (int g = 0; g < RB; ++g) acc[g] = v4i{0, 0, 0, 0};
+    const int8_t *x = X + int64_t(min(r, M - 1)) * K;
+    v4i acc = {0, 0, 0, 0};
     for (int k0 = k_begin; k0 < k_end; k0 += 64 * kDeep) {
-        v4i a[kDeep], b[kDeep][RB];
+        v4i a[kDeep], b[kDeep];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) a[d] = *reinterpret_cast<const loose *>(w + min(k0 + 64 * d + kl, K - 16));
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-            for (int g = 0; g < RB; ++g)
-                b[d][g] = *reinterpret_cast<const loose *>(x[g] + min(k0 + 64 * d + kl, K - 16));
+        for (int d = 0; d < kDeep; ++d) b[d] = *reinterpret_cast<const loose *>(x + min(k0 + 64 * d + kl, K - 16));
         if (k0 + 64 * kDeep > k_end || k0 + 64 * kDeep > K) {
 #pragma unroll
             for (int d = 0; d < kDeep; ++d) {
@@ -62,29 +55,23 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int p = past - 4 * i;
-                    const uint32_t keep = p <= 0 ? ~0u : (p >= 4 ? 0u : ~0u << (8 * p));
-#pragma unroll
-                    for (int g = 0; g < RB; ++g) b[d][g][i] &= int(keep);
+                    b[d][i] &= int(p <= 0 ? ~0u : (p >= 4 ? 0u : ~0u << (8 * p)));
                 }
             }
         }
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-            for (int g = 0; g < RB; ++g)
-                acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[d], b[d][g], acc[g], 0, 0, 0);
+        for (int d = 0; d < kDeep; ++d) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[d], b[d], acc, 0, 0, 0);
     }
-#pragma unroll
-    for (int g = 0; g < RB; ++g) sums[wave][g][lane] = acc[g];
+    sums[wave][lane] = acc;
     __syncthreads();
-    if (wave >= RB) return;
-    v4i s = sums[0][wave][lane];
+    if (wave > 0) return;
+    v4i s = sums[0][lane];
 #pragma unroll
-    for (int o = 1; o < kRowWaves; ++o) s += sums[o][wave][lane];
+    for (int o = 1; o < kRowWaves; ++o) s += sums[o][lane];
     const int e2 = *ep.ea + *ep.eb;
     uint32_t top = 0;
     with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
-        top = finish4<T, decltype(ac)::value, false>(s, ep, e2, 16 * wave + r, n0 + 4 * (lane >> 4), M, N);
+        top = finish4<T, decltype(ac)::value, false>(s, ep, e2, r, n0 + 4 * (lane >> 4), M, N);
     });
     if (ep.absmax) {
         top = wave_max_u32(top);
