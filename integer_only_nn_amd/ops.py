@@ -536,24 +536,62 @@ _FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 def _dtype(t, name):
     """The library's number of a floating tensor's type."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+    d = _FLOATS.get(getattr(t, "dtype", None))
+    if d is None:
         raise TypeError(f"{name}: expected a float32, bfloat16 or float16 tensor")
-    return _FLOATS[t.dtype]
+    return d
 
 
 # The calls below serve single tokens too, where the host's share of a call
-# counts: a tensor that is in order costs _a three attribute reads (_p, with a
-# message for what is not, the rest), and the current stream is read without
-# building a Stream object (0.1 against 1 us).
+# counts (a launch takes 2.8 us of it): a tensor that is in order costs _m or
+# _v a few attribute reads, _refuse has the messages, and the current stream
+# is read without building a Stream object.
 
-def _a(t, dtype=None, numel=0, name="tensor"):
-    """Address of a contiguous device tensor (None -> NULL)."""
+def _refuse(t, dtype, shape, name):
+    """Raises what is wrong with an argument."""
+    if isinstance(t, torch.Tensor):
+        have = t.numel() if isinstance(shape, int) else tuple(t.shape)
+        need = shape if isinstance(shape, int) else tuple(shape)
+        if have != need:
+            raise ValueError(f"shape mismatch: {name} has {have}, needs {need}")
+    _p(t, dtype, name=name)
+    raise ValueError(f"{name}: not accepted")
+
+
+def _m(t, dtype, shape, name):
+    """Address of a contiguous device tensor of this type and shape (None -> NULL)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype == dtype) and t.is_contiguous() and \
-            (numel == 0 or t.numel() >= numel):
-        return t.data_ptr()
-    return _p(t, dtype, numel, name).value
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, name)
+
+
+def _v(t, dtype, n, name):
+    """The same for a tensor of n elements in any shape."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, n, name)
+
+
+def _s(t, dtype, name):
+    """The same for a scalar held in a tensor of at least one element."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.numel() >= 1:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _p(t, dtype, 1, name).value
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -580,7 +618,9 @@ def _space(workspace):
     """Address and bytes of a workspace (None: NULL and 0)."""
     if workspace is None:
         return None, 0
-    return _a(workspace, name="workspace"), workspace.numel() * workspace.element_size()
+    if workspace.is_cuda and workspace.is_contiguous():
+        return workspace.data_ptr(), workspace.nbytes
+    return _p(workspace, name="workspace").value, workspace.nbytes
 
 
 def dfp8_from_float_workspace_bytes():
@@ -588,11 +628,12 @@ def dfp8_from_float_workspace_bytes():
 
 
 def dfp8_from_float(x, out, e_out, absmax=None, workspace=None, status_out=None, stream=None):
-    _same(x.numel() == out.numel(), "x and out")
-    check(lib().dfp8_from_float(_a(x, name="x"), _dtype(x, "x"), x.numel(), _a(absmax, u32, 1, "absmax"),
-                                _a(out, i8, name="out"), _a(e_out, i32, 1, "e_out"),
-                                _a(status_out, i32, 1, "status_out"), *_space(workspace), _on(stream, x)),
-          "dfp8_from_float")
+    ws, nws = _space(workspace)
+    rc = lib().dfp8_from_float(_v(x, x.dtype, x.numel(), "x"), _dtype(x, "x"), x.numel(), _s(absmax, u32, "absmax"),
+                               _v(out, i8, x.numel(), "out"), _s(e_out, i32, "e_out"),
+                               _s(status_out, i32, "status_out"), ws, nws, _on(stream, x))
+    if rc:
+        check(rc, "dfp8_from_float")
 
 
 def dfp8_linear_fwd_workspace_bytes(B, IN, OUT):
@@ -601,17 +642,17 @@ def dfp8_linear_fwd_workspace_bytes(B, IN, OUT):
 
 def dfp8_linear_fwd(X, eX, W, eW, Y, bias=None, act=0, residual=None, Z=None, absmax_Y=None, workspace=None,
                     stream=None):
-    B, IN = X.shape
+    xs, dt = X.shape, Y.dtype
+    B, IN = xs
     OUT = W.shape[0]
-    dt = Y.dtype
-    _same(W.shape == (OUT, IN) and Y.shape == (B, OUT), "X, W and Y")
-    _same((residual is None or residual.shape == (B, OUT)) and (Z is None or Z.shape == (B, OUT)) and
-          (bias is None or bias.numel() == OUT), "bias, residual and Z")
-    check(lib().dfp8_linear_fwd(_a(X, i8, name="X"), _a(eX, i32, 1, "eX"), _a(W, i8, name="W"), _a(eW, i32, 1, "eW"),
-                                _a(bias, f32, name="bias"), _act(act), _a(residual, dt, name="residual"),
-                                _a(Z, dt, name="Z"), _a(Y, name="Y"), _dtype(Y, "Y"), B, IN, OUT,
-                                _a(absmax_Y, u32, 1, "absmax_Y"), *_space(workspace), _on(stream, Y)),
-          "dfp8_linear_fwd")
+    ys = (B, OUT)
+    ws, nws = _space(workspace)
+    rc = lib().dfp8_linear_fwd(_m(X, i8, xs, "X"), _s(eX, i32, "eX"), _m(W, i8, (OUT, IN), "W"), _s(eW, i32, "eW"),
+                               _v(bias, f32, OUT, "bias"), _act(act), _m(residual, dt, ys, "residual"),
+                               _m(Z, dt, ys, "Z"), _m(Y, dt, ys, "Y"), _dtype(Y, "Y"), B, IN, OUT,
+                               _s(absmax_Y, u32, "absmax_Y"), ws, nws, _on(stream, Y))
+    if rc:
+        check(rc, "dfp8_linear_fwd")
 
 
 def dfp8_linear_bwd_workspace_bytes(B, IN, OUT):
@@ -621,30 +662,28 @@ def dfp8_linear_bwd_workspace_bytes(B, IN, OUT):
 def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None, workspace=None, status_out=None,
                     stream=None):
     """Z may be None for no activation; X and eX are read for G, W and eW for dX."""
-    B, OUT = dY.shape
+    ys, dt = dY.shape, dY.dtype
+    B, OUT = ys
     IN = (X if X is not None else W).shape[1]
-    dt = dY.dtype
-    _same((Z is None or Z.shape == (B, OUT)) and dZ8.shape == (B, OUT), "dY, Z and dZ8")
-    _same((X is None or X.shape == (B, IN)) and (W is None or W.shape == (OUT, IN)), "X and W")
-    _same((dX is None or dX.shape == (B, IN)) and (G is None or G.shape == (OUT, IN)) and
-          (gb is None or gb.numel() == OUT), "dX, G and gb")
-    check(lib().dfp8_linear_bwd(_a(dY, name="dY"), _a(Z, dt, name="Z"), _act(act), _dtype(dY, "dY"),
-                                _a(X, i8, name="X"), _a(eX, i32, 1, "eX"), _a(W, i8, name="W"), _a(eW, i32, 1, "eW"),
-                                _a(dZ8, i8, name="dZ8"), _a(edZ, i32, 1, "edZ"), _a(dX, dt, name="dX"),
-                                _a(G, dt, name="G"), _a(gb, f32, name="gb"), B, IN, OUT,
-                                _a(status_out, i32, 1, "status_out"), *_space(workspace), _on(stream, dY)),
-          "dfp8_linear_bwd")
+    xs, gs = (B, IN), (OUT, IN)
+    ws, nws = _space(workspace)
+    rc = lib().dfp8_linear_bwd(_m(dY, dt, ys, "dY"), _m(Z, dt, ys, "Z"), _act(act), _dtype(dY, "dY"),
+                               _m(X, i8, xs, "X"), _s(eX, i32, "eX"), _m(W, i8, gs, "W"), _s(eW, i32, "eW"),
+                               _m(dZ8, i8, ys, "dZ8"), _s(edZ, i32, "edZ"), _m(dX, dt, xs, "dX"), _m(G, dt, gs, "G"),
+                               _v(gb, f32, OUT, "gb"), B, IN, OUT, _s(status_out, i32, "status_out"), ws, nws,
+                               _on(stream, dY))
+    if rc:
+        check(rc, "dfp8_linear_bwd")
 
 
 def ionn_layer_norm_fwd(x, y, gamma=None, beta=None, eps=1e-5, mean=None, rstd=None, absmax_y=None, stream=None):
-    rows, cols = x.shape
-    _same(y.shape == (rows, cols) and (gamma is None or gamma.numel() == cols) and
-          (beta is None or beta.numel() == cols), "x, y, gamma and beta")
-    _same((mean is None or mean.numel() == rows) and (rstd is None or rstd.numel() == rows), "mean and rstd")
-    check(lib().ionn_layer_norm_fwd(_a(x, name="x"), _a(gamma, f32, name="gamma"), _a(beta, f32, name="beta"),
-                                    float(eps), _a(y, x.dtype, name="y"), _a(mean, f32, name="mean"),
-                                    _a(rstd, f32, name="rstd"), _dtype(x, "x"), rows, cols,
-                                    _a(absmax_y, u32, 1, "absmax_y"), _on(stream, x)), "ionn_layer_norm_fwd")
+    xs, dt = x.shape, x.dtype
+    rows, cols = xs
+    rc = lib().ionn_layer_norm_fwd(_m(x, dt, xs, "x"), _v(gamma, f32, cols, "gamma"), _v(beta, f32, cols, "beta"), eps,
+                                   _m(y, dt, xs, "y"), _v(mean, f32, rows, "mean"), _v(rstd, f32, rows, "rstd"),
+                                   _dtype(x, "x"), rows, cols, _s(absmax_y, u32, "absmax_y"), _on(stream, x))
+    if rc:
+        check(rc, "ionn_layer_norm_fwd")
 
 
 def ionn_layer_norm_bwd_workspace_bytes(rows, cols):
@@ -653,16 +692,15 @@ def ionn_layer_norm_bwd_workspace_bytes(rows, cols):
 
 def ionn_layer_norm_bwd(dy, x, mean, rstd, dx, gamma=None, dres=None, dgamma=None, dbeta=None, workspace=None,
                         stream=None):
-    rows, cols = x.shape
-    dt = x.dtype
-    _same(dy.shape == x.shape and dx.shape == x.shape and (dres is None or dres.shape == x.shape), "dy, x, dx and dres")
-    _same(mean.numel() == rows and rstd.numel() == rows, "mean and rstd")
-    _same(all(t is None or t.numel() == cols for t in (gamma, dgamma, dbeta)), "gamma, dgamma and dbeta")
-    check(lib().ionn_layer_norm_bwd(_a(dy, dt, name="dy"), _a(x, name="x"), _a(mean, f32, name="mean"),
-                                    _a(rstd, f32, name="rstd"), _a(gamma, f32, name="gamma"), _a(dres, dt, name="dres"),
-                                    _a(dx, dt, name="dx"), _a(dgamma, f32, name="dgamma"), _a(dbeta, f32, name="dbeta"),
-                                    _dtype(x, "x"), rows, cols, *_space(workspace), _on(stream, x)),
-          "ionn_layer_norm_bwd")
+    xs, dt = x.shape, x.dtype
+    rows, cols = xs
+    ws, nws = _space(workspace)
+    rc = lib().ionn_layer_norm_bwd(_m(dy, dt, xs, "dy"), _m(x, dt, xs, "x"), _v(mean, f32, rows, "mean"),
+                                   _v(rstd, f32, rows, "rstd"), _v(gamma, f32, cols, "gamma"),
+                                   _m(dres, dt, xs, "dres"), _m(dx, dt, xs, "dx"), _v(dgamma, f32, cols, "dgamma"),
+                                   _v(dbeta, f32, cols, "dbeta"), _dtype(x, "x"), rows, cols, ws, nws, _on(stream, x))
+    if rc:
+        check(rc, "ionn_layer_norm_bwd")
 
 
 def _state_ptrs(ts, bits, name):
@@ -684,9 +722,10 @@ def ionn_adamw_step(Ps, Gs, Ms, Vs, t, lr, beta1=0.9, beta2=0.999, eps=1e-8, wei
     _same(Ss is None or all(s.numel() == 2 * -(-p.numel() // ADAMW_BLOCK) for p, s in zip(Ps, Ss)), "S of a tensor")
     if L == 0:
         return
-    check(lib().ionn_adamw_step(L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
-                                _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"),
-                                None if Ss is None else _ptr_array(Ss, i8, "S"), bits, _sizes(Ps), int(t), float(lr),
-                                float(beta1), float(beta2), float(eps), float(weight_decay), _a(step, i32, 1, "step"),
-                                _a(lr_dev, f32, 1, "lr_dev"), _a(grad_scale, f32, 1, "grad_scale"),
-                                _a(absmax_P, u32, L, "absmax_P"), _on(stream, Ps[0])), "ionn_adamw_step")
+    rc = lib().ionn_adamw_step(L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
+                               _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"),
+                               None if Ss is None else _ptr_array(Ss, i8, "S"), bits, _sizes(Ps), int(t), lr, beta1,
+                               beta2, eps, weight_decay, _s(step, i32, "step"), _s(lr_dev, f32, "lr_dev"),
+                               _s(grad_scale, f32, "grad_scale"), _v(absmax_P, u32, L, "absmax_P"), _on(stream, Ps[0]))
+    if rc:
+        check(rc, "ionn_adamw_step")

@@ -510,11 +510,14 @@ class AdamW:
                 with torch.cuda.stream(on):
                     self.step_dev.add_(1)
         self.t += 1
-        ops.check(ops.lib().ionn_adamw_step(
+        rc = ops.lib().ionn_adamw_step(
             len(self.P), self._Pp, self._G[1], self._G[2], self._Mp, self._Vp, self._Sp, self._bits, self._n, self.t,
-            float(self.lr), float(self.betas[0]), float(self.betas[1]), float(self.eps), float(self.weight_decay),
-            ops._a(self.step_dev), ops._a(self.lr_dev), ops._a(grad_scale, torch.float32, 1, "grad_scale"),
-            ops._a(absmax_P, torch.int32, len(self.P), "absmax_P"), ops._on(stream, self.P[0])), "ionn_adamw_step")
+            self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+            ops._s(self.step_dev, torch.int32, "step"), ops._s(self.lr_dev, torch.float32, "lr_dev"),
+            ops._s(grad_scale, torch.float32, "grad_scale"), ops._v(absmax_P, torch.int32, len(self.P), "absmax_P"),
+            ops._on(stream, self.P[0]))
+        if rc:
+            ops.check(rc, "ionn_adamw_step")
 
 
 # ---------------------------------------------------------------------------

@@ -99,10 +99,18 @@ def test_binding_refuses_host_tensors_and_shapes():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError, match="device tensor"):
         ops.ionn_layer_norm_fwd(x, torch.empty_like(x))
-    with pytest.raises(ValueError, match="shape mismatch"):
-        ops.ionn_layer_norm_fwd(x, torch.empty(4, 7))
-    with pytest.raises(ValueError, match="shape mismatch"):
-        ops.dfp8_linear_fwd(x.to(torch.int8), None, torch.zeros(3, 7, dtype=torch.int8), None, torch.empty(4, 3))
+    for shape in ((4, 7), (8, 4)):
+        with pytest.raises(ValueError, match="shape mismatch: y has"):
+            ops._m(torch.empty(shape), torch.float32, x.shape, "y")
+    with pytest.raises(ValueError, match="shape mismatch: gamma has 7, needs 8"):
+        ops._v(torch.empty(7), torch.float32, 8, "gamma")
+    with pytest.raises(ValueError, match="device tensor"):
+        ops._v(torch.empty(8), torch.float32, 8, "gamma")
+    for get in (lambda t: ops._m(t, torch.float32, (8,), "y"), lambda t: ops._v(t, torch.float32, 8, "y"),
+                lambda t: ops._s(t, torch.float32, "y")):
+        assert get(None) is None
+        with pytest.raises(TypeError):
+            get([1.0] * 8)
     with pytest.raises(TypeError):
         ops._dtype(torch.zeros(3, dtype=torch.float64), "x")
     with pytest.raises(ValueError, match="shape mismatch"):

@@ -120,3 +120,21 @@ def test_refuses_weights_that_do_not_fit():
         opt.bind_grads([z(5)])
     with pytest.raises(TypeError):
         ops.ionn_adamw_step([z(4)], [z(4).double()], [z(4)], [z(4)], 1, 1e-3)
+
+
+def test_binding_refuses_wrong_tensors():
+    x = torch.zeros(4, 8, device=dev())
+    for y, error in ((torch.empty(4, 7, device=dev()), "shape mismatch"), (torch.empty(8, 4, device=dev()), "shape"),
+                     (torch.empty(4, 8), "device tensor"), (torch.empty(8, 4, device=dev()).t(), "contiguous")):
+        with pytest.raises(ValueError, match=error):
+            ops.ionn_layer_norm_fwd(x, y)
+    with pytest.raises(TypeError, match="bfloat16"):
+        ops.ionn_layer_norm_fwd(x, torch.empty(4, 8, dtype=torch.bfloat16, device=dev()))
+    i8 = lambda *s: torch.zeros(*s, dtype=torch.int8, device=dev())  # noqa: E731
+    e = torch.zeros(1, dtype=torch.int32, device=dev())
+    with pytest.raises(ValueError, match="W has"):
+        ops.dfp8_linear_fwd(i8(4, 8), e, i8(3, 7), e, torch.empty(4, 3, device=dev()))
+    with pytest.raises(TypeError, match="eX"):
+        ops.dfp8_linear_fwd(i8(4, 8), e.float(), i8(3, 8), e, torch.empty(4, 3, device=dev()))
+    with pytest.raises(ValueError, match="bias has"):
+        ops.dfp8_linear_fwd(i8(4, 8), e, i8(3, 8), e, torch.empty(4, 3, device=dev()), bias=torch.zeros(4, device=dev()))
