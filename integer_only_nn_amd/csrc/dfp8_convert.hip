@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void act_sums_kernel(const T *__restrict_
         auto add = [&](const typename Vec<T, VE>::type &y, const typename Vec<T, VE>::type &z) __attribute__((always_inline)) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[e]));
+                const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, kTermsGrad>(float(z[e]));
                 s[e] += d;
                 m = max(m, mag_bits(d));  // (past a row's end dY, and so d, is 0)
             }
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict
         uint32_t q[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[e]));
+            const float d = ACT == IONN_ACT_NONE ? float(y[e]) : float(y[e]) * act_grad<ACT, kTermsGrad>(float(z[e]));
             q[e] = dfp8_mantissa(d, -E);
         }
         store_bytes(dZ8 + i, q, VE, valid);
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kOneThreads) void act_one_kernel(const T *__restric
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                d[k][e] = ACT == IONN_ACT_NONE ? float(y[k][e]) : float(y[k][e]) * act_grad<ACT, phi_terms<T>(true)>(float(z[k][e]));
+                d[k][e] = ACT == IONN_ACT_NONE ? float(y[k][e]) : float(y[k][e]) * act_grad<ACT, kTermsGrad>(float(z[k][e]));
                 if (e >= valid) d[k][e] = 0.0f;
                 m = max(m, mag_bits(d[k][e]));
             }

@@ -204,7 +204,7 @@ __device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2,
     if (ep.z) store_vec<T, 4>(static_cast<T *>(ep.z) + at, z, valid);
     float o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = act_value<ACT, phi_terms<T>(false)>(z[i]);
+    for (int i = 0; i < 4; ++i) o[i] = act_value<ACT, kTermsValue<T>>(z[i]);
     if (ep.residual) {
         const auto r = load_raw<T, 4>(static_cast<const T *>(ep.residual) + at, valid);
 #pragma unroll
@@ -244,7 +244,7 @@ __device__ __forceinline__ uint32_t finish8(const v4i &lo, const v4i &hi, const 
     if (ep.z) store_vec<T, 8>(static_cast<T *>(ep.z) + at, z, valid);
     float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = act_value<ACT, phi_terms<T>(false)>(z[i]);
+    for (int i = 0; i < 8; ++i) o[i] = act_value<ACT, kTermsValue<T>>(z[i]);
     if (ep.residual) {
         const auto r = load_raw<T, 8>(static_cast<const T *>(ep.residual) + at, valid);
 #pragma unroll

@@ -75,15 +75,12 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[VE], int valid 
 // values are bound by them.
 //   8 terms: off by at most 1.2e-7, two half steps of float32 at 1, which the
 //     rounding of the argument leaves anyway;
-//   5 terms: 1.5e-6, a hundredth of half a step of bfloat16 at 1, where the
-//     result is rounded to 16 bits.  In the backward pass only where it is
-//     rounded to bfloat16: there an error of 1.5e-6 moves one 8-bit mantissa
-//     of dZ in 10^4 by a step, which bfloat16 gradients hide and half
-//     precision ones do not.
+//   5 terms: 1.5e-6, a hundredth of half a step of bfloat16 at 1, for values
+//     that are rounded to 16 bits.  Not for derivatives: their column sums
+//     are float32, and the fit's error does not average out in them.
+constexpr int kTermsGrad = 8;
 template <class T>
-constexpr int phi_terms(bool backward) {
-    return sizeof(T) == 4 || (backward && __is_same(T, f16)) ? 8 : 5;
-}
+constexpr int kTermsValue = sizeof(T) == 4 ? 8 : 5;
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluK = 1.59576912160573071f;  // 2 sqrt(2 / pi)
