@@ -7,11 +7,14 @@
 //   P = P (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps)
 //
 // Bound by HBM: per weight it reads P, g, m, v and writes P, m, v, 28 bytes
-// with float32 states and a float32 gradient, 12 + 1/32 + the gradient's
+// with float32 states and a float32 gradient, 12 + 1/64 + the gradient's
 // with 8-bit ones.  A wavefront takes 1024 weights as four chunks of 256, a
 // lane four consecutive ones of each, so that every access is a contiguous
 // run and a chunk is one 8-bit block: its largest magnitude is a reduction
-// inside the wavefront, and no state is read twice.
+// inside the wavefront, and no state is read twice.  Measured: 67.1 M weights
+// with 8-bit states and bfloat16 gradients 183 us (940 MB, 5.1 TB/s; a large
+// copy reaches 5.2); 20 tensors of 268 k weights with float32 states 6.2 us, one
+// launch.
 //
 // 8-bit states are E4M3 codes with one power-of-two exponent per block of
 // 256.  The second moment is kept as its root r = sqrt(v): E4M3 spans 2^18

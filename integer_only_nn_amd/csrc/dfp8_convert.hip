@@ -10,8 +10,11 @@
 // second pass computes the derivative again rather than read it back: a
 // float32 copy would cost 8 bytes per element where dY and Z cost 4 in the
 // 16-bit types.  Each workgroup of it reduces the first pass's maxima itself
-// (at most 4 KiB, from L2), which saves the launch, the cleared scalar and
-// the queue of atomics of a shared maximum.
+// (about 4 KiB, from L2), which saves the launch, the cleared scalar and the
+// queue of atomics of a shared maximum.  8192 x 4096 bfloat16 errors behind a
+// gelu: 41 and 33 us, 3.3 and 5.0 TB/s; the first is held up by its arithmetic
+// (22 instructions a value, three of them quarter-rate) as much as by memory:
+// neither four rows in flight nor twice the workgroups changed it.
 #include "dfp8_convert.h"
 
 namespace ionn {

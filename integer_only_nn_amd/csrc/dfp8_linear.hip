@@ -7,6 +7,13 @@
 //   z = fl(X W^T) 2^(eX + eW) + bias,  Y = act(z) + residual
 //   dZ = dY act'(Z) -> dZ8, edZ;  dX = fl(dZ8 W) 2^(edZ + eW),
 //   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
+//
+// The sums are exact in int32, so how a product is cut never shows in its
+// result.  Four ways, by the sizes (make_plan): up to 16 rows read W straight
+// into matrix operands (dfp8_rows.h); large products take 256 x 256 tiles
+// (dfp8_tile256.h); the others 64 x 64 tiles (dfp8_tile.h), a long reduction of
+// few tiles in ranges whose int32 sums a second pass adds, and contiguous
+// sides shorter than 16 bytes the same tiles with careful loads.
 #include "dfp8_convert.h"
 #include "dfp8_rows.h"
 #include "dfp8_tile256.h"

@@ -1,8 +1,14 @@
 // The large-product path of the DFP-8 Linear layer: 256 x 256 output tiles,
 // 128-deep K steps, loads straight into LDS, on the operand layouts, fragment
 // reads and issue order of gemm256.h, with a floating epilogue and with edges:
-// any M and N, any K of the K-major pair that is a multiple of 16 (row pitches
-// are, so that 16-byte pieces stay aligned), any K of the others.
+// any sizes whose row pitches are multiples of 16, so that 16-byte pieces stay
+// aligned.
+//
+// Bound by the matrix cores at the clock that their power leaves: 8192 x 4096
+// x 4096 takes 128 us as dX (2140 TOP/s) and 116 us as G (2370 TOP/s), where
+// the library's int8 product reaches 2030 TOP/s on 8192^3; forward with gelu and
+// z 148 us, the epilogue's arithmetic (20 instructions per output, one
+// wavefront per SIMD) not overlapping the products.
 //
 // Edges cost no branch.  Rows past a K-major operand's end and k past an
 // M-major one's lie past its buffer resource and come back as zeros; what a
@@ -19,7 +25,7 @@
 namespace ionn {
 namespace dfp8 {
 
-constexpr uint32_t kOut = 0x80000000u;  // past every resource, whatever is added
+constexpr uint32_t kOut = 0x80000000u;  // past every resource, also with an offset below 2^31 added
 
 // The per-lane offsets of one operand (TileSrc holds the resource, the pitch
 // and the wavefront's and lanes' positions).
@@ -53,8 +59,8 @@ struct EdgeSrc : g256::TileSrc<KMAJOR> {
 // read back eight columns a lane, so that a loop of a few hundred
 // instructions writes whole 128-byte lines of a 16-bit output.  Unrolled over
 // the registers the same epilogue was 60 KB of straight code per activation,
-// whose fetching took longer than its work (8192 x 4096 outputs with gelu and
-// z: 208 us for the product, against 130 without an epilogue).
+// whose fetching took longer than its work (8192 x 4096 x 4096 with gelu and z:
+// 208 us against 171 with the same arithmetic).
 template <class T, int ACT, bool LINEAR>
 __device__ __forceinline__ uint32_t finish_wave(const v16i (&acc)[4][4], int8_t *lds, const Epi &ep, int e2, int64_t m0,
                                                 int n0, int M, int N, int lane) {
@@ -224,10 +230,11 @@ __global__ __launch_bounds__(g256::NT, 1) void tile256_kernel(const int8_t *__re
 }
 
 // Whether tile256_kernel takes the product: 16-byte pieces that stay aligned,
-// and offsets that stay below 2^32 past a ragged tile's end.
+// offsets of a tensor's rows that stay below 2^31 with a step added, and of a
+// ragged tile's below 2^32.
 template <bool A_KM, bool B_KM>
 inline bool tile256_fits(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, int64_t M, int64_t N, int64_t K) {
-    const int64_t ab = (A_KM ? M : K) * lda, bb = (B_KM ? N : K) * ldb, lim = int64_t(1) << 31;
+    const int64_t ab = (A_KM ? M : K) * lda, bb = (B_KM ? N : K) * ldb, lim = (int64_t(1) << 31) - 1024;
     return K >= 1 && aligned(A, 16) && aligned(B, 16) && lda % 16 == 0 && ldb % 16 == 0 && ab < lim && bb < lim &&
            512 * lda < lim && 512 * ldb < lim && lda >= 256 && ldb >= 256;
 }

@@ -13,7 +13,11 @@
 // mean, which a one-pass form loses for a mean far from 0), and a thread keeps
 // the columns it owns from row to row: gamma, beta and the column sums of the
 // backward pass stay in its registers, and the sums leave as one partial row
-// per workgroup, added in a second, fixed-order pass.
+// per workgroup, added in a second, fixed-order pass.  The next row's loads are
+// in flight while a row is reduced (forward 40.6 us without, 8192 x 4096
+// bf16).  Measured: forward 8192 x 4096 bf16 27 us (5.0 TB/s, a large copy
+// reaches 5.2); backward 45 us and 5 for the second pass; 25088 x 256 float32
+// backward 15.4 and 3.9 us; one row of 4096 forward 3.1 us.
 #include "float_ops.h"
 
 namespace ionn {
