@@ -350,13 +350,19 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
     const int M = p.M, N = p.N;
-    const int tiles = p.blocks / p.split, range = id / tiles;
+    // the range of K (scalar divisions cost tens of instructions each: only
+    // where there are ranges)
+    int range = 0, tile = id, k_begin = 0, k_end = p.K;
+    if (p.split > 1) {
+        const uint32_t tiles = uint32_t(p.blocks) / uint32_t(p.split), steps = uint32_t(p.K + BK - 1) / BK;
+        range = int(uint32_t(id) / tiles);
+        tile = id - range * int(tiles);
+        k_begin = int(steps * uint32_t(range) / uint32_t(p.split)) * BK;  // steps <= 1024, split <= 32
+        k_end = min(p.K, int(steps * uint32_t(range + 1) / uint32_t(p.split)) * BK);
+    }
     int tm, tn;
-    gemm::tile_coords(id - range * tiles, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+    gemm::tile_coords(tile, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int steps = (p.K + BK - 1) / BK;
-    const int k_begin = int(int64_t(steps) * range / p.split) * BK;
-    const int k_end = min(p.K, int(int64_t(steps) * (range + 1) / p.split) * BK);
     v16i acc[FM][FN];
     tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(p.A, p.lda, p.B, p.ldb, M, N, m0, n0, k_begin, k_end, lds, wm, wn, lane,
                                                acc);
@@ -444,13 +450,15 @@ __global__ __launch_bounds__(NT) void tile_pair_kernel(Product d, Product g) {
 }
 
 // The sums of the ranges through the epilogue, four columns of a row per
-// thread; element `id` of the product's M * ceil(N / 4).
+// thread; element `id` of the product's M * ceil(N / 4) (below 2^31: only
+// products of few tiles are cut into ranges).
 template <class T, bool LINEAR>
-__device__ __forceinline__ void sum_ranges(const Product &p, int64_t id) {
+__device__ __forceinline__ void sum_ranges(const Product &p, uint32_t id) {
     typedef v4i loose __attribute__((aligned(4)));
-    const int n4 = (p.N + 3) / 4;
-    const int64_t m = id / n4;
-    const int n = 4 * int(id - m * n4);
+    const uint32_t n4 = uint32_t(p.N + 3) / 4;
+    const uint32_t row = id / n4;
+    const int n = 4 * int(id - row * n4);
+    const int64_t m = row;
     uint32_t top = 0;
     if (m < p.M) {
         const int32_t *at = p.part + m * p.N + n;
@@ -478,15 +486,15 @@ __device__ __forceinline__ void sum_ranges(const Product &p, int64_t id) {
 
 template <class T, bool LINEAR>
 __global__ __launch_bounds__(NT) void sum_kernel(Product p) {
-    sum_ranges<T, LINEAR>(p, int64_t(blockIdx.x) * NT + threadIdx.x);
+    sum_ranges<T, LINEAR>(p, blockIdx.x * NT + threadIdx.x);
 }
 
 // The same for the two products of a backward pass (workgroups of the first,
 // d_groups of them, then the second's).
 template <class T>
 __global__ __launch_bounds__(NT) void sum_pair_kernel(Product d, Product g, int d_groups) {
-    if (int(blockIdx.x) < d_groups) sum_ranges<T, true>(d, int64_t(blockIdx.x) * NT + threadIdx.x);
-    else sum_ranges<T, true>(g, int64_t(int(blockIdx.x) - d_groups) * NT + threadIdx.x);
+    if (int(blockIdx.x) < d_groups) sum_ranges<T, true>(d, blockIdx.x * NT + threadIdx.x);
+    else sum_ranges<T, true>(g, (blockIdx.x - uint32_t(d_groups)) * NT + threadIdx.x);
 }
 
 }  // namespace dfp8
