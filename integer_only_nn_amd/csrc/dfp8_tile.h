@@ -18,11 +18,11 @@
 // A's values past K become 0.  Pieces start at whatever byte they start on,
 // so odd sizes cost a shift in the last piece and no byte-wise path.
 //
-// Bound by the trip to memory where there are few steps (256 x 784 x 256: 5.8 us,
-// 3.3 of them a launch in a graph; 512^3 4.7 us) and by the 64 bytes a clock
-// that a compute unit loads where there are many tiles (1000 x 1024 x 2048 9.0
+// Bound by the trip to memory where there are few steps (256 x 784 x 256: 5.4 us,
+// 3.3 of them a launch in a graph; 512^3 4.3 us) and by the 64 bytes a clock
+// that a compute unit loads where there are many tiles (1000 x 1024 x 2048 8.4
 // us; pieces off their 16 bytes and a last column of tiles for one output,
-// 1000 x 1023 x 2049, 15 us).  128 x 128 tiles halve those bytes but leave half
+// 1000 x 1023 x 2049, 15.6 us).  128 x 128 tiles halve those bytes but leave half
 // the compute units without work at these sizes: 17 and 22 us.
 //
 // LDS layouts, without bank conflicts in either direction:
@@ -187,11 +187,21 @@ __device__ __forceinline__ v4i read_frag(const int8_t *lds, int rw, int sl, int 
     return out;
 }
 
-// Four sums of row m, columns n .. n + 3, through the epilogue; returns the
-// largest magnitude's bits of y (of the columns that exist).  LINEAR: no
-// bias, activation, residual or z (the gradients' products).
+// The bias of columns n .. n + V - 1 (zeros without one, or past N).
+template <int V>
+__device__ __forceinline__ void load_bias(const Epi &ep, int n, int N, float (&b)[V]) {
+    const auto raw = load_raw<float, V>(ep.bias + n, ep.bias ? N - n : 0);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = raw[i];
+}
+
+// Four sums of row m, columns n .. n + 3, through the epilogue (b: the
+// columns' bias); returns the largest magnitude's bits of y (of the columns
+// that exist).  LINEAR: no bias, activation, residual or z (the gradients'
+// products).
 template <class T, int ACT, bool LINEAR>
-__device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2, int64_t m, int n, int M, int N) {
+__device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2, const float (&b)[4], int64_t m, int n,
+                                            int M, int N) {
     if (m >= M || n >= N) return 0u;
     const int valid = N - n;
     float z[4];
@@ -203,11 +213,8 @@ __device__ __forceinline__ uint32_t finish4(const v4i &s, const Epi &ep, int e2,
         store_vec<T, 4>(y, z, valid);
         return 0u;
     }
-    if (ep.bias) {
-        const auto b = load_raw<float, 4>(ep.bias + n, valid);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += b[i];
-    }
+    for (int i = 0; i < 4; ++i) z[i] += b[i];
     if (ep.z) store_vec<T, 4>(static_cast<T *>(ep.z) + at, z, valid);
     float o[4];
 #pragma unroll
@@ -384,8 +391,8 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
                     v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
             }
     __syncthreads();
-    const int c = 2 * (int(threadIdx.x) % (BN / 8)), n = n0 + 4 * c;
-    constexpr int kRows = NT / (BN / 8);  // rows finished at once
+    const int c = 2 * (int(threadIdx.x) % (BN / 8)), n = n0 + 4 * c;  // the thread's eight columns
+    constexpr int kRows = NT / (BN / 8);                              // rows finished at once
     if (p.split > 1) {
         typedef v4i loose __attribute__((aligned(4)));
         int32_t *part = p.part + int64_t(range) * M * N;
@@ -412,11 +419,7 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
     const Epi &ep = p.ep;
     const int e2 = *ep.ea + *ep.eb;
     float bias[8] = {};
-    if (!LINEAR && ep.bias) {
-        const auto raw = load_raw<float, 8>(ep.bias + n, N - n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = raw[i];
-    }
+    if (!LINEAR) load_bias(ep, n, N, bias);
     uint32_t top = 0;
     with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
 #pragma unroll
@@ -474,8 +477,10 @@ __device__ __forceinline__ void sum_ranges(const Product &p, uint32_t id) {
                     if (n + e < p.N) s[e] += at[r * step + e];
         }
         const int e2 = *p.ep.ea + *p.ep.eb;
+        float bias[4] = {};
+        if (!LINEAR) load_bias(p.ep, n, p.N, bias);
         with_act(LINEAR ? int(IONN_ACT_NONE) : p.ep.act, [&](auto ac) __attribute__((always_inline)) {
-            top = finish4<T, decltype(ac)::value, LINEAR>(s, p.ep, e2, m, n, p.M, p.N);
+            top = finish4<T, decltype(ac)::value, LINEAR>(s, p.ep, e2, bias, m, n, p.M, p.N);
         });
     }
     if (!LINEAR && p.ep.absmax) {

@@ -80,11 +80,7 @@ __device__ __forceinline__ uint32_t finish_wave(const v16i (&acc)[4][4], int8_t 
                 }
         const int c = 2 * (lane & 7), n = n0 + 64 * h + 8 * (lane & 7);
         float b[8] = {};
-        if (!LINEAR && ep.bias) {
-            const auto raw = load_raw<float, 8>(ep.bias + n, N - n);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = raw[i];
-        }
+        if (!LINEAR) load_bias(ep, n, N, b);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the wavefront's own writes
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 2
