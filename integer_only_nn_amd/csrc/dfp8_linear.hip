@@ -9,11 +9,12 @@
 //   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
 //
 // The sums are exact in int32, so how a product is cut never shows in its
-// result.  Four ways, by the sizes (make_plan): up to 16 rows read W straight
-// into matrix operands (dfp8_rows.h); large products take 256 x 256 tiles
-// (dfp8_tile256.h); the others 64 x 64 tiles (dfp8_tile.h), a long reduction of
-// few tiles in ranges whose int32 sums a second pass adds, and contiguous
-// sides shorter than 16 bytes the same tiles with careful loads.
+// result.  Four ways, by the sizes (make_plan): a forward product of few rows
+// or few outputs, the reduction cut among a workgroup's wavefronts
+// (dfp8_rows.h); large products in 256 x 256 tiles (dfp8_tile256.h); the others
+// in 64 x 64 tiles (dfp8_tile.h), a long reduction of few tiles in ranges whose
+// int32 sums a second pass adds, and contiguous sides shorter than 16 bytes
+// in the same tiles with careful loads.
 #include "dfp8_convert.h"
 #include "dfp8_rows.h"
 #include "dfp8_tile256.h"
@@ -37,6 +38,7 @@ struct Plan {
     Path path;
     int64_t tiles;
     int split;
+    int rows, cols;  // ROWS: groups of 16 rows and of 16 outputs in a workgroup
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -45,15 +47,33 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // address does not suit TILE256 take TILE.
 template <bool A_KM, bool B_KM>
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
-    Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1};
+    Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1, 0, 0};
     const int64_t a_side = A_KM ? K : M, b_side = B_KM ? K : N;  // contiguous
-    // up to 16 rows; not few outputs over a reduction of many trips to memory
-    // (16 x 16384 -> 256: 16 us against 9.5 in tiles cut along the reduction;
-    // 32 rows x 4096 -> 4096: 8.5 against 10.9 us, but 53 against 37 at 32768
-    // outputs and 7.7 against 5.4 at 1024 x 1024)
-    if (forward && M <= kRowsMax && K >= kRowsMinK && (K <= 8192 || N >= 2048)) {
-        p.path = ROWS;
-        return p;
+    // Straight into matrix operands: the smallest tile that a grid of one
+    // workgroup per compute unit covers, for these products are bound by one
+    // trip after another of the longest workgroup (in tiles of 64, 256 x 784 x
+    // 256 takes 5.4 us against 2.7, 512 x 1024 x 1024 5.7 against 4.4).  A long
+    // reduction is better cut between workgroups (K = 32768, 32 rows, 64
+    // outputs: 14.3 us here, 9.5 in tiles; 256 x 12000 x 1000 18.5 and 16.6; but
+    // 32 x 16384 x 256 8.6 and 9.5), a short one leaves the largest tile no
+    // lead (512 x 256 x 1024: 3.7 us both).  Few rows against many outputs are
+    // bound by reading W, here too: 32 x 4096 x 16384 20 against 24.5 us, but
+    // 37.6 and 37.7 at 32768 outputs; for up to 8 rows a second group of
+    // outputs is no gain (8 x 1024 x 65536 14.1 against 16.4 us; 16 x 4096 x
+    // 16384 18.7 against 16.9).
+    if (forward && K >= kRowsMinK) {
+        const auto fits = [&](int rows, int cols) { return ceil_div(M, 16 * rows) * ceil_div(N, 16 * cols) <= 256; };
+        if (K <= 16384 && fits(1, 1)) p.rows = 1, p.cols = 1;
+        else if (K <= 16384 && fits(1, 2)) p.rows = 1, p.cols = 2;
+        else if (K <= 8192 && fits(2, 2)) p.rows = 2, p.cols = 2;
+        else if (K <= 8192 && K >= 512 && fits(4, 2)) p.rows = 4, p.cols = 2;
+        else if (M <= 8 && N > 4096) p.rows = 1, p.cols = 1;
+        else if (M <= 16 && K <= 16384) p.rows = 1, p.cols = 2;
+        else if (M <= 32 && K <= 16384 && N <= 16384) p.rows = 2, p.cols = 2;
+        if (p.rows) {
+            p.path = ROWS;
+            return p;
+        }
     }
     if (a_side < 16 || b_side < 16) {
         p.path = TINY;
@@ -117,7 +137,10 @@ template <class T>
 void launch_forward(const Plan &pl, Product p, hipStream_t st) {
     const Path path = path_of(pl, p.A, p.B);
     if (path == ROWS) {
-        rows_kernel<T><<<dim3(unsigned(ceil_div(p.N, 16))), dim3(kRowWaves * 64), 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
+        if (pl.rows == 1 && pl.cols == 1) launch_rows<T, 1, 1>(p, st);
+        else if (pl.rows == 1) launch_rows<T, 1, 2>(p, st);
+        else if (pl.rows == 2) launch_rows<T, 2, 2>(p, st);
+        else launch_rows<T, 4, 2>(p, st);
     } else if (path == TILE256) {
         launch_tile256<T, true, true, false>(p, st);
     } else {

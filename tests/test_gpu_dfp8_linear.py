@@ -116,6 +116,22 @@ def test_forward_larger(B, IN, OUT, name, kind):
     _check_forward(_case(B, IN, OUT, name, bias=name != "f16", residual=name != "f32"), kind, name)
 
 
+@pytest.mark.parametrize("B,IN,OUT", [
+    # reductions that end in each of a wavefront's trips and inside a piece
+    (16, 16, 16), (17, 17, 15), (1, 63, 33), (5, 65, 47), (16, 1023, 300), (20, 1025, 100), (1, 2047, 70), (15, 2049, 31),
+    (3, 3071, 64), (9, 3100, 50), (2, 16384, 20), (16, 16383, 300), (4, 16385, 50),
+    # groups of rows and outputs, whole and cut, around one workgroup per compute unit
+    (256, 784, 256), (250, 785, 250), (257, 256, 255), (40, 520, 2100), (129, 1030, 1025), (130, 4097, 1000),
+    (513, 1024, 1000), (500, 511, 1024), (500, 513, 1030), (70, 8192, 3000), (65, 8193, 3000),
+    # few rows, many outputs
+    (1, 48, 8200), (8, 100, 9001), (9, 100, 9001), (16, 2050, 8300), (17, 300, 12000), (32, 1100, 16384), (31, 70, 16385),
+    # tiles of 64 cut along the reduction
+    (33, 16500, 70), (300, 9001, 600), (600, 130, 900)])
+@pytest.mark.parametrize("name,kind", [("f32", "gelu_tanh"), ("bf16", "silu"), ("f16", "relu")])
+def test_forward_ways_of_cutting(B, IN, OUT, name, kind):
+    _check_forward(_case(B, IN, OUT, name, bias=name != "bf16", residual=name != "f16"), kind, name)
+
+
 def test_forward_longest_reduction():
     """The largest sum that fits int32: IN = 131071 products of -128 * -128."""
     IN = 131071
