@@ -9,15 +9,15 @@
 //   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
 //
 // The sums are exact in int32, so how a product is cut never shows in its
-// result.  Four ways, by the sizes (make_plan): a forward product of few rows
+// result.  Five ways, by the sizes (make_plan): a forward product of few rows
 // or few outputs, the reduction cut among a workgroup's wavefronts
-// (dfp8_rows.h); large products in 256 x 256 tiles (dfp8_tile256.h); the others
-// in 64 x 64 tiles (dfp8_tile.h), a long reduction of few tiles in ranges whose
-// int32 sums a second pass adds, and contiguous sides shorter than 16 bytes
-// in the same tiles with careful loads.
+// (dfp8_rows.h); large and middle products in 256 x 256 and 128 x 128 tiles
+// (dfp8_tile256.h, dfp8_tile128.h); the others in 64 x 64 tiles (dfp8_tile.h), a
+// long reduction of few tiles in ranges whose int32 sums a second pass adds, and
+// contiguous sides shorter than 16 bytes in the same tiles with careful loads.
 #include "dfp8_convert.h"
 #include "dfp8_rows.h"
-#include "dfp8_tile256.h"
+#include "dfp8_tile128.h"
 
 namespace ionn {
 namespace {
@@ -32,7 +32,7 @@ bool sizes_ok(int64_t B, int64_t IN, int64_t OUT) {
 
 // ---- how a product is cut ------------------------------------------------------
 
-enum Path { ROWS, TILE256, TILE, TINY };
+enum Path { ROWS, TILE256, TILE128, TILE, TINY };
 
 struct Plan {
     Path path;
@@ -44,7 +44,7 @@ struct Plan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // By the sizes alone (the workspace query knows no addresses); operands whose
-// address does not suit TILE256 take TILE.
+// address does not suit TILE256 and TILE128 take TILE.
 template <bool A_KM, bool B_KM>
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
     Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1, 0, 0};
@@ -79,19 +79,25 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
         p.path = TINY;
         return p;
     }
-    const int64_t lda = A_KM ? K : M, ldb = B_KM ? K : N;
-    // 256 x 256 tiles where their rounds of one per compute unit are expected
-    // to end first.  In us, fitted to measurements: a round takes 20 (12
-    // without an activation) and K / 120, the 64 x 64 kernel 8 and its share of
-    // M N K.  64 tiles of 256 at K = 2048: 37 against 23 us forward; 128 at K =
-    // 4096: 55 against 67; 64 at K = 8192, no activation: 80 against 88.
-    const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256);
-    const double rounds = double(ceil_div(tiles256, 256)), work = double(M) * double(N) * double(K) / 65536.0;
-    const bool large = rounds * ((forward ? 20.0 : 12.0) + double(K) / 120.0) < 8.0 + work / (forward ? 8850.0 : 6900.0);
-    if (large && tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
-        p.path = TILE256;
-        p.tiles = tiles256;
-        return p;
+    const int64_t lda = a_side, ldb = b_side;
+    // The tile size that is expected to end first; in us, fitted to
+    // measurements: a round of 256 x 256 tiles, one per compute unit, takes 23 (15
+    // without an activation) and K / 110; 128 x 128 tiles, two at a time on a
+    // compute unit, by the tiles that one gets; 64 x 64 tiles by the share of M N K.
+    // Forward in tiles of 64, 128 and 256: 1000 x 1024 x 2048 8.3, 11.2 and 26 us;
+    // 2048^3 22.5, 17.6 and 35; 2048 x 4096 x 4096 67, 42 and 54; 4096^3 128, 78
+    // and 70.  With both gradients: 512^3 12, 19 and 35; 4096 x 1024 x 4096 110, 81
+    // and 121.
+    if (tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
+        const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256), tiles128 = ceil_div(M, 128) * ceil_div(N, 128);
+        const double rounds = double(ceil_div(tiles256, 256)), each = double(ceil_div(tiles128, 256)), k = double(K);
+        const double t64 = (forward ? 5.0 : 2.5) + double(M) * double(N) * k / 65536.0 / (forward ? 6800.0 : 6500.0);
+        const double t128 = forward ? 3.5 + 2.6 * each + k * (0.0022 + 0.0031 * each)
+                                    : 2.5 + 1.8 * each + k * (0.0018 + 0.0031 * each);
+        const double t256 = rounds * ((forward ? 23.0 : 15.0) + k / 110.0);
+        if (t256 < t64 && t256 < t128) p.path = TILE256;
+        else if (t128 < t64) p.path = TILE128;
+        if (p.path != TILE) return p;
     }
     // few tiles over a long reduction: ranges of at least four steps, about
     // two workgroups per compute unit
@@ -123,12 +129,20 @@ void launch_tile256(const Product &p, hipStream_t st) {
         p.K);
 }
 
-// The path a planned product takes with these operands.
-Path path_of(const Plan &pl, const int8_t *A, const int8_t *B) {
-    return pl.path == TILE256 && !(aligned(A, 16) && aligned(B, 16)) ? TILE : pl.path;
+template <class T, bool A_KM, bool B_KM, bool LINEAR>
+void launch_tile128(const Product &p, hipStream_t st) {
+    const int64_t tiles = ceil_div(p.M, 128) * ceil_div(p.N, 128);
+    tile128_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(
+        p.A, p.lda, p.B, p.ldb, uint32_t((A_KM ? p.M : p.K) * p.lda), uint32_t((B_KM ? p.N : p.K) * p.ldb), p.ep, p.M, p.N,
+        p.K);
 }
 
-// (a TILE256 plan that falls back to 64 x 64 tiles has that many of them)
+// The path a planned product takes with these operands.
+Path path_of(const Plan &pl, const int8_t *A, const int8_t *B) {
+    return (pl.path == TILE256 || pl.path == TILE128) && !(aligned(A, 16) && aligned(B, 16)) ? TILE : pl.path;
+}
+
+// (a plan of larger tiles that falls back to 64 x 64 tiles has that many of them)
 void as_tiles(Product &p) { p.blocks = int(ceil_div(p.M, 64) * ceil_div(p.N, 64) * p.split); }
 
 unsigned sum_groups(const Product &p) { return unsigned(ceil_div(int64_t(p.M) * ceil_div(p.N, 4), NT)); }
@@ -143,6 +157,8 @@ void launch_forward(const Plan &pl, Product p, hipStream_t st) {
         else launch_rows<T, 4, 2>(p, st);
     } else if (path == TILE256) {
         launch_tile256<T, true, true, false>(p, st);
+    } else if (path == TILE128) {
+        launch_tile128<T, true, true, false>(p, st);
     } else {
         as_tiles(p);
         const dim3 grid(unsigned(p.blocks)), block(NT);
@@ -159,8 +175,16 @@ void launch_backward(const Plan &pd, Product d, const Plan &pg, Product g, hipSt
         launch_tile256<T, true, false, true>(d, st);
         d.blocks = 0;
     }
+    if (d.blocks && path_of(pd, d.A, d.B) == TILE128) {
+        launch_tile128<T, true, false, true>(d, st);
+        d.blocks = 0;
+    }
     if (g.blocks && path_of(pg, g.A, g.B) == TILE256) {
         launch_tile256<T, false, false, true>(g, st);
+        g.blocks = 0;
+    }
+    if (g.blocks && path_of(pg, g.A, g.B) == TILE128) {
+        launch_tile128<T, false, false, true>(g, st);
         g.blocks = 0;
     }
     const dim3 block(NT);

@@ -126,7 +126,9 @@ def test_forward_larger(B, IN, OUT, name, kind):
     # few rows, many outputs
     (1, 48, 8200), (8, 100, 9001), (9, 100, 9001), (16, 2050, 8300), (17, 300, 12000), (32, 1100, 16384), (31, 70, 16385),
     # tiles of 64 cut along the reduction
-    (33, 16500, 70), (300, 9001, 600), (600, 130, 900)])
+    (33, 16500, 70), (300, 9001, 600), (600, 130, 900),
+    # tiles of 128, whole and cut, reductions that end inside a step
+    (2040, 1040, 2032), (2047, 2064, 1936), (4090, 1296, 4080), (2048, 1024, 2048)])
 @pytest.mark.parametrize("name,kind", [("f32", "gelu_tanh"), ("bf16", "silu"), ("f16", "relu")])
 def test_forward_ways_of_cutting(B, IN, OUT, name, kind):
     _check_forward(_case(B, IN, OUT, name, bias=name != "bf16", residual=name != "f16"), kind, name)
@@ -251,6 +253,13 @@ def test_backward(B, IN, OUT, name):
                                       (2051, 2320, 2080), (2305, 2048, 272)])
 @pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "gelu"), ("f16", "silu")])
 def test_backward_larger(B, IN, OUT, name, kind):
+    _check_backward(_backward(B, IN, OUT, kind, name), kind, name)
+
+
+@pytest.mark.parametrize("B,IN,OUT", [(2040, 2032, 1040), (517, 4080, 4064), (1029, 4080, 4064), (2048, 2048, 1024)])
+@pytest.mark.parametrize("name,kind", [("f32", "none"), ("bf16", "relu"), ("f16", "gelu")])
+def test_backward_in_tiles_of_128(B, IN, OUT, name, kind):
+    """Both gradients, one of them, cut tiles and a batch that ends inside a step."""
     _check_backward(_backward(B, IN, OUT, kind, name), kind, name)
 
 
