@@ -87,7 +87,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
     // Forward in tiles of 64, 128 and 256: 1000 x 1024 x 2048 8.3, 11.2 and 26 us;
     // 2048^3 22.5, 17.6 and 35; 2048 x 4096 x 4096 67, 42 and 54; 4096^3 128, 78
     // and 70.  With both gradients: 512^3 12, 19 and 35; 4096 x 1024 x 4096 110, 81
-    // and 121.
+    // (74 in one grid) and 121.
     if (tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
         const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256), tiles128 = ceil_div(M, 128) * ceil_div(N, 128);
         const double rounds = double(ceil_div(tiles256, 256)), each = double(ceil_div(tiles128, 256)), k = double(K);
@@ -129,13 +129,7 @@ void launch_tile256(const Product &p, hipStream_t st) {
         p.K);
 }
 
-template <class T, bool A_KM, bool B_KM, bool LINEAR>
-void launch_tile128(const Product &p, hipStream_t st) {
-    const int64_t tiles = ceil_div(p.M, 128) * ceil_div(p.N, 128);
-    tile128_kernel<T, A_KM, B_KM, LINEAR><<<dim3(unsigned(tiles)), dim3(NT), 0, st>>>(
-        p.A, p.lda, p.B, p.ldb, uint32_t((A_KM ? p.M : p.K) * p.lda), uint32_t((B_KM ? p.N : p.K) * p.ldb), p.ep, p.M, p.N,
-        p.K);
-}
+void as_tiles128(Product &p) { p.blocks = int(ceil_div(p.M, 128) * ceil_div(p.N, 128)); }
 
 // The path a planned product takes with these operands.
 Path path_of(const Plan &pl, const int8_t *A, const int8_t *B) {
@@ -158,7 +152,8 @@ void launch_forward(const Plan &pl, Product p, hipStream_t st) {
     } else if (path == TILE256) {
         launch_tile256<T, true, true, false>(p, st);
     } else if (path == TILE128) {
-        launch_tile128<T, true, true, false>(p, st);
+        as_tiles128(p);
+        tile128_kernel<T><<<dim3(unsigned(p.blocks)), dim3(NT), 0, st>>>(p);
     } else {
         as_tiles(p);
         const dim3 grid(unsigned(p.blocks)), block(NT);
@@ -175,19 +170,22 @@ void launch_backward(const Plan &pd, Product d, const Plan &pg, Product g, hipSt
         launch_tile256<T, true, false, true>(d, st);
         d.blocks = 0;
     }
-    if (d.blocks && path_of(pd, d.A, d.B) == TILE128) {
-        launch_tile128<T, true, false, true>(d, st);
-        d.blocks = 0;
-    }
     if (g.blocks && path_of(pg, g.A, g.B) == TILE256) {
         launch_tile256<T, false, false, true>(g, st);
         g.blocks = 0;
     }
-    if (g.blocks && path_of(pg, g.A, g.B) == TILE128) {
-        launch_tile128<T, false, false, true>(g, st);
-        g.blocks = 0;
-    }
     const dim3 block(NT);
+    const bool d128 = d.blocks && path_of(pd, d.A, d.B) == TILE128, g128 = g.blocks && path_of(pg, g.A, g.B) == TILE128;
+    if (d128 || g128) {
+        Product d2 = d, g2 = g;
+        as_tiles128(d2);
+        as_tiles128(g2);
+        if (!d128) d2.blocks = 0;
+        if (!g128) g2.blocks = 0;
+        tile128_pair_kernel<T><<<dim3(unsigned(d2.blocks) + unsigned(g2.blocks)), block, 0, st>>>(d2, g2);
+        if (d128) d.blocks = 0;
+        if (g128) g.blocks = 0;
+    }
     if (d.blocks && pd.path == TINY) {
         tile_kernel<T, 64, 64, 2, true, false, true, true><<<dim3(unsigned(d.blocks)), block, 0, st>>>(d);
         d.blocks = 0;

@@ -78,22 +78,22 @@ __device__ __forceinline__ void wait_and_meet() {
 constexpr int kStages = 2;
 constexpr int kStage128 = 2 * 128 * BK;
 
+// Tile id of a product.
 template <class T, bool A_KM, bool B_KM, bool LINEAR>
-__global__ __launch_bounds__(NT) void tile128_kernel(const int8_t *__restrict__ A, int64_t lda,
-                                                     const int8_t *__restrict__ B, int64_t ldb, uint32_t a_bytes,
-                                                     uint32_t b_bytes, Epi ep, int M, int N, int K) {
-    __shared__ __attribute__((aligned(1024))) int8_t lds[kStages * kStage128];
+__device__ __forceinline__ void run_tile128(const Product &p, int id, int8_t *lds) {
     constexpr bool MASK = A_KM && B_KM;
+    const int M = p.M, N = p.N, K = p.K;
+    const Epi &ep = p.ep;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = 64 * (wave >> 1), wn = 64 * (wave & 1);
     int tm, tn;
-    gemm::tile_coords(blockIdx.x, (M + 127) / 128, (N + 127) / 128, tm, tn);
+    gemm::tile_coords(id, (M + 127) / 128, (N + 127) / 128, tm, tn);
     const int m0 = tm * 128, n0 = tn * 128;
     Src128<A_KM> sa;
     Src128<B_KM> sb;
-    sa.init(A, int(lda), a_bytes, m0, wave, lane);
-    sb.init(B, int(ldb), b_bytes, n0, wave, lane);
+    sa.init(p.A, int(p.lda), uint32_t((A_KM ? M : K) * p.lda), m0, wave, lane);
+    sb.init(p.B, int(p.ldb), uint32_t((B_KM ? N : K) * p.ldb), n0, wave, lane);
     const uint32_t base = g256::lds_addr(lds);
     const int e2 = *ep.ea + *ep.eb;
     v16i acc[2][2];
@@ -158,6 +158,23 @@ __global__ __launch_bounds__(NT) void tile128_kernel(const int8_t *__restrict__ 
         top = wave_max_u32(top);
         if (lane == 0) publish_max_u32(ep.absmax, top);
     }
+}
+
+template <class T>
+__global__ __launch_bounds__(NT) void tile128_kernel(Product p) {
+    __shared__ __attribute__((aligned(1024))) int8_t lds[kStages * kStage128];
+    run_tile128<T, true, true, false>(p, int(blockIdx.x), lds);
+}
+
+// dX's product d and G's g in one grid, where each alone is a single round (2048^3:
+// 44 us for the backward pass in two launches, 38 in one; one of blocks = 0 is not
+// asked for).
+template <class T>
+__global__ __launch_bounds__(NT) void tile128_pair_kernel(Product d, Product g) {
+    __shared__ __attribute__((aligned(1024))) int8_t lds[kStages * kStage128];
+    const int id = int(blockIdx.x);
+    if (id < d.blocks) run_tile128<T, true, false, true>(d, id, lds);
+    else run_tile128<T, false, false, true>(g, id - d.blocks, lds);
 }
 
 }  // namespace dfp8
