@@ -1,4 +1,4 @@
-// AdamW over many tensors in one launch per 64 of them, with float32 master
+// AdamW over many tensors in one launch per 60 of them, with float32 master
 // weights and the two moments held in float32 or in 8 bits ("Mixed Precision
 // Training of Convolutional Neural Networks using Integer Operations",
 // section 4: the weight update runs in floating point, on FP32 weights).
@@ -8,36 +8,60 @@
 //
 // Bound by HBM: per weight it reads P, g, m, v and writes P, m, v, 28 bytes
 // with float32 states and a float32 gradient, 12 + 1/64 + the gradient's
-// with 8-bit ones.  A wavefront takes 1024 weights as four chunks of 256, a
-// lane four consecutive ones of each, so that every access is a contiguous
-// run and a chunk is one 8-bit block: its largest magnitude is a reduction
-// inside the wavefront, and no state is read twice.  Measured: 67.1 M weights
-// with 8-bit states and bfloat16 gradients 183 us (940 MB, 5.1 TB/s; a large
-// copy reaches 5.2); 20 tensors of 268 k weights with float32 states 6.2 us, one
-// launch.
+// with 8-bit ones and 2 more with their remainders.  A wavefront takes four or
+// two chunks of 256 weights, a lane four consecutive ones of each, so that
+// every access is a contiguous run and a chunk is one 8-bit block: its largest
+// magnitude is a reduction inside the wavefront, and no state is read twice.
+// Measured: 67.1 M weights with bfloat16 gradients and float32 states 324 us
+// (1745 MB, 5.4 TB/s; a 1 GiB copy reaches 5.2), 8-bit states 194 us (940 MB, 4.8
+// TB/s), with remainders 231 us (1075 MB, 4.7 TB/s); 20 tensors of 268 k weights
+// with float32 states 6.2 us, one launch.
 //
 // 8-bit states are E4M3 codes with one power-of-two exponent per block of
 // 256.  The second moment is kept as its root r = sqrt(v): E4M3 spans 2^18
 // from its smallest to its largest value, so the root covers 2^36 of v inside
 // a block, and the step needs the root anyway.
+//
+// A step changes r by far less than the distance of two codes (at b2 = 0.999
+// it falls by at most 1 part in 2000; codes are 1 in 16 to 1 in 8 apart), so
+// rounding r to the nearest code would hold it where it is: after 2000 steps
+// of unit gradients at 0.375 of its value, and for good where gradients shrink.
+// Instead it goes to the code below or above, by a hash of the step and the
+// element's index, with the probabilities that keep the expectation of v,
+// which is linear in what came before.  v is then right on average and r
+// scatters by about 15% around its 32-bit value (25% while it falls at b2 =
+// 0.95).  With remainders, a byte more per weight, the step itself reads codes
+// that are the nearest ones, at most half a code's step off, and the remainder,
+// in 254ths of that step and rounded up or down like the codes above, keeps what
+// they leave for the next ones: code and remainder together stay within 2% of
+// the 32-bit root, 0.5% in the mean square.
 #include "float_ops.h"
 
 namespace ionn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunks = 4;                                   // chunks of 256 weights per wavefront
-constexpr int kWaveElems = kChunks * IONN_ADAMW_BLOCK;
-constexpr int kBlockElems = kWaveElems * (kThreads / 64);    // 4096
-constexpr int kTable = 64;                                   // tensors per launch
+constexpr int kTable = 60;                                   // tensors per launch (their table is an argument: 4 KiB)
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 static_assert(IONN_ADAMW_BLOCK == 256, "a block is 64 lanes of four weights");
+
+// How the moments are held: float32, codes, codes with the root's remainder.
+enum States { WORDS, CODES, CARRIED };
+
+// Chunks of 256 weights per wavefront.  The 8-bit states' arithmetic takes
+// nearly as long as their bytes, and overlaps them better from more and
+// smaller wavefronts: with 4, 2 and 1 chunks 242, 228 and 222 us (remainders, 67.1
+// M weights), but 249, 248 and 260 where each wavefront also forms the factors
+// from a count on the device.
+constexpr int chunks_of(int states) { return states == WORDS ? 4 : 2; }
+constexpr int elems_of_wave(int states) { return chunks_of(states) * IONN_ADAMW_BLOCK; }
+constexpr int elems_of_group(int states) { return elems_of_wave(states) * (kThreads / 64); }
 
 struct Table {
     float *P[kTable];
     const void *G[kTable];
     void *M[kTable], *V[kTable];
-    int8_t *S[kTable];
+    int8_t *S[kTable], *R[kTable];
     int64_t n[kTable];
     int32_t first[kTable + 1];  // first workgroup of each tensor; first[L] = grid size
     int32_t L;
@@ -54,6 +78,7 @@ struct Hyper {
 
 struct Factors {
     float b1, c1, b2, c2, rs2, eps, decay, size, scale;
+    uint32_t seed;  // the step's part of the rounding's hash
 };
 
 // b^t by repeated squaring, the same operations on the host and the device.
@@ -77,6 +102,7 @@ __host__ __device__ inline Factors make_factors(const Hyper &h, int64_t t, doubl
     f.decay = float(1.0 - lr * h.wd);
     f.size = float(lr / (1.0 - ipow(h.beta1, uint64_t(t))));
     f.scale = 1.0f;
+    f.seed = uint32_t(t) * 0x6C8E9CF5u;
     return f;
 }
 
@@ -89,6 +115,13 @@ __device__ __forceinline__ void step_one(const Factors &f, float g, float &p, fl
     r = sqrtf(v);
     const float u = m / (r * f.rs2 + f.eps);
     p = p * f.decay - f.size * u;
+}
+
+// The root of v's next value.
+__device__ __forceinline__ float next_root(const Factors &f, float g, float v) {
+#pragma clang fp contract(off)
+    v = f.b2 * v + (f.c2 * g) * g;
+    return sqrtf(v);
 }
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // e in [-126, 127]
@@ -129,6 +162,56 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4]) {
     return uint32_t(w);
 }
 
+// Numbers of (0, 1), in steps of 2^-16, for the four weights of index 4 i .. at a
+// step: a mix of the two (multiplications by odd numbers and shifts, each a
+// bijection; a multiplication takes four times an addition's time, so four
+// weights share them: a hash for each took 8 us more of 230 for 67.1 M weights).
+__device__ __forceinline__ void draw4(uint32_t i, uint32_t seed, float (&u)[4]) {
+    uint32_t h = i * 0x9E3779B9u + seed;
+    h ^= h >> 16;
+    h *= 0x5B8D2E35u;
+    h ^= h >> 15;
+    h *= 0xC6A4F30Bu;
+    const uint32_t a = h ^ (h >> 16);
+    h = a * 0x2D9A73E7u;
+    const uint32_t b = h ^ (h >> 15);
+    u[0] = (float(a & 0xffffu) + 0.5f) * 0x1p-16f;
+    u[1] = (float(a >> 16) + 0.5f) * 0x1p-16f;
+    u[2] = (float(b & 0xffffu) + 0.5f) * 0x1p-16f;
+    u[3] = (float(b >> 16) + 0.5f) * 0x1p-16f;
+}
+
+// The distance of the E4M3 values from the one at or below a in [0, 448] to
+// the next, a power of two, and its reciprocal.
+struct Grid {
+    float step, inverse;
+};
+__device__ __forceinline__ Grid grid_of(float a) {
+    const uint32_t e = max(__float_as_uint(a) >> 23, 121u);  // (2^-9 apart below 2^-6)
+    return Grid{__uint_as_float((e - 3u) << 23), __uint_as_float((257u - e) << 23)};
+}
+
+// The E4M3 value below or above s, above with probability (s^2 - lo^2) / (hi^2 - lo^2).
+__device__ __forceinline__ float round_root(float s, float u) {
+#pragma clang fp contract(off)
+    const Grid g = grid_of(s);
+    const float lo = floorf(s * g.inverse) * g.step;
+    return (s - lo) * (s + lo) > u * (g.step * (lo + lo + g.step)) ? lo + g.step : lo;
+}
+
+// Remainders of roots, in 254ths of the step at the code's value c (both ends
+// of a code's range, half a step away, are whole numbers, so that a root that
+// drifts reaches the next code).
+__device__ __forceinline__ float add_rest(float c, int rest) {
+#pragma clang fp contract(off)
+    return c + float(rest) * grid_of(c).step * (1.0f / 254.0f);
+}
+__device__ __forceinline__ int rest_of(float s, float c, float u) {
+#pragma clang fp contract(off)
+    const float x = floorf((s - c) * (grid_of(c).inverse * 254.0f) + u);
+    return int(__builtin_amdgcn_fmed3f(x, -127.0f, 127.0f));
+}
+
 // Four bytes at any address, the first `valid` of them.
 __device__ __forceinline__ uint32_t load4(const uint8_t *p, int valid) {
     if (valid >= 4) return *reinterpret_cast<const __attribute__((aligned(1))) uint32_t *>(p);
@@ -149,21 +232,25 @@ __device__ __forceinline__ void store4(uint8_t *p, uint32_t w, int valid) {
         if (i < valid) p[i] = uint8_t(w >> (8 * i));
 }
 
-template <class T, bool Q8>
+
+template <class T, int STATES>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Factors f) {
+    constexpr bool Q8 = STATES != WORDS;
+    constexpr int kChunks = chunks_of(STATES), kWaveElems = elems_of_wave(STATES);
     int l = 0;
     while (l + 1 < tab.L && int(blockIdx.x) >= tab.first[l + 1]) ++l;
     const int64_t n = tab.n[l];
     const int lane = threadIdx.x & 63;
-    const int64_t w0 = int64_t(int(blockIdx.x) - tab.first[l]) * kBlockElems + int64_t(threadIdx.x >> 6) * kWaveElems;
+    const int64_t w0 = int64_t(int(blockIdx.x) - tab.first[l]) * elems_of_group(STATES) + int64_t(threadIdx.x >> 6) * kWaveElems;
     float *__restrict__ P = tab.P[l];
     const T *__restrict__ G = static_cast<const T *>(tab.G[l]);
     float *M = static_cast<float *>(tab.M[l]), *V = static_cast<float *>(tab.V[l]);
     uint8_t *M8 = static_cast<uint8_t *>(tab.M[l]), *V8 = static_cast<uint8_t *>(tab.V[l]);
     int8_t *S = tab.S[l];
+    uint8_t *R8 = reinterpret_cast<uint8_t *>(tab.R[l]);
     typename Vec<float, 4>::type p[kChunks], m[kChunks], v[kChunks];
     typename Vec<T, 4>::type g[kChunks];
-    uint32_t mw[kChunks], vw[kChunks];
+    uint32_t mw[kChunks], vw[kChunks], rw[kChunks];
     int em[kChunks], ev[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
@@ -174,6 +261,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
         if (Q8) {
             mw[c] = load4(M8 + i, valid);
             vw[c] = load4(V8 + i, valid);
+            if (STATES == CARRIED) rw[c] = load4(R8 + i, valid);
             const int64_t b = w0 / 256 + c;
             em[c] = valid > 0 ? S[2 * b] : 0;
             ev[c] = valid > 0 ? S[2 * b + 1] : 0;
@@ -190,13 +278,17 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
         const int64_t i = w0 + c * 256 + lane * 4;
         if (w0 + c * 256 >= n) break;  // the same for the whole wavefront
         const int valid = i < n ? int(n - i < 4 ? n - i : 4) : 0;
-        float pn[4], mn[4], vn[4], rn[4];
+        float pn[4], mn[4], vn[4], rn[4], wn[4];  // (wn: the root with its remainder, squared; then new)
         if (Q8) {
             decode4(mw[c], mn);
             decode4(vw[c], vn);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 mn[e] *= pow2f(em[c]);
+                if (STATES == CARRIED) {
+                    const float w = add_rest(vn[e], int8_t(rw[c] >> (8 * e))) * pow2f(ev[c]);
+                    wn[e] = w * w;
+                }
                 const float r = vn[e] * pow2f(ev[c]);
                 vn[e] = r * r;
             }
@@ -209,6 +301,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
                 vn[e] = v[c][e];
             }
             step_one(f, float(g[c][e]) * scale, pn[e], mn[e], vn[e], rn[e]);
+            wn[e] = STATES == CARRIED ? next_root(f, float(g[c][e]) * scale, wn[e]) : rn[e];
             if (e < valid) top = max(top, mag_bits(pn[e]));
         }
         store_vec<float, 4>(P + i, pn, valid);
@@ -217,19 +310,31 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 am = max(am, e < valid ? finite_bits(mn[e]) : 0u);
-                av = max(av, e < valid ? finite_bits(rn[e]) : 0u);
+                av = max(av, e < valid ? finite_bits(wn[e]) : 0u);
             }
             const int xm = block_exponent(wave_max_u32(am)), xv = block_exponent(wave_max_u32(av));
-            float sm[4], sv[4];
+            float sm[4], sv[4], u[4];
+            draw4(uint32_t(i >> 2), f.seed, u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 sm[e] = mn[e] * pow2f(-xm);
-                sv[e] = rn[e] * pow2f(-xv);
+                const bool positive = wn[e] > 0.0f;
+                wn[e] *= pow2f(-xv);
+                sv[e] = STATES == CODES ? round_root(wn[e], u[e]) : wn[e];
                 // a positive root keeps at least the smallest code, 2^-9
-                if (rn[e] > 0.0f && sv[e] < 0x1p-9f) sv[e] = 0x1p-9f;
+                if (positive && sv[e] < 0x1p-9f) sv[e] = 0x1p-9f;
             }
+            const uint32_t codes = encode4(sv);
             store4(M8 + i, encode4(sm), valid);
-            store4(V8 + i, encode4(sv), valid);
+            store4(V8 + i, codes, valid);
+            if (STATES == CARRIED) {
+                decode4(codes, sv);
+                uint32_t w = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w |= (mag_bits(wn[e]) < 0x7f800000u ? uint32_t(rest_of(wn[e], sv[e], u[e])) & 0xffu : 0u) << (8 * e);
+                store4(R8 + i, w, valid);
+            }
             if (lane == 0) {
                 const int64_t b = w0 / 256 + c;
                 S[2 * b] = int8_t(xm);
@@ -251,38 +356,39 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
 
 using namespace ionn;
 
-extern "C" {
-
-int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype, void *const *M, void *const *V,
-                    int8_t *const *S, int state_bits, const int64_t *n, int64_t t, double lr, double beta1,
-                    double beta2, double eps, double weight_decay, const int32_t *step, const float *lr_dev,
-                    const float *grad_scale, uint32_t *absmax_P, void *stream) {
+// (`what`: the entry point, for its messages; R NULL: no remainders)
+static int adamw(const char *what, int L, float *const *P, const void *const *G, int g_dtype, void *const *M,
+                 void *const *V, int8_t *const *S, int8_t *const *R, int state_bits, const int64_t *n, int64_t t,
+                 double lr, double beta1, double beta2, double eps, double weight_decay, const int32_t *step,
+                 const float *lr_dev, const float *grad_scale, uint32_t *absmax_P, void *stream) {
     clear_error();
-    IONN_REQUIRE(L >= 1, IONN_ERR_SHAPE, "ionn_adamw_step: L = %d < 1", L);
-    IONN_REQUIRE(dtype_ok(g_dtype), IONN_ERR_ARG, "ionn_adamw_step: g_dtype = %d", g_dtype);
-    IONN_REQUIRE(state_bits == 32 || state_bits == 8, IONN_ERR_ARG, "ionn_adamw_step: state_bits = %d (8 or 32)",
+    IONN_REQUIRE(L >= 1, IONN_ERR_SHAPE, "%s: L = %d < 1", what, L);
+    IONN_REQUIRE(dtype_ok(g_dtype), IONN_ERR_ARG, "%s: g_dtype = %d", what, g_dtype);
+    IONN_REQUIRE(state_bits == 32 || state_bits == 8, IONN_ERR_ARG, "%s: state_bits = %d (8 or 32)", what,
                  state_bits);
-    IONN_REQUIRE(P && G && M && V && n && (state_bits == 32 || S), IONN_ERR_ARG, "ionn_adamw_step: NULL array");
+    IONN_REQUIRE(P && G && M && V && n && (state_bits == 32 || S), IONN_ERR_ARG, "%s: NULL array", what);
     IONN_REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, IONN_ERR_RANGE,
-                 "ionn_adamw_step: beta1 = %g, beta2 = %g outside [0, 1)", beta1, beta2);
+                 "%s: beta1 = %g, beta2 = %g outside [0, 1)", what, beta1, beta2);
     IONN_REQUIRE(eps >= 0.0 && eps <= 3.0e38 && lr >= -3.0e38 && lr <= 3.0e38 && weight_decay >= -3.0e38 &&
                      weight_decay <= 3.0e38,
-                 IONN_ERR_RANGE, "ionn_adamw_step: eps = %g, lr = %g, weight_decay = %g", eps, lr, weight_decay);
-    IONN_REQUIRE(step || t >= 1, IONN_ERR_RANGE, "ionn_adamw_step: t = %lld < 1", (long long)t);
+                 IONN_ERR_RANGE, "%s: eps = %g, lr = %g, weight_decay = %g", what, eps, lr, weight_decay);
+    IONN_REQUIRE(step || t >= 1, IONN_ERR_RANGE, "%s: t = %lld < 1", what, (long long)t);
     IONN_REQUIRE(aligned(step, 4) && aligned(lr_dev, 4) && aligned(grad_scale, 4) && aligned(absmax_P, 4),
-                 IONN_ERR_ALIGN, "ionn_adamw_step: device scalars must be 4-byte aligned");
+                 IONN_ERR_ALIGN, "%s: device scalars must be 4-byte aligned", what);
     const size_t gs = dtype_size(g_dtype), ss = state_bits == 32 ? 4 : 1;
     for (int l = 0; l < L; ++l) {
-        IONN_REQUIRE(n[l] >= 1 && n[l] <= kMaxElems, IONN_ERR_SHAPE, "ionn_adamw_step: tensor %d has n = %lld", l,
+        IONN_REQUIRE(n[l] >= 1 && n[l] <= kMaxElems, IONN_ERR_SHAPE, "%s: tensor %d has n = %lld", what, l,
                      (long long)n[l]);
         IONN_REQUIRE(P[l] && G[l] && M[l] && V[l] && (state_bits == 32 || S[l]), IONN_ERR_ARG,
-                     "ionn_adamw_step: tensor %d has a NULL pointer", l);
+                     "%s: tensor %d has a NULL pointer", what, l);
         IONN_REQUIRE(aligned(P[l], 4) && aligned(G[l], gs) && aligned(M[l], ss) && aligned(V[l], ss), IONN_ERR_ALIGN,
-                     "ionn_adamw_step: tensor %d must be aligned to its element size", l);
+                     "%s: tensor %d must be aligned to its element size", what, l);
     }
     Hyper h{lr, beta1, beta2, eps, weight_decay, t, step, lr_dev, grad_scale, nullptr};
     const Factors f = make_factors(h, t < 1 ? 1 : t, lr);
     hipStream_t st = as_stream(stream);
+    const int64_t per = elems_of_group(state_bits == 32 ? WORDS : CODES);
+    static_assert(elems_of_group(CODES) == elems_of_group(CARRIED), "one layout of the 8-bit states");
     int l = 0;
     while (l < L) {
         Table tab;
@@ -291,13 +397,14 @@ int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype, v
         h.absmax = absmax_P ? absmax_P + l : nullptr;
         int k = 0;
         for (; k < kTable && l < L; ++k, ++l) {
-            const int64_t b = (n[l] + kBlockElems - 1) / kBlockElems;
-            if (blocks + b > 0x7fffffff) break;  // (a single tensor has at most 2^28)
+            const int64_t b = (n[l] + per - 1) / per;
+            if (blocks + b > 0x7fffffff) break;  // (a single tensor has at most 2^29)
             tab.P[k] = P[l];
             tab.G[k] = G[l];
             tab.M[k] = M[l];
             tab.V[k] = V[l];
             tab.S[k] = state_bits == 8 ? S[l] : nullptr;
+            tab.R[k] = R ? R[l] : nullptr;
             tab.n[k] = n[l];
             tab.first[k] = int32_t(blocks);
             blocks += b;
@@ -306,14 +413,36 @@ int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype, v
         tab.L = k;
         with_dtype(g_dtype, [&](auto tag) {
             using T = decltype(tag);
-            if (state_bits == 8)
-                adamw_kernel<T, true><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(tab, h, f);
-            else
-                adamw_kernel<T, false><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(tab, h, f);
+            const dim3 grid{unsigned(blocks)}, block{kThreads};
+            if (state_bits == 32) adamw_kernel<T, WORDS><<<grid, block, 0, st>>>(tab, h, f);
+            else if (!R) adamw_kernel<T, CODES><<<grid, block, 0, st>>>(tab, h, f);
+            else adamw_kernel<T, CARRIED><<<grid, block, 0, st>>>(tab, h, f);
         });
-        if (int rc = check_launch("ionn_adamw_step")) return rc;
+        if (int rc = check_launch(what)) return rc;
     }
     return IONN_OK;
+}
+
+extern "C" {
+
+int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype, void *const *M, void *const *V,
+                    int8_t *const *S, int state_bits, const int64_t *n, int64_t t, double lr, double beta1,
+                    double beta2, double eps, double weight_decay, const int32_t *step, const float *lr_dev,
+                    const float *grad_scale, uint32_t *absmax_P, void *stream) {
+    return adamw("ionn_adamw_step", L, P, G, g_dtype, M, V, S, nullptr, state_bits, n, t, lr, beta1, beta2, eps,
+                 weight_decay, step, lr_dev, grad_scale, absmax_P, stream);
+}
+
+int ionn_adamw_step_carried(int L, float *const *P, const void *const *G, int g_dtype, void *const *M, void *const *V,
+                            int8_t *const *S, int8_t *const *R, const int64_t *n, int64_t t, double lr, double beta1,
+                            double beta2, double eps, double weight_decay, const int32_t *step, const float *lr_dev,
+                            const float *grad_scale, uint32_t *absmax_P, void *stream) {
+    clear_error();
+    IONN_REQUIRE(R, IONN_ERR_ARG, "ionn_adamw_step_carried: NULL array");
+    for (int l = 0; l < L; ++l)
+        IONN_REQUIRE(R[l], IONN_ERR_ARG, "ionn_adamw_step_carried: tensor %d has a NULL pointer", l);
+    return adamw("ionn_adamw_step_carried", L, P, G, g_dtype, M, V, S, R, 8, n, t, lr, beta1, beta2, eps, weight_decay,
+                 step, lr_dev, grad_scale, absmax_P, stream);
 }
 
 }  // extern "C"

@@ -712,20 +712,26 @@ def _state_ptrs(ts, bits, name):
 
 
 def ionn_adamw_step(Ps, Gs, Ms, Vs, t, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, Ss=None, step=None,
-                    lr_dev=None, grad_scale=None, absmax_P=None, stream=None):
+                    lr_dev=None, grad_scale=None, absmax_P=None, stream=None, Rs=None):
     """One step of every tensor (lists of device tensors); 8-bit states where
-    Ss (int8 [blocks][2] per tensor) is given."""
+    Ss (int8 [blocks][2] per tensor) is given, with the roots' remainders
+    (ionn_adamw_step_carried) where Rs (int8 per element) is."""
     L = len(Ps)
     bits = 32 if Ss is None else 8
     _same(len(Gs) == L and len(Ms) == L and len(Vs) == L and (Ss is None or len(Ss) == L), "lists of tensors")
     _same(all(p.numel() == x.numel() for xs in (Gs, Ms, Vs) for p, x in zip(Ps, xs)), "P, G, M and V of a tensor")
     _same(Ss is None or all(s.numel() == 2 * -(-p.numel() // ADAMW_BLOCK) for p, s in zip(Ps, Ss)), "S of a tensor")
+    _same(Rs is None or (Ss is not None and len(Rs) == L and all(r.numel() == p.numel() for p, r in zip(Ps, Rs))),
+          "R of a tensor")
     if L == 0:
         return
-    rc = lib().ionn_adamw_step(L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
-                               _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"),
-                               None if Ss is None else _ptr_array(Ss, i8, "S"), bits, _sizes(Ps), int(t), lr, beta1,
-                               beta2, eps, weight_decay, _s(step, i32, "step"), _s(lr_dev, f32, "lr_dev"),
-                               _s(grad_scale, f32, "grad_scale"), _v(absmax_P, u32, L, "absmax_P"), _on(stream, Ps[0]))
+    head = (L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"),
+            _state_ptrs(Ms, bits, "M"), _state_ptrs(Vs, bits, "V"), None if Ss is None else _ptr_array(Ss, i8, "S"))
+    tail = (_sizes(Ps), int(t), lr, beta1, beta2, eps, weight_decay, _s(step, i32, "step"), _s(lr_dev, f32, "lr_dev"),
+            _s(grad_scale, f32, "grad_scale"), _v(absmax_P, u32, L, "absmax_P"), _on(stream, Ps[0]))
+    if Rs is None:
+        rc = lib().ionn_adamw_step(*head, bits, *tail)
+    else:
+        rc = lib().ionn_adamw_step_carried(*head, _ptr_array(Rs, i8, "R"), *tail)
     if rc:
-        check(rc, "ionn_adamw_step")
+        check(rc, "ionn_adamw_step" if Rs is None else "ionn_adamw_step_carried")

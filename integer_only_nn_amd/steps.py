@@ -443,30 +443,41 @@ class AptLayers:
 class AdamW:
     """The optimiser of a list of float32 master weights, updated in place.
     Ms and Vs: the moments, float32 tensors; or, with Ss (int8 [blocks][2] per
-    tensor), codes of one byte of m and of sqrt(v) (make() allocates either
-    kind, cleared).  The ctypes arrays are built once (bind_grads for the
-    gradient buffers), so a step costs one library call.
+    tensor), codes of one byte of m and of sqrt(v).  Rs (int8, as the weights)
+    carries what a code leaves of sqrt(v), so that the second moment follows
+    its definition within 2%; None: allocated as zeros, the codes' own values
+    (keep them with the other states).  Rs=False: codes alone, whose v is right
+    on average and scatters by about 30% per weight.  The ctypes arrays are
+    built once (bind_grads for the gradient buffers), so a step costs one
+    library call.
 
     t counts the steps taken.  With on_device the count and the learning rate
     live in device scalars (self.step_dev, advanced by each step, and
     self.lr_dev), so that steps can be captured in a graph and replayed."""
 
     def __init__(self, Ps, Ms, Vs, Ss=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, t=0,
-                 on_device=False):
+                 on_device=False, Rs=None):
         self.P, self.M, self.V, self.S = list(Ps), list(Ms), list(Vs), None if Ss is None else list(Ss)
         self.lr, self.betas, self.eps, self.weight_decay, self.t = lr, betas, eps, weight_decay, int(t)
         bits = 32 if Ss is None else 8
         for xs in (self.M, self.V):
             ops._same(len(xs) == len(self.P) and all(x.numel() == p.numel() for x, p in zip(xs, self.P)),
                       "weights and states")
+        self.R = None
+        ops._same(not Rs or Ss is not None, "remainders without codes")
+        if Ss is not None and Rs is not False:
+            zeros = lambda p: torch.zeros(p.shape, dtype=torch.int8, device=p.device)  # noqa: E731
+            self.R = [zeros(p) for p in self.P] if Rs is None else list(Rs)
+            ops._same(len(self.R) == len(self.P) and all(r.numel() == p.numel() for r, p in zip(self.R, self.P)),
+                      "weights and remainders")
         if Ss is not None:
             ops._same(len(self.S) == len(self.P) and
                       all(s.numel() == 2 * -(-p.numel() // ops.ADAMW_BLOCK) for s, p in zip(self.S, self.P)),
                       "weights and state exponents")
-        self._bits = bits
         self._Pp = ops._ptr_array(self.P, torch.float32, "P")
-        self._Mp, self._Vp = ops._state_ptrs(self.M, bits, "M"), ops._state_ptrs(self.V, bits, "V")
-        self._Sp = None if Ss is None else ops._ptr_array(self.S, torch.int8, "S")
+        self._states = [ops._state_ptrs(self.M, bits, "M"), ops._state_ptrs(self.V, bits, "V")]
+        self._states += [None if Ss is None else ops._ptr_array(self.S, torch.int8, "S"),
+                         bits if self.R is None else ops._ptr_array(self.R, torch.int8, "R")]
         self._n = ops._sizes(self.P)
         self._G = None
         self.step_dev = self.lr_dev = None
@@ -477,14 +488,15 @@ class AdamW:
 
     @staticmethod
     def make(Ps, bits=32, **kw):
-        """Cleared states of 32 or 8 bits for these weights."""
+        """Cleared states of 32 or 8 bits for these weights: 8 or 2 bytes per
+        weight, 3 with remainders (bits=8, Rs=None)."""
         if bits == 32:
             return AdamW(Ps, [torch.zeros_like(p) for p in Ps], [torch.zeros_like(p) for p in Ps], **kw)
         if bits != 8:
             raise ValueError(f"bits = {bits} (8 or 32)")
         codes = lambda: [torch.zeros(p.shape, dtype=torch.uint8, device=p.device) for p in Ps]  # noqa: E731
         blocks = [torch.zeros(-(-p.numel() // ops.ADAMW_BLOCK), 2, dtype=torch.int8, device=p.device) for p in Ps]
-        return AdamW(Ps, codes(), codes(), blocks, **kw)
+        return AdamW(Ps, codes(), codes(), blocks, **{"Rs": False, **kw})
 
     def bind_grads(self, Gs):
         """Fix the gradient buffers (device tensors of one floating type, one
@@ -510,14 +522,15 @@ class AdamW:
                 with torch.cuda.stream(on):
                     self.step_dev.add_(1)
         self.t += 1
-        rc = ops.lib().ionn_adamw_step(
-            len(self.P), self._Pp, self._G[1], self._G[2], self._Mp, self._Vp, self._Sp, self._bits, self._n, self.t,
+        name = "ionn_adamw_step" if self.R is None else "ionn_adamw_step_carried"
+        rc = getattr(ops.lib(), name)(
+            len(self.P), self._Pp, self._G[1], self._G[2], *self._states, self._n, self.t,
             self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
             ops._s(self.step_dev, torch.int32, "step"), ops._s(self.lr_dev, torch.float32, "lr_dev"),
             ops._s(grad_scale, torch.float32, "grad_scale"), ops._v(absmax_P, torch.int32, len(self.P), "absmax_P"),
             ops._on(stream, self.P[0]))
         if rc:
-            ops.check(rc, "ionn_adamw_step")
+            ops.check(rc, name)
 
 
 # ---------------------------------------------------------------------------
@@ -532,7 +545,8 @@ class ResidualMlp:
     point, FP32 master weights.
 
     Activations and their gradients are of type dtype.  Weights decay, gains
-    and biases do not; both groups keep their moments in state_bits bits.  All
+    and biases do not; both groups keep their moments in state_bits bits (8:
+    with remainders of the second moment, three bytes per weight).  All
     buffers are allocated here, so a step only enqueues kernels (and can be
     captured in a graph with on_device)."""
 
@@ -563,7 +577,7 @@ class ResidualMlp:
                    ops.dfp8_linear_bwd_workspace_bytes(B, D, H), ops.dfp8_linear_bwd_workspace_bytes(B, H, D),
                    ops.ionn_layer_norm_bwd_workspace_bytes(B, D), ops.dfp8_from_float_workspace_bytes())
         self.ws = new(need, dt=torch.uint8)
-        kw = dict(bits=state_bits, lr=lr, betas=betas, on_device=on_device)
+        kw = dict(bits=state_bits, lr=lr, betas=betas, on_device=on_device, Rs=None)
         self.opt = AdamW.make([W1, W2], weight_decay=weight_decay, **kw)
         self.opt.bind_grads([self.gW1, self.gW2])
         self.opt_vectors = AdamW.make([b1, b2, gamma, beta], weight_decay=0.0, **kw)

@@ -152,10 +152,81 @@ def state_decode(c, e):
     return np.ldexp(_TABLE[c], e.astype(np.int64).repeat(ADAMW_BLOCK)[:c.size]).astype(np.float32)
 
 
-def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.0, exps=None):
-    """(p, m, v[, exps]) after one step of one tensor.  v: the second moment
-    (float32), or with exps (int8 [blocks][2]) m and v are E4M3 codes of m
-    and of the root of the second moment."""
+def draws(n, t):
+    """One of the numbers (k + 1/2) / 65536 for each
+    element of a tensor at step t: a fixed hash of the step and the index of
+    the four elements that share it, in 32-bit arithmetic, two elements from
+    the halves of each of two words."""
+    u = np.uint32
+    h = np.arange(-(-n // 4), dtype=u) * u(0x9E3779B9) + u((t * 0x6C8E9CF5) & 0xffffffff)
+    h ^= h >> u(16)
+    h *= u(0x5B8D2E35)
+    h ^= h >> u(15)
+    h *= u(0xC6A4F30B)
+    a = h ^ (h >> u(16))
+    h = a * u(0x2D9A73E7)
+    b = h ^ (h >> u(15))
+    k = np.stack([a & u(0xffff), a >> u(16), b & u(0xffff), b >> u(16)], 1).reshape(-1)[:n]
+    return (k.astype(np.float32) + np.float32(0.5)) * np.float32(2.0 ** -16)
+
+
+def _scaled(x):
+    """float32 x over its block's power of two, and the exponents."""
+    e = block_exponents(x)
+    return np.ldexp(x, -e.astype(np.int32).repeat(ADAMW_BLOCK)[:x.size]), e
+
+
+def _grid(a):
+    """The largest E4M3 value that is not above a >= 0, and the distance to the next one (float32, exact)."""
+    f = np.float32
+    step = np.maximum(np.ldexp(f(1.0), np.frexp(a)[1] - 4), f(2.0 ** -9)).astype(f)
+    return np.floor(a / step) * step, step
+
+
+def root_encode(r, draw):
+    """(codes, exponents) of a float32 root r >= 0: the E4M3 value below or
+    above it, above with the probability that keeps the expectation of r^2."""
+    f = np.float32
+    s, e = _scaled(r)
+    with np.errstate(all="ignore"):
+        fin = np.where(np.isfinite(s), s, f(0))
+        lo, step = _grid(fin)
+        up = (fin - lo) * (fin + lo) > draw * (step * (lo + lo + step))
+        q = np.where(up, lo + step, lo)
+    q = np.where((r > 0) & (q < f(2.0 ** -9)), f(2.0 ** -9), q)
+    return e4m3_encode(np.where(np.isfinite(s), q, s)), e
+
+
+_REST = np.float32(1.0 / 254.0)
+
+
+def root_encode_carried(r, draw):
+    """(codes, remainders, exponents): the nearest E4M3 code (not 0 for a
+    positive r), and what is left of r in 254ths of the code's step, one of
+    the two whole numbers around it with its expectation kept."""
+    f = np.float32
+    s, _ = _scaled(r)
+    c, e = state_encode(r, True)
+    v = _TABLE[c].astype(f)
+    with np.errstate(all="ignore"):
+        x = (s - v) * (f(254.0) / _grid(np.where(np.isnan(v), f(0), v))[1])
+        q = np.clip(np.floor(x + draw), -127, 127)
+    return c, np.where(np.isfinite(s), q, 0).astype(np.int8), e
+
+
+def root_decode_carried(c, rest, e):
+    f = np.float32
+    v = _TABLE[c].astype(f)
+    v = v + (rest.astype(f) * _grid(np.where(np.isnan(v), f(0), v))[1]) * _REST
+    return np.ldexp(v, e.astype(np.int32).repeat(ADAMW_BLOCK)[:c.size])
+
+
+def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.0, exps=None, rest=None):
+    """(p, m, v[, exps[, rest]]) after one step of one tensor.  v: the second
+    moment (float32), or with exps (int8 [blocks][2]) m and v are E4M3 codes
+    of m and of the root of the second moment.  The step reads the codes;
+    rest, where it is given, carries what they leave of the root, for the next
+    codes."""
     f = np.float32
     b1, c1, b2, c2 = f(beta1), f(1.0 - beta1), f(beta2), f(1.0 - beta2)
     rs2 = f(1.0 / math.sqrt(1.0 - beta2 ** t))
@@ -163,7 +234,9 @@ def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.
     with np.errstate(all="ignore"):
         g = g.astype(f) * f(grad_scale)
         if exps is not None:
-            m, r = state_decode(m, exps[:, 0]), state_decode(v, exps[:, 1])
+            m = state_decode(m, exps[:, 0])
+            r = state_decode(v, exps[:, 1])
+            whole = None if rest is None else root_decode_carried(v, rest, exps[:, 1])
             v = r * r
         m = b1 * m + c1 * g
         v = b2 * v + (c2 * g) * g
@@ -173,5 +246,12 @@ def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.
     assert p.dtype == m.dtype == v.dtype == f
     if exps is None:
         return p, m, v
-    (cm, em), (cr, er) = state_encode(m, False), state_encode(r, True)
-    return p, cm, cr, np.stack([em, er], 1)
+    cm, em = state_encode(m, False)
+    draw = draws(p.size, t)
+    if rest is None:
+        cr, er = root_encode(r, draw)
+        return p, cm, cr, np.stack([em, er], 1)
+    with np.errstate(all="ignore"):
+        r = np.sqrt(b2 * (whole * whole) + (c2 * g) * g)
+    cr, rest, er = root_encode_carried(r, draw)
+    return p, cm, cr, np.stack([em, er], 1), rest
