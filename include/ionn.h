@@ -804,7 +804,9 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
  * the float32 m and v and stores both again: for a block's largest finite
  * magnitude f * 2^q (f in [1, 2)) the exponent is q - 8 where f <= 1.75,
  * q - 7 otherwise, at least -126 (0 for an all-zero block).  m rounds to the
- * nearest code (even).  r, which a step changes by less than a code's half
+ * nearest code (even) where beta1 <= 15/16; above, a step changes it by less
+ * than a code's half step, and it goes to the code on either side of it with
+ * its expectation kept, by the hash below.  r, which a step changes by less than a code's half
  * step, goes to the code below or above, lo or hi: with s = r / 2^exponent to
  * hi where (s - lo) * (s + lo) > u * (hi^2 - lo^2) in float32, u in
  * (0, 1) a hash of t and the element's index (draws() in oracle/floats.py), so

@@ -183,6 +183,18 @@ def _grid(a):
     return np.floor(a / step) * step, step
 
 
+def mean_encode(m, draw):
+    """(codes, exponents) of a float32 mean: the E4M3 value on either side of
+    it, with its expectation kept."""
+    f = np.float32
+    s, e = _scaled(m)
+    with np.errstate(all="ignore"):
+        a = np.abs(np.where(np.isfinite(s), s, f(0)))
+        lo, step = _grid(a)
+        q = np.copysign(np.where(a - lo > draw * step, lo + step, lo), s)
+    return e4m3_encode(np.where(np.isfinite(s), q, s)), e
+
+
 def root_encode(r, draw):
     """(codes, exponents) of a float32 root r >= 0: the E4M3 value below or
     above it, above with the probability that keeps the expectation of r^2."""
@@ -246,8 +258,12 @@ def adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay, grad_scale=1.
     assert p.dtype == m.dtype == v.dtype == f
     if exps is None:
         return p, m, v
-    cm, em = state_encode(m, False)
     draw = draws(p.size, t)
+    if beta1 <= 0.9375:
+        cm, em = state_encode(m, False)
+    else:  # (the number of the element two on, or back, among its four)
+        other = draws(-(-p.size // 4) * 4, t).reshape(-1, 4)[:, [2, 3, 0, 1]].reshape(-1)[:p.size]
+        cm, em = mean_encode(m, other)
     if rest is None:
         cr, er = root_encode(r, draw)
         return p, cm, cr, np.stack([em, er], 1)
