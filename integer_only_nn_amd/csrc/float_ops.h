@@ -67,17 +67,17 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[VE], int valid 
 // distribution function Phi; gelu_tanh is z * sigmoid(2 k (z + c z^3)), k =
 // sqrt(2 / pi), c = 0.044715 (0.5 (1 + tanh w) = sigmoid(2 w)).
 //
-// Phi(z) = sigmoid(z Q(z^2)) with Q the polynomial that comes nearest to
-// logit(Phi(z)) / z (a least-maximum fit, weighted by z Phi (1 - Phi), over z
-// in (0, 6.5]; it stays positive and grows beyond).  It keeps the negative
-// tail's scale, where 1 + erf cancels, and takes 10 or 13 instructions, two of
-// them quarter-rate, where erfc takes about 40; the passes over 8192 x 4096
-// values are bound by them.
-//   8 terms: off by at most 1.2e-7, two half steps of float32 at 1, which the
-//     rounding of the argument leaves anyway;
-//   5 terms: 1.5e-6, a hundredth of half a step of bfloat16 at 1, for values
-//     that are rounded to 16 bits.  Not for derivatives: their column sums
-//     are float32, and the fit's error does not average out in them.
+// Phi's tail is Phi(-x) = exp(-x^2 / 2) t P(t), t = 1 / (1 + p x), with p and the
+// polynomial P that come nearest to it in relative error over x in [0, 14] (at
+// 13.2 the exponential leaves float32's range).  So gelu(z) = max(z, 0) - |z|
+// Phi(-|z|) keeps its relative exactness however small it gets, where 1 + erf
+// cancels.  Beside the fit's error there are the roundings of exp's argument, z^2
+// half steps of float32 at most.  The passes over 8192 x 4096 values are bound by
+// these instructions, two of 13 or 16 quarter-rate.
+//   8 terms: off by at most 1.1e-7 of the value, two half steps of float32;
+//   5 terms: 3.1e-5, a sixteenth of half a step of float16, for values that are
+//     rounded to 16 bits.  Not for derivatives: their column sums are float32,
+//     and the fit's error does not average out in them.
 constexpr int kTermsGrad = 8;
 template <class T>
 constexpr int kTermsValue = sizeof(T) == 4 ? 8 : 5;
@@ -85,7 +85,7 @@ constexpr int kTermsValue = sizeof(T) == 4 ? 8 : 5;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGeluK = 1.59576912160573071f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
-constexpr float kLog2InvSqrt2Pi = -1.32574806473616f;  // log2(1 / sqrt(2 pi))
+constexpr float kInvSqrt2Pi = 0.398942280401432678f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // 1 / (1 + 2^x): the logistic function of -x ln 2
@@ -96,22 +96,28 @@ __device__ __forceinline__ float logistic2(float x) { return __builtin_amdgcn_rc
 __device__ __forceinline__ float above(float z) { return fmaxf(z, -200.0f); }
 __device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -30.0f, 30.0f); }
 
-// Phi(z), u = z^2.
+// exp(-x^2 / 2) and, of it, Phi(-x); x >= 0.
+__device__ __forceinline__ float normal_exp(float x) { return exp2_fast(x * x * (-0.5f * kLog2e)); }
 template <int TERMS>
-__device__ __forceinline__ float normal_cdf(float z, float u) {
-    constexpr float c8[8] = {1.5957697844099097e+00f, 7.266674921058917e-02f,  -6.60603328097877e-05f, -1.1009835059468343e-04f,
-                             7.788852044459863e-06f,  -2.45761265691951e-07f, 2.3421368291093768e-09f, 2.696477063689756e-11f};
-    constexpr float c5[5] = {1.59573911e+00f, 7.27856189e-02f, -1.76439094e-04f, -7.32000513e-05f, 2.83706209e-06f};
-    float q = -kLog2e * (TERMS == 8 ? c8[7] : c5[4]);
+__device__ __forceinline__ float normal_tail(float x, float e) {
+    constexpr float p = TERMS == 8 ? 0.30625f : 0.375f;
+    constexpr float c8[8] = {1.221450791e-01f,  1.228500903e-01f, 1.045957729e-01f,  1.180542856e-01f,
+                             -3.183713555e-02f, 1.778280437e-01f, -1.501339674e-01f, 3.649786860e-02f};
+    constexpr float c5[5] = {1.490610093e-01f, 1.577341557e-01f, 8.356352150e-02f, 2.002823502e-01f, -9.064312279e-02f};
+    const float t = __builtin_amdgcn_rcpf(fmaf(p, x, 1.0f));
+    float q = TERMS == 8 ? c8[7] : c5[4];
 #pragma unroll
-    for (int i = TERMS - 2; i >= 0; --i) q = fmaf(q, u, -kLog2e * (TERMS == 8 ? c8[i] : c5[i < 5 ? i : 4]));
-    return logistic2(z * q);
+    for (int i = TERMS - 2; i >= 0; --i) q = fmaf(q, t, TERMS == 8 ? c8[i] : c5[i < 5 ? i : 4]);
+    return e * (t * q);
 }
 
 template <int ACT, int TERMS>
 __device__ __forceinline__ float act_value(float z) {
     if (ACT == IONN_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if (ACT == IONN_ACT_GELU) return above(z) * normal_cdf<TERMS>(z, z * z);
+    if (ACT == IONN_ACT_GELU) {  // (|z| clipped where the tail is 0, so that infinities do not meet it)
+        const float x = fabsf(z);
+        return fmaf(-fminf(x, 30.0f), normal_tail<TERMS>(x, normal_exp(x)), fmaxf(z, 0.0f));
+    }
     if (ACT == IONN_ACT_GELU_TANH)
         return above(z) * logistic2(z * fmaf(z * z, -kLog2e * kGeluK * kGeluC, -kLog2e * kGeluK));
     if (ACT == IONN_ACT_SILU) return above(z) * logistic2(-kLog2e * z);
@@ -122,8 +128,8 @@ template <int ACT, int TERMS>
 __device__ __forceinline__ float act_grad(float z) {
     if (ACT == IONN_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     if (ACT == IONN_ACT_GELU) {  // Phi + z phi
-        const float u = z * z;
-        return fmaf(within(z), exp2_fast(fmaf(u, -0.5f * kLog2e, kLog2InvSqrt2Pi)), normal_cdf<TERMS>(z, u));
+        const float x = fabsf(z), e = normal_exp(x), tail = normal_tail<TERMS>(x, e);
+        return fmaf(within(z) * kInvSqrt2Pi, e, z < 0.0f ? tail : 1.0f - tail);
     }
     if (ACT == IONN_ACT_GELU_TANH) {
         const float p = logistic2(z * fmaf(z * z, -kLog2e * kGeluK * kGeluC, -kLog2e * kGeluK)), y = within(z);
