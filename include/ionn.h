@@ -707,9 +707,10 @@ enum {
  * x: dtype [n]; out: int8 [n]; e_out: device int32; status_out (nullable,
  * device int32): 0, 1 when E leaves the signed 8-bit range (E still
  * written), 2 when x holds a NaN or infinity (outputs then unspecified).
- * absmax (nullable): device uint32 that holds the float32 bits of max |x|,
- * as the absmax arguments below leave them; the maximum is then not taken
- * again.  Without it the call takes it, in `workspace` (4-byte aligned,
+ * absmax (nullable): device uint32 that holds the float32 bits of max |x|, of
+ * x itself or as it was before it was rounded to its type (as the absmax
+ * arguments below leave them: the call rounds it); the maximum is then not
+ * taken again.  Without it the call takes it, in `workspace` (4-byte aligned,
  * dfp8_from_float_workspace_bytes() bytes).  n >= 1. */
 size_t dfp8_from_float_workspace_bytes(void);
 int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax,

@@ -67,13 +67,16 @@ __device__ __forceinline__ uint32_t all_max(const uint32_t *__restrict__ part, i
     return block_max(m);
 }
 
-template <class T>
+// GIVEN: part is a producer's maximum, taken before it rounded its values to
+// T; rounding keeps their order, so it is rounded here (and an infinity that
+// only the type made shows).
+template <class T, bool GIVEN>
 __global__ __launch_bounds__(kThreads) void round_kernel(const T *__restrict__ x, int64_t n,
                                                          const uint32_t *__restrict__ part, int nparts,
                                                          int8_t *__restrict__ out, int32_t *__restrict__ e_out,
                                                          int32_t *__restrict__ status) {
     constexpr int VE = 16 / sizeof(T);
-    const uint32_t m = all_max(part, nparts);
+    const uint32_t m = GIVEN ? mag_bits(float(T(__uint_as_float(*part)))) : all_max(part, nparts);
     const int E = dfp8_exponent(m);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *e_out = E;
@@ -411,7 +414,7 @@ int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax,
                  dfp8_from_float_workspace_bytes());
     hipStream_t st = as_stream(stream);
     uint32_t *part = static_cast<uint32_t *>(workspace);
-    int nparts = 1;
+    int nparts = 0;
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
         const T *p = static_cast<const T *>(x);
@@ -419,8 +422,9 @@ int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax,
             nparts = int(pass_groups(n, sizeof(T), kMaxParts));
             max_kernel<T><<<dim3(unsigned(nparts)), dim3(kThreads), 0, st>>>(p, n, part);
         }
-        round_kernel<T><<<dim3(pass_groups(n, sizeof(T), 2048)), dim3(kThreads), 0, st>>>(
-            p, n, absmax ? absmax : part, nparts, out, e_out, status_out);
+        const dim3 grid{pass_groups(n, sizeof(T), 2048)}, block{kThreads};
+        if (absmax) round_kernel<T, true><<<grid, block, 0, st>>>(p, n, absmax, 1, out, e_out, status_out);
+        else round_kernel<T, false><<<grid, block, 0, st>>>(p, n, part, nparts, out, e_out, status_out);
     });
     return check_launch("dfp8_from_float");
 }
