@@ -566,7 +566,10 @@ class ResidualMlp:
         self.e = torch.zeros(6, dtype=i32, device=dev)
         # largest magnitudes: norm output, hidden activation, W1, W2 (float32 bits)
         self.top = torch.zeros(4, dtype=i32, device=dev)
-        self.status = torch.zeros(2, dtype=i32, device=dev)  # of the last backward's errors
+        # as dfp8_from_float leaves it: of the last backward's errors, and of
+        # the last norm output, hidden activation, W1 and W2
+        self.status = torch.zeros(2, dtype=i32, device=dev)
+        self.operand_status = torch.zeros(4, dtype=i32, device=dev)
         self.h, self.h8, self.mean, self.rstd = new(B, D), new(B, D, dt=i8), new(B, dt=f32), new(B, dt=f32)
         self.z, self.a, self.a8, self.y = new(B, H), new(B, H), new(B, H, dt=i8), new(B, D)
         self.da, self.dh, self.dx = new(B, H), new(B, D), new(B, D)
@@ -582,19 +585,20 @@ class ResidualMlp:
         self.opt.bind_grads([self.gW1, self.gW2])
         self.opt_vectors = AdamW.make([b1, b2, gamma, beta], weight_decay=0.0, **kw)
         self.opt_vectors.bind_grads([self.gb1, self.gb2, self.ggamma, self.gbeta])
-        ops.dfp8_from_float(W1, self.W1_8, self.e[2:3], workspace=self.ws)
-        ops.dfp8_from_float(W2, self.W2_8, self.e[3:4], workspace=self.ws)
+        st = self.operand_status
+        ops.dfp8_from_float(W1, self.W1_8, self.e[2:3], workspace=self.ws, status_out=st[2:3])
+        ops.dfp8_from_float(W2, self.W2_8, self.e[3:4], workspace=self.ws, status_out=st[3:4])
 
     def forward(self, x, stream=None):
         """y of a batch x [B][D]; keeps what backward() reads."""
-        e, top, kw = self.e, self.top, dict(stream=stream)
+        e, top, st, kw = self.e, self.top, self.operand_status, dict(stream=stream)
         ops.ionn_fill_u32(top, 0, **kw)
         ops.ionn_layer_norm_fwd(x, self.h, gamma=self.gamma, beta=self.beta, eps=self.eps, mean=self.mean,
                                 rstd=self.rstd, absmax_y=top[0:1], **kw)
-        ops.dfp8_from_float(self.h, self.h8, e[0:1], absmax=top[0:1], **kw)
+        ops.dfp8_from_float(self.h, self.h8, e[0:1], absmax=top[0:1], status_out=st[0:1], **kw)
         ops.dfp8_linear_fwd(self.h8, e[0:1], self.W1_8, e[2:3], self.a, bias=self.b1, act=self.act, Z=self.z,
                             absmax_Y=top[1:2], workspace=self.ws, **kw)
-        ops.dfp8_from_float(self.a, self.a8, e[1:2], absmax=top[1:2], **kw)
+        ops.dfp8_from_float(self.a, self.a8, e[1:2], absmax=top[1:2], status_out=st[1:2], **kw)
         ops.dfp8_linear_fwd(self.a8, e[1:2], self.W2_8, e[3:4], self.y, bias=self.b2, residual=x, workspace=self.ws,
                             **kw)
         return self.y
@@ -614,5 +618,6 @@ class ResidualMlp:
         """The optimiser step on the last backward's gradients, and the new DFP-8 weights."""
         self.opt.step(absmax_P=self.top[2:4], stream=stream)
         self.opt_vectors.step(stream=stream)
-        ops.dfp8_from_float(self.W1, self.W1_8, self.e[2:3], absmax=self.top[2:3], stream=stream)
-        ops.dfp8_from_float(self.W2, self.W2_8, self.e[3:4], absmax=self.top[3:4], stream=stream)
+        st = self.operand_status
+        ops.dfp8_from_float(self.W1, self.W1_8, self.e[2:3], absmax=self.top[2:3], status_out=st[2:3], stream=stream)
+        ops.dfp8_from_float(self.W2, self.W2_8, self.e[3:4], absmax=self.top[3:4], status_out=st[3:4], stream=stream)

@@ -1,0 +1,49 @@
+"""GPU: what the residual MLP block and the optimiser report and keep: the
+status of every 8-bit operand, updates without a forward pass between them,
+and refused optimiser steps."""
+import pytest
+import torch
+
+from gpu_helpers import dev, host, say
+from integer_only_nn_amd import ops, steps
+from test_gpu_residual_mlp import _block
+
+pytestmark = pytest.mark.gpu
+
+
+def _forward(blk, x, dtype):
+    blk.forward(x.to(dev()).to(dtype))
+    return host(blk.operand_status).tolist()
+
+
+def test_operands_report_what_is_not_finite():
+    """operand_status: norm output, hidden activation, W1, W2."""
+    blk, x, dy = _block(20, 64, 96, dtype=torch.float16)
+    assert _forward(blk, x, torch.float16) == [0, 0, 0, 0]
+    # an activation that float16 cannot hold
+    blk.b1[5] = 1e5
+    assert _forward(blk, x, torch.float16) == [0, 2, 0, 0]
+    blk.b1[5] = 0.0
+    blk.gamma[3] = float("nan")
+    assert _forward(blk, x, torch.float16)[0] == 2
+    blk.gamma[3] = 1.0
+    assert _forward(blk, x, torch.float16) == [0, 0, 0, 0]  # no state is left over
+
+
+def test_updated_weights_report_what_is_not_finite():
+    blk, x, dy = _block(20, 64, 96, lr=1e-3)
+    x, dy = x.to(dev()).bfloat16(), dy.to(dev()).bfloat16()
+    blk.forward(x)
+    blk.backward(x, dy)
+    blk.update()
+    assert host(blk.operand_status).tolist() == [0, 0, 0, 0]
+    blk.gW2[7, 9] = float("inf")
+    blk.update()
+    assert host(blk.operand_status).tolist()[2:] == [0, 2]
+
+
+def test_first_weights_report_what_is_not_finite():
+    p = [torch.ones(s, device=dev()) for s in ((96, 64), (96,), (64, 96), (64,), (64,), (64,))]
+    p[0][2, 3] = float("inf")
+    blk = steps.ResidualMlp(*p, B=4)
+    assert host(blk.operand_status).tolist()[2:] == [2, 0]
