@@ -592,7 +592,7 @@ class ResidualMlp:
     def forward(self, x, stream=None):
         """y of a batch x [B][D]; keeps what backward() reads."""
         e, top, st, kw = self.e, self.top, self.operand_status, dict(stream=stream)
-        ops.ionn_fill_u32(top, 0, **kw)
+        ops.ionn_fill_u32(top[0:2], 0, **kw)
         ops.ionn_layer_norm_fwd(x, self.h, gamma=self.gamma, beta=self.beta, eps=self.eps, mean=self.mean,
                                 rstd=self.rstd, absmax_y=top[0:1], **kw)
         ops.dfp8_from_float(self.h, self.h8, e[0:1], absmax=top[0:1], status_out=st[0:1], **kw)
@@ -616,6 +616,7 @@ class ResidualMlp:
 
     def update(self, stream=None):
         """The optimiser step on the last backward's gradients, and the new DFP-8 weights."""
+        ops.ionn_fill_u32(self.top[2:4], 0, stream=stream)
         self.opt.step(absmax_P=self.top[2:4], stream=stream)
         self.opt_vectors.step(stream=stream)
         st = self.operand_status

@@ -47,3 +47,23 @@ def test_first_weights_report_what_is_not_finite():
     p[0][2, 3] = float("inf")
     blk = steps.ResidualMlp(*p, B=4)
     assert host(blk.operand_status).tolist()[2:] == [2, 0]
+
+
+def test_updates_without_a_forward_pass_between_them():
+    """Each update's 8-bit weights go by the weights' own maximum, not by an earlier one."""
+    blk, x, dy = _block(20, 64, 96, lr=1e-3)
+    x, dy = x.to(dev()).bfloat16(), dy.to(dev()).bfloat16()
+    blk.forward(x)
+    blk.backward(x, dy)
+    ws = torch.empty(ops.dfp8_from_float_workspace_bytes(), dtype=torch.uint8, device=dev())
+    for scale in (1.0, 2.0 ** -6, 2.0 ** -3):
+        blk.W1.mul_(scale)
+        blk.W2.mul_(scale)
+        blk.update()
+        for W, q, e in ((blk.W1, blk.W1_8, blk.e[2]), (blk.W2, blk.W2_8, blk.e[3])):
+            out, eo = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device=dev())
+            ops.dfp8_from_float(W, out, eo, workspace=ws)
+            assert int(e) == int(eo) and torch.equal(q, out), scale
+    blk.forward(x)  # (clears its own maxima only)
+    top = host(blk.top).view("float32")
+    assert abs(top[2] / float(blk.W1.abs().max()) - 1) < 1e-6 and top[0] > 0 and top[1] > 0
