@@ -514,23 +514,30 @@ class AdamW:
             self.bind_grads(Gs)
         if self._G is None:
             raise ValueError("no gradient buffers")
-        if self.step_dev is not None:
-            if stream is None:
-                self.step_dev.add_(1)
-            else:
-                on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-                with torch.cuda.stream(on):
-                    self.step_dev.add_(1)
-        self.t += 1
         name = "ionn_adamw_step" if self.R is None else "ionn_adamw_step_carried"
-        rc = getattr(ops.lib(), name)(
-            len(self.P), self._Pp, self._G[1], self._G[2], *self._states, self._n, self.t,
-            self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-            ops._s(self.step_dev, torch.int32, "step"), ops._s(self.lr_dev, torch.float32, "lr_dev"),
-            ops._s(grad_scale, torch.float32, "grad_scale"), ops._v(absmax_P, torch.int32, len(self.P), "absmax_P"),
-            ops._on(stream, self.P[0]))
-        if rc:
+        call = getattr(ops.lib(), name)
+        args = (len(self.P), self._Pp, self._G[1], self._G[2], *self._states, self._n, self.t + 1,
+                self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                ops._s(self.step_dev, torch.int32, "step"), ops._s(self.lr_dev, torch.float32, "lr_dev"),
+                ops._s(grad_scale, torch.float32, "grad_scale"), ops._v(absmax_P, torch.int32, len(self.P), "absmax_P"),
+                ops._on(stream, self.P[0]))
+        self._count(1, stream)
+        rc = call(*args)
+        if rc:  # (not a step: neither count keeps it)
+            self._count(-1, stream)
             ops.check(rc, name)
+        self.t += 1
+
+    def _count(self, by, stream):
+        """Moves the count on the device, if there is one."""
+        if self.step_dev is None:
+            return
+        if stream is None:
+            self.step_dev.add_(by)
+            return
+        on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(on):
+            self.step_dev.add_(by)
 
 
 # ---------------------------------------------------------------------------

@@ -67,3 +67,34 @@ def test_updates_without_a_forward_pass_between_them():
     blk.forward(x)  # (clears its own maxima only)
     top = host(blk.top).view("float32")
     assert abs(top[2] / float(blk.W1.abs().max()) - 1) < 1e-6 and top[0] > 0 and top[1] > 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_refused_steps_are_not_counted(bits, on_device):
+    z = lambda n: torch.zeros(n, device=dev())  # noqa: E731
+    P = torch.ones(300, device=dev())
+    opt = steps.AdamW.make([P], bits=bits, on_device=on_device)
+    g = torch.full((300,), 0.5, device=dev())
+    opt.step([g])
+    w = P.clone()
+
+    def counts():
+        return opt.t, int(opt.step_dev) if on_device else None
+
+    assert counts() == (1, 1 if on_device else None)
+    eps, opt.eps = opt.eps, -1.0
+    say("refused", bits, on_device)
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(RuntimeError, match="eps"):
+            opt.step([g], stream=stream)  # refused by the library
+    opt.eps = eps
+    with pytest.raises(ValueError):
+        opt.step([z(299)])  # refused by the class
+    with pytest.raises(TypeError):
+        opt.step([g], grad_scale=torch.ones(1, device=dev(), dtype=torch.float64))  # and by the binding
+    with pytest.raises(ValueError):
+        opt.step([g], absmax_P=torch.zeros(2, dtype=torch.int32, device=dev()))
+    assert counts() == (1, 1 if on_device else None) and torch.equal(P, w)
+    opt.step([g])
+    assert counts() == (2, 2 if on_device else None)
