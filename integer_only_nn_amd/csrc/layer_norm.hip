@@ -238,10 +238,18 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void norm_bwd_kernel(
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) h[i][e] = (float(rx[i][e]) - mu) * rs;
+            // past the row's end dy is 0, and so is every sum's term where h is
+            // finite, which mu rs need not be
+            if (cols - c < VE) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (c + e >= cols) h[i][e] = 0.0f;
+            }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                // (past the row's end dy is 0, and so is every sum's term)
-                h[i][e] = (float(rx[i][e]) - mu) * rs;
                 const float a = float(ry[i][e]);
                 sg[i][e] += a * h[i][e];
                 sb[i][e] += a;
@@ -323,7 +331,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(const T *dy, const 
             for (int e = 0; e < VE; ++e) {
                 const float d = float(ry[e]) * (gamma && e < valid ? gamma[c + e] : 1.0f);
                 s1 += d;
-                s2 += d * ((float(rx[e]) - mu) * rs);
+                s2 += d * (e < valid ? (float(rx[e]) - mu) * rs : 0.0f);
             }
         }
         const float c1 = row_sum<1024>(s1, buf, ph) / n_cols;
