@@ -726,7 +726,8 @@ int dfp8_from_float(const void *x, int dtype, int64_t n, const uint32_t *absmax,
  * receives z for the backward pass.  absmax_Y (nullable): device uint32,
  * max-combined with the float32 bits of |Y| before its rounding (a NaN counts
  * above every number), to be rounded by dfp8_from_float.  B, OUT in
- * [0, 2^30]; 0 <= IN <= IONN_DFP8_MAX_REDUCTION (IN = 0: the sum is 0).
+ * [0, 2^30], of fewer than 2^24 tiles of 64 x 64 where the output is cut into
+ * them; 0 <= IN <= IONN_DFP8_MAX_REDUCTION (IN = 0: the sum is 0).
  * workspace: 16-byte aligned, dfp8_linear_fwd_workspace_bytes(B, IN, OUT)
  * bytes (may be 0). */
 size_t dfp8_linear_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT);
@@ -747,7 +748,8 @@ int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W,
  * [B][IN]; G (nullable): dtype [OUT][IN]; gb (nullable): float [OUT].
  * status_out (nullable, device int32): as in dfp8_from_float, for dZ.
  * B, IN, OUT in [0, 2^30]; OUT <= IONN_DFP8_MAX_REDUCTION with dX, B <= it
- * with G.
+ * with G; the gradients, together, of fewer than 2^24 tiles of 64 x 64 where
+ * they are cut into them.
  * B = 0 writes G = 0 and gb = 0; OUT = 0 writes dX = 0; edZ = 0 either way.
  * workspace: 16-byte aligned, dfp8_linear_bwd_workspace_bytes(B, IN, OUT)
  * bytes. */
@@ -822,7 +824,8 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
  * kernel runs; the caller advances them.  grad_scale (nullable, device
  * float): 1.  absmax_P (nullable, device uint32 [L]): max-combined with the
  * float32 bits of |P| after the step, for dfp8_from_float.
- * L >= 1; P, G, M, V, S, n are HOST arrays; 1 <= n[l] <= 2^40.
+ * L >= 1; P, G, M, V, S, n are HOST arrays; 1 <= n[l] <= 2^35 - 2^12 (8-bit
+ * states; twice that in 32 bits).
  * 0 <= beta1, beta2 < 1; eps >= 0; lr and weight_decay finite. */
 #define IONN_ADAMW_BLOCK 256
 int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype,

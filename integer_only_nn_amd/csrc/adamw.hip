@@ -47,7 +47,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTable = 60;                                   // tensors per launch (their table is an argument: 4 KiB)
-constexpr int64_t kMaxElems = int64_t(1) << 40;
 static_assert(IONN_ADAMW_BLOCK == 256, "a block is 64 lanes of four weights");
 
 // How the moments are held: float32, codes, codes with the root's remainder.
@@ -396,9 +395,11 @@ static int adamw(const char *what, int L, float *const *P, const void *const *G,
     IONN_REQUIRE(aligned(step, 4) && aligned(lr_dev, 4) && aligned(grad_scale, 4) && aligned(absmax_P, 4),
                  IONN_ERR_ALIGN, "%s: device scalars must be 4-byte aligned", what);
     const size_t gs = dtype_size(g_dtype), ss = state_bits == 32 ? 4 : 1;
+    const int64_t per = elems_of_group(state_bits == 32 ? WORDS : CODES);
+    static_assert(elems_of_group(CODES) == elems_of_group(CARRIED), "one layout of the 8-bit states");
     for (int l = 0; l < L; ++l) {
-        IONN_REQUIRE(n[l] >= 1 && n[l] <= kMaxElems, IONN_ERR_SHAPE, "%s: tensor %d has n = %lld", what, l,
-                     (long long)n[l]);
+        IONN_REQUIRE(n[l] >= 1 && n[l] <= per * max_groups(kThreads), IONN_ERR_SHAPE, "%s: tensor %d has n = %lld",
+                     what, l, (long long)n[l]);
         IONN_REQUIRE(P[l] && G[l] && M[l] && V[l] && (state_bits == 32 || S[l]), IONN_ERR_ARG,
                      "%s: tensor %d has a NULL pointer", what, l);
         IONN_REQUIRE(aligned(P[l], 4) && aligned(G[l], gs) && aligned(M[l], ss) && aligned(V[l], ss), IONN_ERR_ALIGN,
@@ -407,8 +408,6 @@ static int adamw(const char *what, int L, float *const *P, const void *const *G,
     Hyper h{lr, beta1, beta2, eps, weight_decay, t, step, lr_dev, grad_scale, nullptr};
     const Factors f = make_factors(h, t < 1 ? 1 : t, lr);
     hipStream_t st = as_stream(stream);
-    const int64_t per = elems_of_group(state_bits == 32 ? WORDS : CODES);
-    static_assert(elems_of_group(CODES) == elems_of_group(CARRIED), "one layout of the 8-bit states");
     int l = 0;
     while (l < L) {
         Table tab;
@@ -418,7 +417,7 @@ static int adamw(const char *what, int L, float *const *P, const void *const *G,
         int k = 0;
         for (; k < kTable && l < L; ++k, ++l) {
             const int64_t b = (n[l] + per - 1) / per;
-            if (blocks + b > 0x7fffffff) break;  // (a single tensor has at most 2^29)
+            if (blocks + b > max_groups(kThreads)) break;  // (one tensor alone never is)
             tab.P[k] = P[l];
             tab.G[k] = G[l];
             tab.M[k] = M[l];

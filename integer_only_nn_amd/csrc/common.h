@@ -52,6 +52,9 @@ inline int device_cus() {
     return v;
 }
 
+// The runtime takes fewer than 2^32 threads along a dimension of a grid.
+constexpr int64_t max_groups(int threads) { return int64_t(0xffffffffu) / threads; }
+
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 // ---------------------------------------------------------------------------

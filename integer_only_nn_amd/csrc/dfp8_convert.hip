@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void act_sums_kernel(const T *__restrict_
 }
 
 // Workgroups below n_round round the errors; those from it on add up the
-// chunks' column sums, 64 columns each, every fourth chunk per wavefront.
+// chunks' column sums, 64 columns at a time, every fourth chunk per wavefront.
 template <class T, int ACT>
 __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict__ dY, const T *__restrict__ Z,
                                                              int64_t n, int OUT, const uint32_t *__restrict__ part_max,
@@ -169,15 +169,19 @@ __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict
     if (int(blockIdx.x) >= n_round) {
         __shared__ float red[kThreads / 64][64];
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int64_t c = int64_t(int(blockIdx.x) - n_round) * 64 + lane;
-        float s = 0.0f;
-        if (c < OUT) {
+        const int64_t step = (int64_t(gridDim.x) - n_round) * 64;
+        for (int64_t c0 = int64_t(int(blockIdx.x) - n_round) * 64; c0 < OUT; c0 += step) {
+            const int64_t c = c0 + lane;
+            float s = 0.0f;
+            if (c < OUT) {
 #pragma unroll 8
-            for (int k = wave; k < chunks; k += kThreads / 64) s += part_sum[int64_t(k) * OUT + c];
+                for (int k = wave; k < chunks; k += kThreads / 64) s += part_sum[int64_t(k) * OUT + c];
+            }
+            red[wave][lane] = s;
+            __syncthreads();
+            if (wave == 0 && c < OUT) gb[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+            __syncthreads();
         }
-        red[wave][lane] = s;
-        __syncthreads();
-        if (wave == 0 && c < OUT) gb[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
         return;
     }
     const uint32_t m = all_max(part_max, nparts);
@@ -371,7 +375,8 @@ int launch_act_bwd(const void *dY, const void *Z, int act, int dtype, int64_t B,
     const bool one = a.strips * groups <= kOneValues / int64_t(16 / dtype_size(dtype)) &&
                      B * OUT >= int64_t(16 / dtype_size(dtype));
     const unsigned n_round = pass_groups(B * OUT, dtype_size(dtype), 2048);
-    const unsigned n_sum = gb ? unsigned((OUT + 63) / 64) : 0u;
+    // (at most 2^20: one for each 64 of 2^30 columns and the others would be too many threads)
+    const unsigned n_sum = gb ? unsigned(OUT <= int64_t(64) << 20 ? (OUT + 63) / 64 : int64_t(1) << 20) : 0u;
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
         const T *y = static_cast<const T *>(dY), *z = static_cast<const T *>(Z);

@@ -63,12 +63,14 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
     // 16384 18.7 against 16.9).
     if (forward && K >= kRowsMinK) {
         const auto fits = [&](int rows, int cols) { return ceil_div(M, 16 * rows) * ceil_div(N, 16 * cols) <= 256; };
+        // (a grid of more threads than the runtime takes: B = 1, IN = 16, 2^27 outputs)
+        const auto starts = [&](int cols) { return ceil_div(N, 16 * cols) <= max_groups(kRowWaves * 64); };
         if (K <= 16384 && fits(1, 1)) p.rows = 1, p.cols = 1;
         else if (K <= 16384 && fits(1, 2)) p.rows = 1, p.cols = 2;
         else if (K <= 8192 && fits(2, 2)) p.rows = 2, p.cols = 2;
         else if (K <= 8192 && K >= 512 && fits(4, 2)) p.rows = 4, p.cols = 2;
-        else if (M <= 8 && N > 4096) p.rows = 1, p.cols = 1;
-        else if (M <= 16 && K <= 16384) p.rows = 1, p.cols = 2;
+        else if (M <= 8 && N > 4096 && starts(1)) p.rows = 1, p.cols = 1;
+        else if (M <= 16 && K <= 16384 && starts(2)) p.rows = 1, p.cols = 2;
         else if (M <= 32 && K <= 16384 && N <= 16384) p.rows = 2, p.cols = 2;
         if (p.rows) {
             p.path = ROWS;
@@ -202,7 +204,28 @@ void launch_backward(const Plan &pd, Product d, const Plan &pg, Product g, hipSt
     if (sd + sg) sum_pair_kernel<T><<<dim3(sd + sg), block, 0, st>>>(d, g, int(sd));
 }
 
-// (twice: the two products of a backward pass share a grid)
+// The workgroups of a product, on the path that it takes.
+int64_t groups_of(const Plan &pl, const Product &p) {
+    const Path path = path_of(pl, p.A, p.B);
+    if (path == ROWS) return ceil_div(p.N, 16 * pl.cols);
+    const int side = path == TILE256 ? 256 : path == TILE128 ? 128 : 64;
+    return ceil_div(p.M, side) * ceil_div(p.N, side) * (side == 64 ? pl.split : 1);
+}
+
+// Whether their launches are within what the runtime takes.
+bool launches(const Plan &pl, const Product &p) {
+    return groups_of(pl, p) <= max_groups(path_of(pl, p.A, p.B) == ROWS ? kRowWaves * 64 : NT);
+}
+bool launches(const Plan &pd, const Product &d, const Plan &pg, const Product &g) {
+    if (!d.blocks || !g.blocks) return (!d.blocks || launches(pd, d)) && (!g.blocks || launches(pg, g));
+    const Path path = path_of(pd, d.A, d.B);
+    if ((path == TILE || path == TILE128) && path == path_of(pg, g.A, g.B))  // in one grid
+        return groups_of(pd, d) + groups_of(pg, g) <= max_groups(NT);
+    return launches(pd, d) && launches(pg, g);
+}
+
+// (products whose tiles can be counted; twice: the two products of a backward
+// pass share a grid)
 bool tiles_ok(int64_t M, int64_t N) { return 2 * ceil_div(M, 64) * ceil_div(N, 64) <= 0x7fffffff; }
 
 // edZ = 0 (and status 0) for an empty error; G and gb of an empty batch, dX
@@ -253,6 +276,8 @@ int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const i
     const Epi ep{eX, eW, bias, residual, Z, Y, absmax_Y, act};
     const Plan plan = make_plan<true, true>(B, OUT, IN, true);
     const Product p = make_product(plan, X, IN, W, IN, ep, B, OUT, IN, workspace);
+    IONN_REQUIRE(launches(plan, p), IONN_ERR_SHAPE, "dfp8_linear_fwd: B=%lld OUT=%lld have too many tiles",
+                 (long long)B, (long long)OUT);
     with_dtype(dtype, [&](auto tag) { launch_forward<decltype(tag)>(plan, p, as_stream(stream)); });
     return check_launch("dfp8_linear_fwd");
 }
@@ -299,16 +324,18 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype, const int
         zero_bytes(gb, OUT * 4, st);
         return check_launch("dfp8_linear_bwd");
     }
-    if (int rc = launch_act_bwd(dY, Z, act, dtype, B, OUT, dZ8, edZ, gb, status_out, workspace, st)) return rc;
-    if (IN == 0) return IONN_OK;
     char *parts = static_cast<char *>(workspace) + act_workspace_bytes(B, OUT);
     const Plan pd = make_plan<true, false>(B, IN, OUT, false), pg = make_plan<false, false>(OUT, IN, B, false);
     const Epi ed{edZ, eW, nullptr, nullptr, nullptr, dX, nullptr, IONN_ACT_NONE};
     const Epi eg{edZ, eX, nullptr, nullptr, nullptr, G, nullptr, IONN_ACT_NONE};
     Product d = make_product(pd, dZ8, OUT, W, IN, ed, B, IN, OUT, parts);
     Product g = make_product(pg, dZ8, OUT, X, IN, eg, OUT, IN, B, parts + part_bytes(pd, B, IN));
-    if (!dX) d.blocks = 0;
-    if (!G) g.blocks = 0;
+    if (!dX || IN == 0) d.blocks = 0;
+    if (!G || IN == 0) g.blocks = 0;
+    IONN_REQUIRE(launches(pd, d, pg, g), IONN_ERR_SHAPE, "dfp8_linear_bwd: B=%lld IN=%lld OUT=%lld have too many tiles",
+                 (long long)B, (long long)IN, (long long)OUT);
+    if (int rc = launch_act_bwd(dY, Z, act, dtype, B, OUT, dZ8, edZ, gb, status_out, workspace, st)) return rc;
+    if (IN == 0) return IONN_OK;
     with_dtype(dtype, [&](auto tag) { launch_backward<decltype(tag)>(pd, d, pg, g, st); });
     return check_launch("dfp8_linear_bwd");
 }

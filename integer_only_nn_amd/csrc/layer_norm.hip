@@ -378,27 +378,33 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_cols_kernel(const T *__rest
     store_vec<float, VE>(p + cols, sb, valid);
 }
 
-// The partial rows added up: 64 columns (of the 2 * cols) per workgroup, each
-// by 16 threads that take every 16th partial row, then those 16 in order.
+// The partial rows added up: 64 columns (of the 2 * cols) at a time per
+// workgroup, each by 16 threads that take every 16th partial row, then those 16
+// in order.
 constexpr int kSumGroups = 16;
+constexpr int64_t kSumBlocks = 65536;  // at most (one for each 64 of 2^28 sums would be too many threads to launch)
 __global__ __launch_bounds__(64 * kSumGroups) void norm_sum_kernel(const float *__restrict__ part, int nparts,
                                                                    int64_t cols, float *__restrict__ dgamma,
                                                                    float *__restrict__ dbeta) {
     __shared__ float red[kSumGroups][64];
     const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    const int64_t c = int64_t(blockIdx.x) * 64 + lane;
-    float s = 0.0f;
-    if (c < 2 * cols) {
+    for (int64_t c0 = int64_t(blockIdx.x) * 64; c0 < 2 * cols; c0 += int64_t(gridDim.x) * 64) {
+        const int64_t c = c0 + lane;
+        float s = 0.0f;
+        if (c < 2 * cols) {
 #pragma unroll 16
-        for (int p = grp; p < nparts; p += kSumGroups) s += part[int64_t(p) * 2 * cols + c];
-    }
-    red[grp][lane] = s;
-    __syncthreads();
-    if (grp > 0 || c >= 2 * cols) return;
+            for (int p = grp; p < nparts; p += kSumGroups) s += part[int64_t(p) * 2 * cols + c];
+        }
+        red[grp][lane] = s;
+        __syncthreads();
+        if (grp == 0 && c < 2 * cols) {
 #pragma unroll
-    for (int k = 1; k < kSumGroups; ++k) s += red[k][lane];
-    float *out = c < cols ? dgamma : dbeta;
-    if (out) out[c < cols ? c : c - cols] = s;
+            for (int k = 1; k < kSumGroups; ++k) s += red[k][lane];
+            float *out = c < cols ? dgamma : dbeta;
+            if (out) out[c < cols ? c : c - cols] = s;
+        }
+        __syncthreads();
+    }
 }
 
 // f(threads per row, vectors per thread) for a row of cols columns that fits
@@ -546,7 +552,8 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean, const 
         if (int rc = check_launch("ionn_layer_norm_bwd")) return rc;
     }
     if (sums) {
-        norm_sum_kernel<<<dim3(unsigned((2 * cols + 63) / 64)), dim3(64 * kSumGroups), 0, st>>>(
+        const int64_t blocks = (2 * cols + 63) / 64;
+        norm_sum_kernel<<<dim3(unsigned(blocks < kSumBlocks ? blocks : kSumBlocks)), dim3(64 * kSumGroups), 0, st>>>(
             part, int(groups), cols, dgamma, dbeta);
         return check_launch("ionn_layer_norm_bwd");
     }
