@@ -761,6 +761,21 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype,
                     int32_t *status_out, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/* How a product of that layer is cut, by its sizes: the forward product, dX or
+ * G (product 0, 1 or 2), IONN_DFP8_ROWS: small tiles, the reduction cut among
+ * a workgroup's wavefronts; _TILES_256, _TILES_128: tiles of that side, of
+ * operands whose addresses are multiples of 16 (others take _TILES);
+ * _TILES: tiles of 64, in ranges of the reduction where there are few;
+ * _NARROW: the same for contiguous sides below 16.  -1: sizes out of range. */
+enum {
+    IONN_DFP8_ROWS = 0,
+    IONN_DFP8_TILES_256 = 1,
+    IONN_DFP8_TILES_128 = 2,
+    IONN_DFP8_TILES = 3,
+    IONN_DFP8_NARROW = 4
+};
+int dfp8_linear_path(int product, int64_t B, int64_t IN, int64_t OUT);
+
 /* Layer norm over the rows of x:
  *   mean[r] = sum_c x[r][c] / cols, rstd[r] = 1 / sqrt(sum_c (x[r][c] -
  *   mean[r])^2 / cols + eps),

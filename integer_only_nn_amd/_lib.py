@@ -79,6 +79,7 @@ SIGNATURES = {
     "dfp8_linear_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "dfp8_linear_bwd": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P,
                              ctypes.c_size_t, _P]),
+    "dfp8_linear_path": (_I, [_I, _I64, _I64, _I64]),
     "ionn_layer_norm_fwd": (_I, [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I, _I64, _I64, _P, _P]),
     "ionn_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "ionn_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _P, ctypes.c_size_t, _P]),

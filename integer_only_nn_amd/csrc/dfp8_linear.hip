@@ -32,7 +32,13 @@ bool sizes_ok(int64_t B, int64_t IN, int64_t OUT) {
 
 // ---- how a product is cut ------------------------------------------------------
 
-enum Path { ROWS, TILE256, TILE128, TILE, TINY };
+enum Path {
+    ROWS = IONN_DFP8_ROWS,
+    TILE256 = IONN_DFP8_TILES_256,
+    TILE128 = IONN_DFP8_TILES_128,
+    TILE = IONN_DFP8_TILES,
+    TINY = IONN_DFP8_NARROW
+};
 
 struct Plan {
     Path path;
@@ -280,6 +286,12 @@ int dfp8_linear_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const i
                  (long long)B, (long long)OUT);
     with_dtype(dtype, [&](auto tag) { launch_forward<decltype(tag)>(plan, p, as_stream(stream)); });
     return check_launch("dfp8_linear_fwd");
+}
+
+int dfp8_linear_path(int product, int64_t B, int64_t IN, int64_t OUT) {
+    if (product < 0 || product > 2 || !sizes_ok(B, IN, OUT)) return -1;
+    if (product == 0) return make_plan<true, true>(B, OUT, IN, true).path;
+    return product == 1 ? make_plan<true, false>(B, IN, OUT, false).path : make_plan<false, false>(OUT, IN, B, false).path;
 }
 
 size_t dfp8_linear_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT) {

@@ -676,6 +676,14 @@ def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None
         check(rc, "dfp8_linear_bwd")
 
 
+def dfp8_linear_path(product, B, IN, OUT):
+    """"rows", "tiles 256", "tiles 128", "tiles" or "narrow", for product "fwd", "dX" or "G"."""
+    p = lib().dfp8_linear_path(("fwd", "dX", "G").index(product), int(B), int(IN), int(OUT))
+    if p < 0:
+        raise ValueError(f"B = {B}, IN = {IN}, OUT = {OUT}")
+    return ("rows", "tiles 256", "tiles 128", "tiles", "narrow")[p]
+
+
 def ionn_layer_norm_fwd(x, y, gamma=None, beta=None, eps=1e-5, mean=None, rstd=None, absmax_y=None, stream=None):
     xs, dt = x.shape, x.dtype
     rows, cols = xs
