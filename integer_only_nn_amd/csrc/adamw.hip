@@ -13,9 +13,10 @@
 // every access is a contiguous run and a chunk is one 8-bit block: its largest
 // magnitude is a reduction inside the wavefront, and no state is read twice.
 // Measured: 67.1 M weights with bfloat16 gradients and float32 states 324 us
-// (1745 MB, 5.4 TB/s; a 1 GiB copy reaches 5.2), 8-bit states 194 us (940 MB, 4.8
-// TB/s), with remainders 231 us (1075 MB, 4.7 TB/s); 20 tensors of 268 k weights
-// with float32 states 6.2 us, one launch.
+// (1745 MB, 5.4 TB/s; a 1 GiB copy reaches 5.2), 8-bit states 184 us (940 MB, 5.1
+// TB/s), with remainders 226 us (1075 MB, 4.8 TB/s: about 130 instructions per
+// weight, of which the two exact roots and the division are 50, take as long as
+// the bytes); 20 tensors of 268 k weights with float32 states 6.2 us, one launch.
 //
 // 8-bit states are E4M3 codes with one power-of-two exponent per block of
 // 256.  The second moment is kept as its root r = sqrt(v): E4M3 spans 2^18
@@ -54,8 +55,8 @@ enum States { WORDS, CODES, CARRIED };
 
 // Chunks of 256 weights per wavefront.  The 8-bit states' arithmetic takes
 // nearly as long as their bytes, and overlaps them better from more and
-// smaller wavefronts: with 4, 2 and 1 chunks 242, 228 and 222 us (remainders, 67.1
-// M weights), but 249, 248 and 260 where each wavefront also forms the factors
+// smaller wavefronts: with 4, 2 and 1 chunks 231, 223 and 213 us (remainders, 67.1
+// M weights), but 244, 241 and 253 where each wavefront also forms the factors
 // from a count on the device.
 constexpr int chunks_of(int states) { return states == WORDS ? 4 : 2; }
 constexpr int elems_of_wave(int states) { return chunks_of(states) * IONN_ADAMW_BLOCK; }
@@ -132,19 +133,20 @@ __device__ __forceinline__ float next_root(const Factors &f, float g, float v) {
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // e in [-126, 127]
 
-// The exponent of a block from the bits of its largest finite magnitude f 2^q.
-__device__ __forceinline__ int block_exponent(uint32_t bits) {
-    const int e = int(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return bits == 0u ? 0 : (e < -126 ? -126 : e);
+// A number that orders as the exponents of blocks whose largest magnitude is x
+// = f 2^q do (0: an all-zero block; the addition carries where f > 1.75), and the
+// exponent that it stands for.
+__device__ __forceinline__ uint32_t exponent_key(float x) {
+    const uint32_t bits = __float_as_uint(x);
+    return ((bits + 0x1fffffu) >> 23) + min(bits, 1u);
 }
+__device__ __forceinline__ int block_exponent(uint32_t key) { return key == 0u ? 0 : max(int(key) - 136, -126); }
 
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t b = mag_bits(x);
-    return b < 0x7f800000u ? b : 0u;
-}
+__device__ __forceinline__ bool finite(float x) { return mag_bits(x) < 0x7f800000u; }
 
-// Four E4M3 codes of a dword as floats, and back (to nearest even; the
-// values are within the format's range; a NaN or an infinity becomes code 0x7f).
+// Four E4M3 codes of a dword as floats, and back (to nearest even; the values
+// are within the format's range; where some may not be finite, those become
+// code 0x7f).
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
     typedef float v2f __attribute__((ext_vector_type(2)));
     const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
@@ -154,16 +156,13 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
     x[3] = hi.y;
 }
 
-__device__ __forceinline__ uint32_t encode4(const float (&x)[4]) {
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], bool all_finite) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, mag_bits(x[i]));
-    if (top >= 0x7f800000u) {
+    if (!all_finite) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (mag_bits(x[i]) >= 0x7f800000u) w = (w & ~(0xff << (8 * i))) | 0x7f << (8 * i);
+            if (!finite(x[i])) w = (w & ~(0xff << (8 * i))) | 0x7f << (8 * i);
     }
     return uint32_t(w);
 }
@@ -193,8 +192,8 @@ struct Grid {
     float step, inverse;
 };
 __device__ __forceinline__ Grid grid_of(float a) {
-    const uint32_t e = max(__float_as_uint(a) >> 23, 121u);  // (2^-9 apart below 2^-6)
-    return Grid{__uint_as_float((e - 3u) << 23), __uint_as_float((257u - e) << 23)};
+    const uint32_t e = max(__float_as_uint(a) & 0x7f800000u, 121u << 23);  // (2^-9 apart below 2^-6)
+    return Grid{__uint_as_float(e - (3u << 23)), __uint_as_float((257u << 23) - e)};
 }
 
 // The E4M3 value below or above s, above with probability (s^2 - lo^2) / (hi^2 - lo^2).
@@ -225,6 +224,15 @@ __device__ __forceinline__ int rest_of(float s, float c, float u) {
 #pragma clang fp contract(off)
     const float x = floorf((s - c) * (grid_of(c).inverse * 254.0f) + u);
     return int(__builtin_amdgcn_fmed3f(x, -127.0f, 127.0f));
+}
+
+// Both halves' largest over the wavefront.
+typedef uint16_t v2h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v2h wave_max(v2h v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        v = __builtin_elementwise_max(v, __builtin_bit_cast(v2h, __shfl_xor(__builtin_bit_cast(int, v), off, 64)));
+    return v;
 }
 
 // Four bytes at any address, the first `valid` of them.
@@ -321,13 +329,27 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
         }
         store_vec<float, 4>(P + i, pn, valid);
         if (Q8) {
-            uint32_t am = 0, av = 0;
+            // the block's largest finite magnitudes (past the tensor's end both
+            // moments are 0, and a maximum with a NaN is the other value)
+            float am = 0.0f, av = 0.0f;
+            bool odd = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                am = max(am, e < valid ? finite_bits(mn[e]) : 0u);
-                av = max(av, e < valid ? finite_bits(wn[e]) : 0u);
+                am = fmaxf(am, fabsf(mn[e]));
+                av = fmaxf(av, wn[e]);
+                odd |= !finite(mn[e] + wn[e]);
             }
-            const int xm = block_exponent(wave_max_u32(am)), xv = block_exponent(wave_max_u32(av));
+            const bool all_finite = __builtin_amdgcn_ballot_w64(odd) == 0;
+            if (!all_finite) {
+                am = av = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    am = fmaxf(am, finite(mn[e]) ? fabsf(mn[e]) : 0.0f);
+                    av = fmaxf(av, finite(wn[e]) ? wn[e] : 0.0f);
+                }
+            }
+            const v2h keys = wave_max(v2h{uint16_t(exponent_key(am)), uint16_t(exponent_key(av))});
+            const int xm = block_exponent(keys.x), xv = block_exponent(keys.y);
             float sm[4], sv[4], u[4];
             draw4(uint32_t(i >> 2), f.seed, u);
 #pragma unroll
@@ -343,15 +365,17 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, Hyper h, Fac
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sm[e] = round_mean(sm[e], u[e ^ 2]);
             }
-            const uint32_t codes = encode4(sv);
-            store4(M8 + i, encode4(sm), valid);
+            const uint32_t codes = encode4(sv, all_finite);
+            store4(M8 + i, encode4(sm, all_finite), valid);
             store4(V8 + i, codes, valid);
             if (STATES == CARRIED) {
                 decode4(codes, sv);
                 uint32_t w = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w |= (mag_bits(wn[e]) < 0x7f800000u ? uint32_t(rest_of(wn[e], sv[e], u[e])) & 0xffu : 0u) << (8 * e);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t q = uint32_t(rest_of(wn[e], sv[e], u[e])) & 0xffu;
+                    w |= (all_finite || finite(wn[e]) ? q : 0u) << (8 * e);
+                }
                 store4(R8 + i, w, valid);
             }
             if (lane == 0) {
