@@ -135,6 +135,10 @@ def lib():
             raise ImportError(
                 f"{LIB_PATH} not found: build it with `python -m integer_only_nn_amd.build` "
                 "(or __graft_entry__.build()); there is no CPU fallback")
+        # torch first: it brings the HIP runtime that the process then has one
+        # of; loaded after the library, it would find the devices and the
+        # library's launches would not
+        import torch  # noqa: F401
         L = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in SIGNATURES.items():
             f = getattr(L, name)
