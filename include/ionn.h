@@ -857,7 +857,7 @@ int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype,
  * value to the next; w steps as the root of v does, V's codes are the nearest
  * ones to it (even; at least the smallest for a positive w), and q is the whole
  * number below or above, by the same hash (floor(x + u)), from -127 to 127.  w
- * stays within 2% of the 32-bit state's root, 0.5% in the mean square.  R = 0
+ * stays within about 2% of the 32-bit state's root, 0.5% in the mean square.  R = 0
  * to begin with. */
 int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
                             int g_dtype, void *const *M, void *const *V,

@@ -14,7 +14,7 @@
 // magnitude is a reduction inside the wavefront, and no state is read twice.
 // Measured: 67.1 M weights with bfloat16 gradients and float32 states 324 us
 // (1745 MB, 5.4 TB/s; a 1 GiB copy reaches 5.2), 8-bit states 184 us (940 MB, 5.1
-// TB/s), with remainders 226 us (1075 MB, 4.8 TB/s: about 130 instructions per
+// TB/s), with remainders 226 us (1075 MB, 4.8 TB/s: about 140 instructions per
 // weight, of which the two exact roots and the division are 50, take as long as
 // the bytes); 20 tensors of 268 k weights with float32 states 6.2 us, one launch.
 //
@@ -34,7 +34,7 @@
 // 0.95).  With remainders, a byte more per weight, the step itself reads codes
 // that are the nearest ones, at most half a code's step off, and the remainder,
 // in 254ths of that step and rounded up or down like the codes above, keeps what
-// they leave for the next ones: code and remainder together stay within 2% of
+// they leave for the next ones: code and remainder together stay within about 2% of
 // the 32-bit root, 0.5% in the mean square.
 //
 // The mean m leaves a code's surroundings (5.6% of the value, at most) by itself

@@ -12,8 +12,8 @@
 // 16-bit types.  Each workgroup of it reduces the first pass's maxima itself
 // (about 4 KiB, from L2), which saves the launch, the cleared scalar and the
 // queue of atomics of a shared maximum.  8192 x 4096 bfloat16 errors behind a
-// gelu: 41 and 33 us, 3.3 and 5.0 TB/s; the first is held up by its arithmetic
-// (22 instructions a value, three of them quarter-rate) as much as by memory:
+// gelu: 41 and 36 us, 3.3 and 4.7 TB/s; the first is held up by its arithmetic
+// (27 instructions a value, two of them quarter-rate) as much as by memory:
 // neither four rows in flight nor twice the workgroups changed it.
 #include "dfp8_convert.h"
 
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void act_round_kernel(const T *__restrict
 // Both passes in one workgroup, for an error of at most 16 values a thread:
 // read once, no second launch.  Piece k of kOneValues / VE is strip k / groups
 // of the columns, rows group k % groups: 16 wavefronts of 64 / lanes rows
-// each.  One compute unit takes 4.2 us for 64 x 64 errors and 6.3 for 64 x 256
+// each.  One compute unit takes 3.9 us for 64 x 64 errors and 5.9 for 64 x 256
 // (gelu, bfloat16) where the two launches take 7.7; past that it is the slower
 // (11 us at 128 x 256).
 constexpr int kOneThreads = 1024, kOneValues = 16;

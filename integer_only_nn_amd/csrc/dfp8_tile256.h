@@ -7,7 +7,7 @@
 // Bound by the matrix cores at the clock that their power leaves: 8192 x 4096
 // x 4096 takes 128 us as dX (2140 TOP/s) and 116 us as G (2370 TOP/s), where
 // the library's int8 product reaches 2030 TOP/s on 8192^3; forward with gelu and
-// z 146 us, the epilogue's arithmetic (20 instructions per output, one
+// z 150 us, the epilogue's arithmetic (24 instructions per output, one
 // wavefront per SIMD) not overlapping the products.
 //
 // Edges cost no branch.  Rows past a K-major operand's end and k past an

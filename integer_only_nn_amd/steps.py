@@ -445,7 +445,7 @@ class AdamW:
     Ms and Vs: the moments, float32 tensors; or, with Ss (int8 [blocks][2] per
     tensor), codes of one byte of m and of sqrt(v).  Rs (int8, as the weights)
     carries what a code leaves of sqrt(v), so that the second moment follows
-    its definition within 2%; None: allocated as zeros, the codes' own values
+    its definition within about 2%; None: allocated as zeros, the codes' own values
     (keep them with the other states).  Rs=False: codes alone, whose v is right
     on average and scatters by about 30% per weight.  The ctypes arrays are
     built once (bind_grads for the gradient buffers), so a step costs one
