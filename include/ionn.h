@@ -821,25 +821,28 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
  * 2^S[l][2 b + 1] in block b, S[l]: int8 [2 * blocks].  The step works on
  * the float32 m and v and stores both again: for a block's largest finite
  * magnitude f * 2^q (f in [1, 2)) the exponent is q - 8 where f <= 1.75,
- * q - 7 otherwise, at least -126 (0 for an all-zero block).  m rounds to the
- * nearest code (even) where beta1 <= 15/16; above, a step changes it by less
- * than a code's half step, and it goes to the code on either side of it with
- * its expectation kept, by the hash below.  r, which a step changes by less than a code's half
- * step, goes to the code below or above, lo or hi: with s = r / 2^exponent to
- * hi where (s - lo) * (s + lo) > u * (hi^2 - lo^2) in float32, u in
- * (0, 1) a hash of t and the element's index (draws() in oracle/floats.py), so
- * that the expectation of v is kept.  Over many steps v is right on average, and r
- * scatters by about 15% around the 32-bit state's (25% where beta2 = 0.95 and
- * the gradients fall); ionn_adamw_step_carried follows it closely.  A positive
- * r never becomes 0 (the smallest code, 2^-18 of the block's largest, takes its
- * place, so that no later step divides by a vanished r).  A value that is not
- * finite becomes the NaN code 0x7f; the block's others are unaffected.
+ * q - 7 otherwise, at least -126 (0 for an all-zero block).
+ *   m rounds to the nearest code (even) where beta1 <= 15/16.  Above, a step
+ * changes it by less than a code's half step, and it goes to the code on either
+ * side of it, the farther from 0 with probability (|s| - lo) / (hi - lo), s =
+ * m / 2^exponent.
+ *   r, which a step changes by less than a code's half step, goes to the code
+ * below or above, lo or hi: with s = r / 2^exponent to hi where (s - lo) * (s +
+ * lo) > d * (hi^2 - lo^2) in float32, d in (0, 1) a hash of t and the element's
+ * index (draw4() in csrc/adamw.hip), so that the expectation of v is kept.  Over
+ * many steps v is right on average, and r scatters by about 15% around the
+ * 32-bit state's (25% where beta2 = 0.95 and the gradients fall);
+ * ionn_adamw_step_carried follows it closely.  A positive r never becomes 0 (the
+ * smallest code, 2^-18 of the block's largest, takes its place, so that no later
+ * step divides by a vanished r).
+ *   A value that is not finite becomes the NaN code 0x7f; the block's others are
+ * unaffected.
  * t: the number of this step, from 1.  For a captured graph, step (nullable,
  * device int32) gives t and lr_dev (nullable, device float) gives lr when the
  * kernel runs; the caller advances them.  grad_scale (nullable, device
  * float): 1.  absmax_P (nullable, device uint32 [L]): max-combined with the
  * float32 bits of |P| after the step, for dfp8_from_float.
- * L >= 1; P, G, M, V, S, n are HOST arrays; 1 <= n[l] <= 2^35 - 2^12 (8-bit
+ * L >= 1; P, G, M, V, S, n are HOST arrays; 1 <= n[l] <= 2^35 - 2^11 (8-bit
  * states; twice that in 32 bits).
  * 0 <= beta1, beta2 < 1; eps >= 0; lr and weight_decay finite. */
 #define IONN_ADAMW_BLOCK 256
@@ -851,14 +854,14 @@ int ionn_adamw_step(int L, float *const *P, const void *const *G, int g_dtype,
                     const float *grad_scale, uint32_t *absmax_P, void *stream);
 
 /* The same step of 8-bit states whose roots carry a remainder, so that the
- * second moment follows its definition over any number of steps.  P, M and u
- * are the step's above.  R[l], int8 [n[l]], holds q of the whole root w /
+ * second moment follows its definition over any number of steps.  P and M are
+ * the step's above.  R[l], int8 [n[l]], holds q of the whole root w /
  * 2^exponent = value(code) + q * step / 254, step the distance from the code's
  * value to the next; w steps as the root of v does, V's codes are the nearest
  * ones to it (even; at least the smallest for a positive w), and q is the whole
- * number below or above, by the same hash (floor(x + u)), from -127 to 127.  w
- * stays within about 2% of the 32-bit state's root, 0.5% in the mean square.  R = 0
- * to begin with. */
+ * number below or above, by the same hash (floor(x + d)), from -127 to 127.  w
+ * stays within about 2% of the 32-bit state's root, 0.5% in the mean square.
+ * R = 0 to begin with. */
 int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
                             int g_dtype, void *const *M, void *const *V,
                             int8_t *const *S, int8_t *const *R,
