@@ -52,10 +52,6 @@ inline int device_cus() {
     return v;
 }
 
-// A grid has fewer than 2^32 threads along a dimension; the runtime takes some
-// larger ones without a word and runs the rest of their division by 2^32.
-constexpr int64_t max_groups(int threads) { return int64_t(0xffffffffu) / threads; }
-
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 // ---------------------------------------------------------------------------

@@ -16,6 +16,10 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 inline bool dtype_ok(int dtype) { return dtype == IONN_F32 || dtype == IONN_BF16 || dtype == IONN_F16; }
 inline size_t dtype_size(int dtype) { return dtype == IONN_F32 ? 4 : 2; }
 
+// A grid has fewer than 2^32 threads along a dimension; the runtime takes some
+// larger ones without a word and runs the rest of their division by 2^32.
+constexpr int64_t max_groups(int threads) { return int64_t(0xffffffffu) / threads; }
+
 // Calls f with a value of the element type of `dtype` (checked before).
 template <class F>
 inline void with_dtype(int dtype, F &&f) {
