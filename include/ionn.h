@@ -761,7 +761,41 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype,
                     int32_t *status_out, void *workspace,
                     size_t workspace_bytes, void *stream);
 
-/* How a product of that layer is cut, by its sizes: the forward product, dX or
+/* The gated layer of a feed-forward block.  W: int8 [2 H][IN], the gate's rows
+ * and then the up projection's, one DFP-8 tensor; with (g | u) the two halves of
+ *   z[b][o] = fl(sum_i X[b][i] * W[o][i]) * 2^(eX + eW) + bias[o],
+ *   Y[b][h] = act(g[b][h]) * u[b][h]
+ * (act IONN_ACT_NONE: g * u).  bias (nullable): float [2 H]; Y: dtype [B][H];
+ * Z (nullable): dtype [B][2 H], receives z for the backward pass (apart from Y).
+ * absmax_Y and the rest as in dfp8_linear_fwd with OUT = 2 H: H in [0, 2^29],
+ * 0 <= IN <= IONN_DFP8_MAX_REDUCTION.  workspace: 16-byte aligned,
+ * dfp8_gated_fwd_workspace_bytes(B, IN, H) bytes (may be 0). */
+size_t dfp8_gated_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t H);
+int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W,
+                   const int32_t *eW, const float *bias, int act, void *Z,
+                   void *Y, int dtype, int64_t B, int64_t IN, int64_t H,
+                   uint32_t *absmax_Y, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/* Its backward pass, for the error dY of Y:
+ *   dZ = (dY * u * act'(g) | dY * act(g))   (not stored; float32, and float64
+ *     for dtype IONN_F32 with IONN_ACT_NONE or IONN_ACT_RELU)
+ *   gb[o] = sum_b dZ[b][o]                  (float32, a fixed order)
+ *   dZ8, edZ = DFP-8 of dZ, one exponent for both halves
+ *   dX = fl(dZ8 . W) * 2^(edZ + eW),  G = fl(dZ8^T . X) * 2^(edZ + eX)
+ * Z: dtype [B][2 H] as the forward stored it (for every act); dZ8: int8
+ * [B][2 H] and edZ: device int32 (written); dX (nullable): dtype [B][IN]; G
+ * (nullable): dtype [2 H][IN]; gb (nullable): float [2 H]; the rest as in
+ * dfp8_linear_bwd with OUT = 2 H. */
+size_t dfp8_gated_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t H);
+int dfp8_gated_bwd(const void *dY, const void *Z, int act, int dtype,
+                   const int8_t *X, const int32_t *eX, const int8_t *W,
+                   const int32_t *eW, int8_t *dZ8, int32_t *edZ, void *dX,
+                   void *G, float *gb, int64_t B, int64_t IN, int64_t H,
+                   int32_t *status_out, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* How a product of the Linear layer is cut, by its sizes: the forward product, dX or
  * G (product 0, 1 or 2), IONN_DFP8_ROWS: small tiles, the reduction cut among
  * a workgroup's wavefronts; _TILES_256, _TILES_128: tiles of that side, of
  * operands whose addresses are multiples of 16 (others take _TILES);

@@ -7,6 +7,19 @@
 namespace ionn {
 namespace dfp8 {
 
+// `valid` of count (4 or 8) mantissas, the low bytes of q, at p.
+__device__ __forceinline__ void store_bytes(int8_t *p, const uint32_t *q, int count, int valid) {
+    if (valid >= count) {
+        if (count == 8)
+            *reinterpret_cast<__attribute__((aligned(1))) uint64_t *>(p) =
+                uint64_t(pack4_u8(q[0], q[1], q[2], q[3])) | uint64_t(pack4_u8(q[4], q[5], q[6], q[7])) << 32;
+        else
+            *reinterpret_cast<__attribute__((aligned(1))) uint32_t *>(p) = pack4_u8(q[0], q[1], q[2], q[3]);
+        return;
+    }
+    for (int e = 0; e < valid; ++e) p[e] = int8_t(q[e]);
+}
+
 // Workgroups that a maximum is taken by, and maxima that the rounding pass
 // reads back.
 constexpr int kMaxParts = 1024;

@@ -48,18 +48,6 @@ __global__ __launch_bounds__(kThreads) void max_kernel(const T *__restrict__ x, 
     if (threadIdx.x == 0) part[blockIdx.x] = m;
 }
 
-__device__ __forceinline__ void store_bytes(int8_t *p, const uint32_t *q, int count, int valid) {
-    if (valid >= count) {
-        if (count == 8)
-            *reinterpret_cast<__attribute__((aligned(1))) uint64_t *>(p) =
-                uint64_t(pack4_u8(q[0], q[1], q[2], q[3])) | uint64_t(pack4_u8(q[4], q[5], q[6], q[7])) << 32;
-        else
-            *reinterpret_cast<__attribute__((aligned(1))) uint32_t *>(p) = pack4_u8(q[0], q[1], q[2], q[3]);
-        return;
-    }
-    for (int e = 0; e < valid; ++e) p[e] = int8_t(q[e]);
-}
-
 // The largest of the first pass's maxima.
 __device__ __forceinline__ uint32_t all_max(const uint32_t *__restrict__ part, int nparts) {
     uint32_t m = 0;

@@ -1,0 +1,396 @@
+// The gated layer of a transformer's feed-forward block on DFP-8 operands (int8
+// mantissas, one shared exponent per tensor), and its backward pass ("Mixed
+// Precision Training of Convolutional Neural Networks using Integer
+// Operations", sections 3 and 4: integer products, the operations around them
+// in floating point).  W [2 H][IN] holds the gate's rows and then the up
+// projection's, one tensor with one exponent.
+//
+//   (g | u) = fl(X W^T) 2^(eX + eW) + bias,  Y = act(g) u
+//   dZ = (dY u act'(g) | dY act(g)) -> dZ8, edZ;  dX = fl(dZ8 W) 2^(edZ + eW),
+//   G = fl(dZ8^T X) 2^(edZ + eX),  gb = column sums of dZ
+//
+// The forward product is a Linear layer's of 2 H outputs, in the same tiles and
+// by the same rule (dfp8_plan.h), with one change: a tile's rows of W are half
+// gate rows and half the up rows of the same outputs, so that both halves of an
+// output meet in one workgroup's (or one lane's) sums and Y leaves in the
+// epilogue.  The gradients' products are a Linear layer's of 2 H errors as they
+// stand.
+//
+// The errors are two passes over dY, g and u, bound by HBM: one that takes the
+// maximum and the column sums, one that rounds (the exponent needs the maximum
+// of the whole tensor first, and a float32 copy of dZ would cost more bytes than
+// computing it again).
+#include <type_traits>
+
+#include "dfp8_convert.h"
+#include "dfp8_plan.h"
+
+namespace ionn {
+namespace {
+
+using namespace dfp8;
+
+constexpr int kThreads = 256;
+
+// ---- forward -------------------------------------------------------------------
+
+// A Linear layer's plan for the 2 H rows of W; its tiles are counted in outputs.
+Plan gated_plan(int64_t B, int64_t IN, int64_t H) {
+    Plan p = make_plan<true, true>(B, 2 * H, IN, true);
+    if (p.path == ROWS) p.cols = 1;
+    p.tiles = ceil_div(B, 64) * ceil_div(H, 32);
+    return p;
+}
+
+template <class T>
+void launch_gated(const Plan &pl, Product p, hipStream_t st) {
+    const Path path = path_of(pl, p.A, p.B);
+    const dim3 block(NT);
+    if (path == ROWS) {
+        if (pl.rows == 1) launch_rows<T, 1, 2, true>(p, st);
+        else if (pl.rows == 2) launch_rows<T, 2, 2, true>(p, st);
+        else launch_rows<T, 4, 2, true>(p, st);
+    } else if (path == TILE256) {
+        tile256_kernel<T, true, true, false, true>
+            <<<dim3(unsigned(ceil_div(p.M, 256) * ceil_div(p.N, 128))), dim3(g256::NT), 0, st>>>(
+                p.A, p.lda, p.B, p.ldb, uint32_t(p.M * p.lda), uint32_t(2 * p.N * p.ldb), p.ep, p.M, p.N, p.K);
+    } else if (path == TILE128) {
+        tile128_kernel<T, true><<<dim3(unsigned(ceil_div(p.M, 128) * ceil_div(p.N, 64))), block, 0, st>>>(p);
+    } else {
+        const dim3 grid(unsigned(p.blocks));
+        if (path == TINY) tile_kernel<T, 64, 64, 2, true, true, false, true, true><<<grid, block, 0, st>>>(p);
+        else tile_kernel<T, 64, 64, 4, true, true, false, false, true><<<grid, block, 0, st>>>(p);
+        if (p.split > 1) sum_gated_kernel<T><<<dim3(sum_groups(p)), block, 0, st>>>(p);
+    }
+}
+
+// ---- the errors ----------------------------------------------------------------
+
+// Two float32 values have a product of 48 bits, and rounding it to float32 on
+// the way to 8 bits would now and then round a tie the wrong way: float32
+// errors whose derivative is exact (none, relu) are taken in float64.  Products
+// of 16-bit values are exact in float32.
+template <class T, int ACT>
+using Wide = std::conditional_t<sizeof(T) == 4 && (ACT == IONN_ACT_NONE || ACT == IONN_ACT_RELU), double, float>;
+
+// An activation's value f and derivative df at z from one exponential.  With e =
+// 2^x and p = 1 / (1 + e), 1 - p is e p: exact to its own size, where 1.0f - p is
+// off by half a step of 1, which z (or, of gelu_tanh, z (1 + 0.13 z^2)) times it
+// would carry into the result.  (p is 0 where e is infinite, and so is df.)
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float &f, float &df) {
+    if (ACT == IONN_ACT_SILU || ACT == IONN_ACT_GELU_TANH) {
+        const float x = ACT == IONN_ACT_SILU ? -kLog2e * z : z * fmaf(z * z, -kLog2e * kGeluK * kGeluC, -kLog2e * kGeluK);
+        const float e = exp2_fast(x), p = __builtin_amdgcn_rcpf(1.0f + e), pq = p * (fminf(e, 0x1p126f) * p);
+        const float y = within(z);
+        f = above(z) * p;
+        df = fmaf(ACT == IONN_ACT_SILU ? y : y * fmaf(y * y, 3.0f * kGeluK * kGeluC, kGeluK), pq, p);
+    } else if (ACT == IONN_ACT_GELU) {
+        const float x = fabsf(z), e = normal_exp(x), tail = normal_tail<kTermsGrad>(x, e);
+        f = fmaf(-fminf(x, 30.0f), tail, fmaxf(z, 0.0f));
+        df = fmaf(within(z) * kInvSqrt2Pi, e, z < 0.0f ? tail : 1.0f - tail);
+    } else {
+        f = act_value<ACT, kTermsGrad>(z);
+        df = act_grad<ACT, kTermsGrad>(z);
+    }
+}
+
+template <int ACT, class V>
+__device__ __forceinline__ void gated_error(float dy, float g, float u, V &dg, V &du) {
+    float f, df;
+    act_both<ACT>(g, f, df);
+    dg = V(dy) * V(u) * V(df);
+    du = V(dy) * V(f);
+}
+
+__device__ __forceinline__ uint32_t mantissa_of(float x, int negE) { return dfp8_mantissa(x, negE); }
+__device__ __forceinline__ uint32_t mantissa_of(double x, int negE) {
+    const double y = fmin(fmax(ldexp(x, negE), -128.0), 127.0);
+    return uint32_t(__double_as_longlong(y + 6755399441055744.0));  // 1.5 * 2^52
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    __shared__ uint32_t red[kThreads / 64];
+    v = wave_max_u32(v);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// The pieces (dy, g, u) of row r at columns c ..
+template <class T, int VE>
+struct Piece {
+    typename Vec<T, VE>::type y, g, u;
+    __device__ __forceinline__ void load(const T *dY, const T *Z, int64_t r, int H, int c, int valid) {
+        y = load_raw<T, VE>(dY + r * H + c, valid);
+        g = load_raw<T, VE>(Z + 2 * r * H + c, valid);
+        u = load_raw<T, VE>(Z + 2 * r * H + H + c, valid);
+    }
+};
+
+// Workgroup (strip, chunk): the strip's columns over the chunk's rows, four
+// wavefronts of 64 / lanes rows each at a time (act_layout of the H columns).
+template <class T, int ACT>
+__global__ __launch_bounds__(kThreads) void gated_sums_kernel(const T *__restrict__ dY, const T *__restrict__ Z,
+                                                              int64_t B, int H, int lanes_log, int64_t chunk_rows,
+                                                              uint32_t *__restrict__ part_max,
+                                                              float *__restrict__ part_sum) {
+    constexpr int VE = 16 / sizeof(T);
+    __shared__ float fold[kThreads / 64][2][64 * VE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lanes = 1 << lanes_log, per_wave = 64 >> lanes_log;
+    const int c = (int(blockIdx.x) * lanes + (lane & (lanes - 1))) * VE;
+    const int64_t r1 = min(B, int64_t(blockIdx.y + 1) * chunk_rows);
+    float s[2][VE] = {};
+    uint32_t m = 0;
+    if (c < H) {
+        const int valid = H - c, step = (kThreads / 64) * per_wave;
+        auto add = [&](const Piece<T, VE> &p) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                Wide<T, ACT> dg, du;
+                gated_error<ACT>(float(p.y[e]), float(p.g[e]), float(p.u[e]), dg, du);
+                s[0][e] += float(dg);
+                s[1][e] += float(du);
+                // (past a row's end all three are 0, and so are both errors)
+                m = max(m, max(mag_bits(float(dg)), mag_bits(float(du))));
+            }
+        };
+        int64_t r = int64_t(blockIdx.y) * chunk_rows + wave * per_wave + (lane >> lanes_log);
+        for (; r + step < r1; r += 2 * step) {  // two rows' loads in flight
+            Piece<T, VE> p[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) p[k].load(dY, Z, r + k * step, H, c, valid);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) add(p[k]);
+        }
+        for (; r < r1; r += step) {
+            Piece<T, VE> p;
+            p.load(dY, Z, r, H, c, valid);
+            add(p);
+        }
+    }
+    // the row groups of a wavefront, then the wavefronts
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            for (int off = lanes; off < 64; off <<= 1) s[k][e] += __shfl_xor(s[k][e], off, 64);
+            fold[wave][k][(lane & (lanes - 1)) * VE + e] = s[k][e];
+        }
+    m = block_max(m);  // (its barrier orders fold as well)
+    if (threadIdx.x == 0) part_max[blockIdx.y * gridDim.x + blockIdx.x] = m;
+    if (part_sum == nullptr) return;
+    for (int i = threadIdx.x; i < 2 * lanes * VE; i += kThreads) {
+        const int k = i >= lanes * VE, j = i - k * lanes * VE, col = int(blockIdx.x) * lanes * VE + j;
+        if (col < H)
+            part_sum[(2 * int64_t(blockIdx.y) + k) * H + col] =
+                (fold[0][k][j] + fold[1][k][j]) + (fold[2][k][j] + fold[3][k][j]);
+    }
+}
+
+// Workgroups below n_round round the errors, (strip, chunk) as above; those from
+// it on add up the chunks' column sums, 64 columns at a time, every fourth chunk
+// per wavefront.
+template <class T, int ACT>
+__global__ __launch_bounds__(kThreads) void gated_round_kernel(
+    const T *__restrict__ dY, const T *__restrict__ Z, int64_t B, int H, int lanes_log, int strips, int64_t chunk_rows,
+    int n_round, const uint32_t *__restrict__ part_max, int nparts, const float *__restrict__ part_sum, int chunks,
+    int8_t *__restrict__ dZ8, int32_t *__restrict__ edZ, float *__restrict__ gb, int32_t *__restrict__ status) {
+    constexpr int VE = 16 / sizeof(T);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (int(blockIdx.x) >= n_round) {
+        __shared__ float red[kThreads / 64][64];
+        const int64_t cols = 2 * int64_t(H), step = (int64_t(gridDim.x) - n_round) * 64;
+        for (int64_t c0 = int64_t(int(blockIdx.x) - n_round) * 64; c0 < cols; c0 += step) {
+            const int64_t c = c0 + lane;
+            float s = 0.0f;
+            if (c < cols) {
+#pragma unroll 8
+                for (int k = wave; k < chunks; k += kThreads / 64) s += part_sum[int64_t(k) * cols + c];
+            }
+            red[wave][lane] = s;
+            __syncthreads();
+            if (wave == 0 && c < cols) gb[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+            __syncthreads();
+        }
+        return;
+    }
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < nparts; i += kThreads) m = max(m, part_max[i]);
+    m = block_max(m);
+    const int E = dfp8_exponent(m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *edZ = E;
+        if (status) *status = dfp8_status(m, E);
+    }
+    const int lanes = 1 << lanes_log, per_wave = 64 >> lanes_log, step = (kThreads / 64) * per_wave;
+    const int chunk = int(blockIdx.x) / strips, strip = int(blockIdx.x) - chunk * strips;
+    const int c = (strip * lanes + (lane & (lanes - 1))) * VE;
+    if (c >= H) return;
+    const int valid = H - c;
+    const int64_t r1 = min(B, int64_t(chunk + 1) * chunk_rows);
+    auto put = [&](const Piece<T, VE> &p, int64_t r) __attribute__((always_inline)) {
+        uint32_t qg[VE], qu[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            Wide<T, ACT> dg, du;
+            gated_error<ACT>(float(p.y[e]), float(p.g[e]), float(p.u[e]), dg, du);
+            qg[e] = mantissa_of(dg, -E);
+            qu[e] = mantissa_of(du, -E);
+        }
+        int8_t *z = dZ8 + 2 * r * H + c;
+        store_bytes(z, qg, VE, valid);
+        store_bytes(z + H, qu, VE, valid);
+    };
+    int64_t r = int64_t(chunk) * chunk_rows + wave * per_wave + (lane >> lanes_log);
+    for (; r + step < r1; r += 2 * step) {  // two rows' loads in flight
+        Piece<T, VE> p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) p[k].load(dY, Z, r + k * step, H, c, valid);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) put(p[k], r + k * step);
+    }
+    for (; r < r1; r += step) {
+        Piece<T, VE> p;
+        p.load(dY, Z, r, H, c, valid);
+        put(p, r);
+    }
+}
+
+// Bytes of the maxima and of the column sums' partial rows.
+size_t error_bytes(int64_t B, int64_t H) {
+    size_t most = 0;
+    for (size_t es : {size_t(2), size_t(4)}) {
+        const ActLayout a = act_layout(B, H, es);
+        const size_t maxima = (size_t(a.strips) * a.chunks * sizeof(uint32_t) + 15) & ~size_t(15);
+        const size_t b = maxima + size_t(a.chunks) * 2 * H * sizeof(float);
+        most = b > most ? b : most;
+    }
+    return (most + 15) & ~size_t(15);
+}
+
+void launch_errors(const void *dY, const void *Z, int act, int dtype, int64_t B, int64_t H, int8_t *dZ8, int32_t *edZ,
+                   float *gb, int32_t *status, void *workspace, hipStream_t st) {
+    const ActLayout a = act_layout(B, H, dtype_size(dtype));
+    const int nparts = a.strips * a.chunks;
+    uint32_t *maxima = static_cast<uint32_t *>(workspace);
+    float *sums = gb ? reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                                 ((size_t(nparts) * sizeof(uint32_t) + 15) & ~size_t(15)))
+                     : nullptr;
+    int lanes_log = 0;
+    while ((1 << lanes_log) < a.lanes) ++lanes_log;
+    // (at most 2^20 workgroups of sums: one for each 64 of 2^30 columns and the others would be too many threads)
+    const unsigned n_sum = gb ? unsigned(2 * H <= int64_t(64) << 20 ? (2 * H + 63) / 64 : int64_t(1) << 20) : 0u;
+    with_dtype(dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const T *y = static_cast<const T *>(dY), *z = static_cast<const T *>(Z);
+        with_act(act, [&](auto ac) {
+            constexpr int ACT = decltype(ac)::value;
+            gated_sums_kernel<T, ACT><<<dim3(unsigned(a.strips), unsigned(a.chunks)), dim3(kThreads), 0, st>>>(
+                y, z, B, int(H), lanes_log, a.rows, maxima, sums);
+            gated_round_kernel<T, ACT><<<dim3(unsigned(nparts) + n_sum), dim3(kThreads), 0, st>>>(
+                y, z, B, int(H), lanes_log, a.strips, a.rows, nparts, maxima, nparts, sums, a.chunks, dZ8, edZ, gb,
+                status);
+        });
+    });
+}
+
+bool gated_sizes_ok(int64_t B, int64_t IN, int64_t H) {
+    return H >= 0 && H <= kMaxSide / 2 && sizes_ok(B, IN, 2 * H) && tiles_ok(B, 2 * H);
+}
+
+bool apart(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || x + na <= y || y + nb <= x;
+}
+
+}  // namespace
+}  // namespace ionn
+
+using namespace ionn;
+using namespace ionn::dfp8;
+
+extern "C" {
+
+size_t dfp8_gated_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t H) {
+    if (!gated_sizes_ok(B, IN, H) || B == 0 || H == 0) return 0;
+    return part_bytes(gated_plan(B, IN, H), B, 2 * H);
+}
+
+int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const int32_t *eW, const float *bias, int act,
+                   void *Z, void *Y, int dtype, int64_t B, int64_t IN, int64_t H, uint32_t *absmax_Y, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    clear_error();
+    IONN_REQUIRE(dtype_ok(dtype), IONN_ERR_ARG, "dfp8_gated_fwd: dtype = %d", dtype);
+    IONN_REQUIRE(act >= IONN_ACT_NONE && act <= IONN_ACT_SILU, IONN_ERR_ARG, "dfp8_gated_fwd: act = %d", act);
+    IONN_REQUIRE(gated_sizes_ok(B, IN, H) && IN <= IONN_DFP8_MAX_REDUCTION, IONN_ERR_SHAPE,
+                 "dfp8_gated_fwd: B=%lld IN=%lld H=%lld (IN at most %d)", (long long)B, (long long)IN, (long long)H,
+                 IONN_DFP8_MAX_REDUCTION);
+    if (B == 0 || H == 0) return IONN_OK;
+    IONN_REQUIRE(Y && eX && eW && (IN == 0 || (X && W)), IONN_ERR_ARG, "dfp8_gated_fwd: NULL tensor");
+    const size_t es = dtype_size(dtype), out = size_t(B) * H * es;
+    IONN_REQUIRE(apart(Y, out, Z, 2 * out), IONN_ERR_ARG, "dfp8_gated_fwd: Z must not overlap Y");
+    IONN_REQUIRE(aligned(Y, es) && aligned(Z, es) && aligned(bias, 4) && aligned(eX, 4) && aligned(eW, 4) &&
+                     aligned(absmax_Y, 4),
+                 IONN_ERR_ALIGN, "dfp8_gated_fwd: tensors must be aligned to their element size");
+    const size_t need = dfp8_gated_fwd_workspace_bytes(B, IN, H);
+    IONN_REQUIRE(need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need), IONN_ERR_WORKSPACE,
+                 "dfp8_gated_fwd: needs a 16-byte aligned workspace of %zu bytes", need);
+    const Epi ep{eX, eW, bias, nullptr, Z, Y, absmax_Y, act};
+    const Plan plan = gated_plan(B, IN, H);
+    Product p = make_product(plan, X, IN, W, IN, ep, B, H, IN, workspace);
+    const int64_t most = path_of(plan, X, W) == ROWS ? ceil_div(H, 16) : int64_t(p.blocks);
+    IONN_REQUIRE(most <= max_groups(path_of(plan, X, W) == ROWS ? kRowWaves * 64 : NT), IONN_ERR_SHAPE,
+                 "dfp8_gated_fwd: B=%lld H=%lld have too many tiles", (long long)B, (long long)H);
+    with_dtype(dtype, [&](auto tag) { launch_gated<decltype(tag)>(plan, p, as_stream(stream)); });
+    return check_launch("dfp8_gated_fwd");
+}
+
+size_t dfp8_gated_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t H) {
+    if (!gated_sizes_ok(B, IN, H) || B == 0 || H == 0) return 0;
+    return error_bytes(B, H) + (IN > 0 ? backward_part_bytes(B, IN, 2 * H) : 0);
+}
+
+int dfp8_gated_bwd(const void *dY, const void *Z, int act, int dtype, const int8_t *X, const int32_t *eX,
+                   const int8_t *W, const int32_t *eW, int8_t *dZ8, int32_t *edZ, void *dX, void *G, float *gb,
+                   int64_t B, int64_t IN, int64_t H, int32_t *status_out, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+    clear_error();
+    IONN_REQUIRE(dtype_ok(dtype), IONN_ERR_ARG, "dfp8_gated_bwd: dtype = %d", dtype);
+    IONN_REQUIRE(act >= IONN_ACT_NONE && act <= IONN_ACT_SILU, IONN_ERR_ARG, "dfp8_gated_bwd: act = %d", act);
+    IONN_REQUIRE(gated_sizes_ok(B, IN, H) && (dX == nullptr || 2 * H <= IONN_DFP8_MAX_REDUCTION) &&
+                     (G == nullptr || B <= IONN_DFP8_MAX_REDUCTION) && tiles_ok(B, IN) && tiles_ok(2 * H, IN),
+                 IONN_ERR_SHAPE, "dfp8_gated_bwd: B=%lld IN=%lld H=%lld (2 H with dX, B with G: at most %d)",
+                 (long long)B, (long long)IN, (long long)H, IONN_DFP8_MAX_REDUCTION);
+    const bool error = B > 0 && H > 0;  // there is an error to go by
+    IONN_REQUIRE(edZ && (!error || (dY && Z && dZ8)), IONN_ERR_ARG, "dfp8_gated_bwd: NULL dY, Z, dZ8 or edZ");
+    IONN_REQUIRE(!error || IN == 0 || ((dX == nullptr || (W && eW)) && (G == nullptr || (X && eX))), IONN_ERR_ARG,
+                 "dfp8_gated_bwd: dX needs W and eW, G needs X and eX");
+    const size_t es = dtype_size(dtype);
+    IONN_REQUIRE(aligned(dY, es) && aligned(Z, es) && aligned(dX, es) && aligned(G, es) && aligned(gb, 4) &&
+                     aligned(eX, 4) && aligned(eW, 4) && aligned(edZ, 4) && aligned(status_out, 4),
+                 IONN_ERR_ALIGN, "dfp8_gated_bwd: tensors must be aligned to their element size");
+    const size_t need = dfp8_gated_bwd_workspace_bytes(B, IN, H);
+    IONN_REQUIRE(need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need), IONN_ERR_WORKSPACE,
+                 "dfp8_gated_bwd: needs a 16-byte aligned workspace of %zu bytes", need);
+    hipStream_t st = as_stream(stream);
+    if (!error) {
+        zero_bytes(edZ, 4, st);
+        zero_bytes(status_out, 4, st);
+        zero_bytes(dX, B * IN * int64_t(es), st);
+        zero_bytes(G, 2 * H * IN * int64_t(es), st);
+        zero_bytes(gb, 8 * H, st);
+        return check_launch("dfp8_gated_bwd");
+    }
+    const BackwardProducts p{dZ8, X, W, edZ, eX, eW, dX, G, B, IN, 2 * H, static_cast<char *>(workspace) + error_bytes(B, H)};
+    IONN_REQUIRE(IN == 0 || backward_launches(p), IONN_ERR_SHAPE,
+                 "dfp8_gated_bwd: B=%lld IN=%lld H=%lld have too many tiles", (long long)B, (long long)IN, (long long)H);
+    launch_errors(dY, Z, act, dtype, B, H, dZ8, edZ, gb, status_out, workspace, st);
+    if (int rc = check_launch("dfp8_gated_bwd")) return rc;
+    if (IN == 0) return IONN_OK;
+    launch_backward_products(p, dtype, st);
+    return check_launch("dfp8_gated_bwd");
+}
+
+}  // extern "C"

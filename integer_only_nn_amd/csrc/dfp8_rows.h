@@ -30,8 +30,10 @@ __device__ __forceinline__ void in_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// K >= 16; RG groups of 16 rows, NG groups of 16 outputs.
-template <class T, int RG, int NG>
+// K >= 16; RG groups of 16 rows, NG groups of 16 outputs.  GATED: N outputs of
+// W's 2 N rows; the first NG / 2 groups are gate rows, the others the up rows of
+// the same outputs.
+template <class T, int RG, int NG, bool GATED = false>
 __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__restrict__ X, const int8_t *__restrict__ W,
                                                               Epi ep, int M, int N, int K) {
     constexpr int kDeep = 2;
@@ -40,7 +42,9 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
     __shared__ v4i stage[kRowWaves][NG + RG][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int n0 = int(blockIdx.x) * (16 * NG), m0 = int(blockIdx.y) * (16 * RG);
+    constexpr int NO = GATED ? NG / 2 : NG;  // groups of outputs
+    static_assert(!GATED || NG % 2 == 0, "both halves of a group");
+    const int n0 = int(blockIdx.x) * (16 * NO), m0 = int(blockIdx.y) * (16 * RG);
     // this wavefront's range of k: whole pieces of 64
     const int pieces = (K + 63) / 64, per = (pieces + kRowWaves - 1) / kRowWaves;
     const int k_begin = 64 * per * wave, k_end = min(K, k_begin + 64 * per);
@@ -61,14 +65,17 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
     typedef v4i loose __attribute__((aligned(1)));
     const int8_t *w[NG], *x[RG];
 #pragma unroll
-    for (int h = 0; h < NG; ++h) w[h] = W + int64_t(min(n0 + 16 * h + lr, N - 1)) * K;
+    for (int h = 0; h < NG; ++h) w[h] = W + (int64_t(min(n0 + 16 * (h % NO) + lr, N - 1)) + int64_t(h / NO) * N) * K;
 #pragma unroll
     for (int g = 0; g < RG; ++g) x[g] = X + int64_t(min(m0 + 16 * g + lr, M - 1)) * K;
     // what the epilogue needs besides the sums is loaded ahead of them: the
     // wavefront finishes rows m0 + 16 (wave % RG) .., outputs n0 + 16 (wave / RG) ..
     const int ea = *ep.ea, eb = *ep.eb, n = n0 + 16 * (wave / RG) + 4 * (lane >> 4);
-    float bias[4] = {};
-    if (wave < RG * NG) load_bias(ep, n, N, bias);
+    float bias[4] = {}, bias_up[4] = {};
+    if (wave < RG * NO) {
+        if (GATED) load_bias2(ep, n, N, bias, bias_up);
+        else load_bias(ep, n, N, bias);
+    }
     v4i acc[NG][RG];
 #pragma unroll
     for (int h = 0; h < NG; ++h)
@@ -139,13 +146,20 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
 #pragma unroll
         for (int g = 0; g < RG; ++g) sums[h * RG + g][wave][lane] = acc[h][g];
     __syncthreads();
-    if (wave >= RG * NG) return;
+    if (wave >= RG * NO) return;
     v4i s = sums[wave][0][lane];
 #pragma unroll
     for (int o = 1; o < kRowWaves; ++o) s += sums[wave][o][lane];
     const int e2 = ea + eb;
     uint32_t top = 0;
-    with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
+    if constexpr (GATED) {
+        v4i u = sums[RG * NO + wave][0][lane];
+#pragma unroll
+        for (int o = 1; o < kRowWaves; ++o) u += sums[RG * NO + wave][o][lane];
+        with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
+            top = finish_gated4<T, decltype(ac)::value>(s, u, ep, e2, bias, bias_up, m0 + 16 * (wave % RG) + r, n, M, N);
+        });
+    } else with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
         top = finish4<T, decltype(ac)::value, false>(s, ep, e2, bias, m0 + 16 * (wave % RG) + r, n, M, N);
     });
     if (ep.absmax) {
@@ -154,10 +168,11 @@ __global__ __launch_bounds__(kRowWaves * 64) void rows_kernel(const int8_t *__re
     }
 }
 
-template <class T, int RG, int NG>
+template <class T, int RG, int NG, bool GATED = false>
 void launch_rows(const Product &p, hipStream_t st) {
-    const dim3 grid(unsigned((p.N + 16 * NG - 1) / (16 * NG)), unsigned((p.M + 16 * RG - 1) / (16 * RG)));
-    rows_kernel<T, RG, NG><<<grid, dim3(kRowWaves * 64), 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
+    constexpr int kCols = 16 * (GATED ? NG / 2 : NG);
+    const dim3 grid(unsigned((p.N + kCols - 1) / kCols), unsigned((p.M + 16 * RG - 1) / (16 * RG)));
+    rows_kernel<T, RG, NG, GATED><<<grid, dim3(kRowWaves * 64), 0, st>>>(p.A, p.B, p.ep, p.M, p.N, p.K);
 }
 
 }  // namespace dfp8

@@ -112,8 +112,11 @@ __device__ __forceinline__ int fT(int k) {
 
 // One operand's tile of R rows: a step's pieces to registers, then to LDS.
 // TINY: the contiguous side is shorter than a piece.
-template <int R, bool KMAJOR, bool TINY>
+// HALF: a gated layer's weights [2 rows][kdim]; the tile's first R / 2 rows are
+// gate rows from r0 / 2 on, the others the up rows of the same outputs.
+template <int R, bool KMAJOR, bool TINY, bool HALF = false>
 struct Stage {
+    static_assert(!HALF || KMAJOR, "the gated layer's weights are K-major");
     static constexpr int kPer = R * BK / 16 / NT;
     static_assert(R * BK / 16 % NT == 0, "whole pieces per thread");
     v4i reg[kPer];
@@ -124,7 +127,12 @@ struct Stage {
             const int id = j * NT + int(threadIdx.x);
             const int r = r0 + (KMAJOR ? id / (BK / 16) : 16 * (id % (R / 16)));
             const int k = k0 + (KMAJOR ? 16 * (id % (BK / 16)) : id / (R / 16));
-            if (TINY && KMAJOR)
+            if (HALF) {
+                const int t = id / (BK / 16), h = t >= R / 2;
+                const int64_t row = int64_t(h) * rows + min(r0 / 2 + t - h * (R / 2), rows - 1);
+                reg[j] = TINY ? load_piece(base, row * ld + k, kdim - k)
+                              : *reinterpret_cast<const loose *>(base + row * ld + min(k, kdim - 16));
+            } else if (TINY && KMAJOR)
                 reg[j] = load_piece(base, r * ld + k, r < rows ? kdim - k : 0);
             else if (TINY)
                 reg[j] = load_piece(base, k * ld + r, k < kdim ? rows - r : 0);
@@ -193,6 +201,62 @@ __device__ __forceinline__ void load_bias(const Epi &ep, int n, int N, float (&b
     const auto raw = load_raw<float, V>(ep.bias + n, ep.bias ? N - n : 0);
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = raw[i];
+}
+
+// The same for the two halves of a gated layer's bias [2 H]: columns n .. of each.
+template <int V>
+__device__ __forceinline__ void load_bias2(const Epi &ep, int n, int H, float (&bg)[V], float (&bu)[V]) {
+    load_bias(ep, n, H, bg);
+    const auto raw = load_raw<float, V>(ep.bias + H + n, ep.bias ? H - n : 0);
+#pragma unroll
+    for (int i = 0; i < V; ++i) bu[i] = raw[i];
+}
+
+// A gated layer's outputs n .. n + V - 1 of row m from the sums of its gate and
+// up halves: y = act(g) u at row pitch H, z = (g, u) at 2 H.
+template <class T, int ACT, int V>
+__device__ __forceinline__ uint32_t finish_gated(const int (&sg)[V], const int (&su)[V], const Epi &ep, int e2,
+                                                 const float (&bg)[V], const float (&bu)[V], int64_t m, int n, int M,
+                                                 int H) {
+    if (m >= M || n >= H) return 0u;
+    const int valid = H - n;
+    float g[V], u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        g[i] = __builtin_amdgcn_ldexpf(float(sg[i]), e2) + bg[i];
+        u[i] = __builtin_amdgcn_ldexpf(float(su[i]), e2) + bu[i];
+    }
+    if (ep.z) {
+        T *z = static_cast<T *>(ep.z) + 2 * m * H + n;
+        store_vec<T, V>(z, g, valid);
+        store_vec<T, V>(z + H, u, valid);
+    }
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = act_value<ACT, kTermsValue<T>>(g[i]) * u[i];
+    store_vec<T, V>(static_cast<T *>(ep.y) + m * H + n, o, valid);
+    uint32_t top = 0;
+    if (ep.absmax) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) top = max(top, mag_bits(o[i]));
+    }
+    return top;
+}
+template <class T, int ACT>
+__device__ __forceinline__ uint32_t finish_gated8(const v4i &glo, const v4i &ghi, const v4i &ulo, const v4i &uhi,
+                                                  const Epi &ep, int e2, const float (&bg)[8], const float (&bu)[8],
+                                                  int64_t m, int n, int M, int H) {
+    const int g[8] = {glo.x, glo.y, glo.z, glo.w, ghi.x, ghi.y, ghi.z, ghi.w};
+    const int u[8] = {ulo.x, ulo.y, ulo.z, ulo.w, uhi.x, uhi.y, uhi.z, uhi.w};
+    return finish_gated<T, ACT, 8>(g, u, ep, e2, bg, bu, m, n, M, H);
+}
+template <class T, int ACT>
+__device__ __forceinline__ uint32_t finish_gated4(const v4i &sg, const v4i &su, const Epi &ep, int e2,
+                                                  const float (&bg)[4], const float (&bu)[4], int64_t m, int n, int M,
+                                                  int H) {
+    const int g[4] = {sg.x, sg.y, sg.z, sg.w}, u[4] = {su.x, su.y, su.z, su.w};
+    return finish_gated<T, ACT, 4>(g, u, ep, e2, bg, bu, m, n, M, H);
 }
 
 // Four sums of row m, columns n .. n + 3, through the epilogue (b: the
@@ -276,7 +340,7 @@ __device__ __forceinline__ uint32_t finish8(const v4i &lo, const v4i &hi, const 
 
 // The sums of one tile over k in [k_begin, k_end) (k_begin and, but for the
 // last range, k_end multiples of BK).  lds: 2 stages of (BM + BN) * BK bytes.
-template <int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool TINY>
+template <int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool TINY, bool GATED = false>
 __device__ __forceinline__ void tile_sums(const int8_t *__restrict__ A, int64_t lda, const int8_t *__restrict__ B,
                                           int64_t ldb, int M, int N, int m0, int n0, int k_begin, int k_end, int8_t *lds,
                                           int wm, int wn, int lane, v16i (&acc)[BM / 64][BN / 64]) {
@@ -290,7 +354,7 @@ __device__ __forceinline__ void tile_sums(const int8_t *__restrict__ A, int64_t 
     const int nk = (k_end - k_begin + BK - 1) / BK;
     if (nk <= 0) return;
     Stage<BM, A_KM, TINY> sa[DEPTH];
-    Stage<BN, B_KM, TINY> sb[DEPTH];
+    Stage<BN, B_KM, TINY, GATED> sb[DEPTH];
     auto load = [&](int s, int kt) __attribute__((always_inline)) {
         sa[s].load(A, lda, M, k_end, m0, k_begin + kt * BK);
         sb[s].load(B, ldb, N, k_end, n0, k_begin + kt * BK);
@@ -332,6 +396,9 @@ __device__ __forceinline__ void tile_sums(const int8_t *__restrict__ A, int64_t 
     }
 }
 
+// (A gated layer's product has N = H outputs, B its 2 H rows of weights, and n0
+// of a tile counts rows of both halves: outputs n0 / 2 ...)
+//
 // A product C [M][N] over K with its epilogue, cut into tiles and, where
 // there are few of them over a long reduction, into `split` ranges of K: each
 // range leaves its int32 sums in part [split][M][N], and sum_kernel adds them
@@ -349,8 +416,61 @@ struct Product {
 template <int BM, int BN>
 constexpr int kTileLds = 2 * (BM + BN) * BK;
 
+// Eight sums of row m at columns n .. of a range's [M][N] part.
+__device__ __forceinline__ void store_part8(int32_t *row, const v4i &lo, const v4i &hi, int valid) {
+    typedef v4i loose __attribute__((aligned(4)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const v4i s = h ? hi : lo;
+        if (4 * h + 4 <= valid) {
+            *reinterpret_cast<loose *>(row + 4 * h) = s;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (4 * h + e < valid) row[4 * h + e] = s[e];
+        }
+    }
+}
+
+// A gated layer's tile, its sums in LDS as run_tile lays them: BN / 2 outputs
+// from n0 on, their gate sums in the first columns and the up sums in the others.
+// Ranges leave theirs in part [split][M][2 H].
+template <class T, int BM, int BN>
+__device__ __forceinline__ void finish_gated_tile(const Product &p, const v4i *buf, int range, int m0, int n0) {
+    constexpr int kPieces = BN / 4, kLanes = BN / 16, kRows = NT / kLanes;
+    const int M = p.M, H = p.N;
+    const int c = 2 * (int(threadIdx.x) % kLanes), n = n0 + 4 * c, r0 = int(threadIdx.x) / kLanes;
+    const Epi &ep = p.ep;
+    int32_t *part = p.part + int64_t(range) * M * 2 * H;
+    const int e2 = *ep.ea + *ep.eb;
+    float bg[8] = {}, bu[8] = {};
+    if (p.split == 1 && n < H) load_bias2(ep, n, H, bg, bu);
+    uint32_t top = 0;
+    with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < BM / kRows; ++k) {
+            const int r = kRows * k + r0;
+            const int64_t m = int64_t(m0) + r;
+            const auto at = [&](int i) __attribute__((always_inline)) { return buf[r * kPieces + ((c + i) ^ (r & 15))]; };
+            const v4i glo = at(0), ghi = at(1), ulo = at(kPieces / 2), uhi = at(kPieces / 2 + 1);
+            if (p.split > 1) {
+                if (m < M && n < H) {
+                    store_part8(part + 2 * m * H + n, glo, ghi, H - n);
+                    store_part8(part + 2 * m * H + H + n, ulo, uhi, H - n);
+                }
+            } else {
+                top = max(top, finish_gated8<T, decltype(ac)::value>(glo, ghi, ulo, uhi, ep, e2, bg, bu, m, n, M, H));
+            }
+        }
+    });
+    if (ep.absmax && p.split == 1) {
+        top = wave_max_u32(top);
+        if ((threadIdx.x & 63) == 0) publish_max_u32(ep.absmax, top);
+    }
+}
+
 // Workgroup `id` of a product: the tile id % tiles over range id / tiles.
-template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
+template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY, bool GATED = false>
 __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) {
     constexpr int FM = BM / 64, FN = BN / 64;
     const int lane = threadIdx.x & 63;
@@ -368,10 +488,11 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
         k_end = min(p.K, int(steps * uint32_t(range + 1) / uint32_t(p.split)) * BK);
     }
     int tm, tn;
-    gemm::tile_coords(tile, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+    constexpr int kCols = GATED ? BN / 2 : BN;  // outputs of a tile
+    gemm::tile_coords(tile, (M + BM - 1) / BM, (N + kCols - 1) / kCols, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     v16i acc[FM][FN];
-    tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY>(p.A, p.lda, p.B, p.ldb, M, N, m0, n0, k_begin, k_end, lds, wm, wn, lane,
+    tile_sums<BM, BN, DEPTH, A_KM, B_KM, TINY, GATED>(p.A, p.lda, p.B, p.ldb, M, N, m0, n0, k_begin, k_end, lds, wm, wn, lane,
                                                acc);
     // The tile through LDS (lane: row lane % 32, columns 8 q + 4 (lane / 32)
     // .. + 3 of each 32 x 32 block; 16-byte piece c of row r at position c ^ (r
@@ -391,6 +512,10 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
                     v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
             }
     __syncthreads();
+    if constexpr (GATED) {
+        finish_gated_tile<T, BM, BN>(p, buf, range, m0, n0 / 2);
+        return;
+    }
     const int c = 2 * (int(threadIdx.x) % (BN / 8)), n = n0 + 4 * c;  // the thread's eight columns
     constexpr int kRows = NT / (BN / 8);                              // rows finished at once
     if (p.split > 1) {
@@ -435,10 +560,10 @@ __device__ __forceinline__ void run_tile(const Product &p, int id, int8_t *lds) 
     }
 }
 
-template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY>
+template <class T, int BM, int BN, int DEPTH, bool A_KM, bool B_KM, bool LINEAR, bool TINY, bool GATED = false>
 __global__ __launch_bounds__(NT) void tile_kernel(Product p) {
     __shared__ __attribute__((aligned(256))) int8_t lds[kTileLds<BM, BN>];
-    run_tile<T, BM, BN, DEPTH, A_KM, B_KM, LINEAR, TINY>(p, int(blockIdx.x), lds);
+    run_tile<T, BM, BN, DEPTH, A_KM, B_KM, LINEAR, TINY, GATED>(p, int(blockIdx.x), lds);
 }
 
 // The two products of a backward pass in one launch: dX's workgroups, then
@@ -484,6 +609,42 @@ __device__ __forceinline__ void sum_ranges(const Product &p, uint32_t id) {
         });
     }
     if (!LINEAR && p.ep.absmax) {
+        top = wave_max_u32(top);
+        if ((threadIdx.x & 63) == 0) publish_max_u32(p.ep.absmax, top);
+    }
+}
+
+// The same of a gated layer's halves, from part [split][M][2 H].
+template <class T>
+__global__ __launch_bounds__(NT) void sum_gated_kernel(Product p) {
+    const uint32_t id = blockIdx.x * NT + threadIdx.x, n4 = uint32_t(p.N + 3) / 4, row = id / n4;
+    const int n = 4 * int(id - row * n4), H = p.N, valid = H - n;
+    const int64_t m = row, step = int64_t(p.M) * 2 * H;
+    uint32_t top = 0;
+    if (m < p.M) {
+        typedef v4i loose __attribute__((aligned(4)));
+        v4i s[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int32_t *at = p.part + 2 * m * H + h * H + n;
+            for (int r = 0; r < p.split; ++r, at += step) {
+                if (valid >= 4) {
+                    s[h] += *reinterpret_cast<const loose *>(at);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        if (e < valid) s[h][e] += at[e];
+                }
+            }
+        }
+        const int e2 = *p.ep.ea + *p.ep.eb;
+        float bg[4], bu[4];
+        load_bias2(p.ep, n, H, bg, bu);
+        with_act(p.ep.act, [&](auto ac) __attribute__((always_inline)) {
+            top = finish_gated4<T, decltype(ac)::value>(s[0], s[1], p.ep, e2, bg, bu, m, n, p.M, H);
+        });
+    }
+    if (p.ep.absmax) {
         top = wave_max_u32(top);
         if ((threadIdx.x & 63) == 0) publish_max_u32(p.ep.absmax, top);
     }

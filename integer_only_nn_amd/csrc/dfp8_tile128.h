@@ -33,7 +33,8 @@ struct Src128 {
     uint32_t off[4];  // of the lane's piece in each of the wavefront's four instructions, at k = 0
     int col[2];       // K-major: its first k, by the instruction's parity
     uint32_t step;    // bytes from one K step to the next
-    __device__ __forceinline__ void init(const int8_t *b, int ld, uint32_t bytes, int r0, int wave, int lane) {
+    // r1: the tile's row r0 + 32 wave of the operand, where its rows do not lie in one run (K-major)
+    __device__ __forceinline__ void init(const int8_t *b, int ld, uint32_t bytes, int r0, int r1, int wave, int lane) {
         const uint64_t a = uint64_t(uintptr_t(b));
         rsrc = v4i{__builtin_amdgcn_readfirstlane(int(uint32_t(a))),
                    __builtin_amdgcn_readfirstlane(int(uint32_t(a >> 32) & 0xffffu)),  // stride 0
@@ -45,7 +46,7 @@ struct Src128 {
             const int row = 8 * (4 * wave + q) + sub;
             if (KMAJOR) {
                 col[q & 1] = 16 * (at ^ g256::fK(row & 15));
-                off[q] = uint32_t(r0 + row) * uint32_t(ld) + uint32_t(col[q & 1]);
+                off[q] = uint32_t(r1 + 8 * q + sub) * uint32_t(ld) + uint32_t(col[q & 1]);
             } else {
                 off[q] = uint32_t(row) * uint32_t(ld) + uint32_t(r0 + 16 * (at ^ fT<128>(row)));
             }
@@ -79,7 +80,9 @@ constexpr int kStages = 2;
 constexpr int kStage128 = 2 * 128 * BK;
 
 // Tile id of a product.
-template <class T, bool A_KM, bool B_KM, bool LINEAR>
+// (GATED: N outputs of B's 2 N rows.  A tile is 64 outputs, 32 of each column of
+// wavefronts, whose 64 rows of B are their gate rows and then their up rows.)
+template <class T, bool A_KM, bool B_KM, bool LINEAR, bool GATED = false>
 __device__ __forceinline__ void run_tile128(const Product &p, int id, int8_t *lds) {
     constexpr bool MASK = A_KM && B_KM;
     const int M = p.M, N = p.N, K = p.K;
@@ -88,12 +91,14 @@ __device__ __forceinline__ void run_tile128(const Product &p, int id, int8_t *ld
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = 64 * (wave >> 1), wn = 64 * (wave & 1);
     int tm, tn;
-    gemm::tile_coords(id, (M + 127) / 128, (N + 127) / 128, tm, tn);
-    const int m0 = tm * 128, n0 = tn * 128;
+    constexpr int kCols = GATED ? 64 : 128;  // outputs of a tile
+    gemm::tile_coords(id, (M + 127) / 128, (N + kCols - 1) / kCols, tm, tn);
+    const int m0 = tm * 128, n0 = tn * kCols;
     Src128<A_KM> sa;
     Src128<B_KM> sb;
-    sa.init(p.A, int(p.lda), uint32_t((A_KM ? M : K) * p.lda), m0, wave, lane);
-    sb.init(p.B, int(p.ldb), uint32_t((B_KM ? N : K) * p.ldb), n0, wave, lane);
+    sa.init(p.A, int(p.lda), uint32_t((A_KM ? M : K) * p.lda), m0, m0 + 32 * wave, wave, lane);
+    sb.init(p.B, int(p.ldb), uint32_t((B_KM ? (GATED ? 2 * N : N) : K) * p.ldb), n0,
+            GATED ? n0 + 32 * (wave >> 1) + (wave & 1) * N : n0 + 32 * wave, wave, lane);
     const uint32_t base = g256::lds_addr(lds);
     const int e2 = *ep.ea + *ep.eb;
     v16i acc[2][2];
@@ -140,6 +145,28 @@ __device__ __forceinline__ void run_tile128(const Product &p, int id, int8_t *ld
                 const int r = 32 * i + (lane & 31), c = 8 * j + 2 * q + (lane >> 5);
                 buf[16 * r + (c ^ (r & 15))] = v4i{s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]};
             }
+    if constexpr (GATED) {
+        const int c = 2 * (lane & 3), n = n0 + wn / 2 + 8 * (lane & 3);
+        float bg[8], bu[8];
+        load_bias2(ep, n, N, bg, bu);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the wavefront's own writes
+        __builtin_amdgcn_wave_barrier();
+        uint32_t top = 0;
+        with_act(ep.act, [&](auto ac) __attribute__((always_inline)) {
+#pragma unroll 2
+            for (int k = 0; k < 4; ++k) {
+                const int r = 16 * k + (lane >> 2);
+                const auto at = [&](int i) __attribute__((always_inline)) { return buf[16 * r + ((c + i) ^ (r & 15))]; };
+                top = max(top, finish_gated8<T, decltype(ac)::value>(at(0), at(1), at(8), at(9), ep, e2, bg, bu,
+                                                                     int64_t(m0) + wm + r, n, M, N));
+            }
+        });
+        if (ep.absmax) {
+            top = wave_max_u32(top);
+            if (lane == 0) publish_max_u32(ep.absmax, top);
+        }
+        return;
+    }
     const int c = 2 * (lane & 7), n = n0 + wn + 8 * (lane & 7);
     float bias[8] = {};
     if (!LINEAR) load_bias(ep, n, N, bias);
@@ -160,10 +187,10 @@ __device__ __forceinline__ void run_tile128(const Product &p, int id, int8_t *ld
     }
 }
 
-template <class T>
+template <class T, bool GATED = false>
 __global__ __launch_bounds__(NT) void tile128_kernel(Product p) {
     __shared__ __attribute__((aligned(1024))) int8_t lds[kStages * kStage128];
-    run_tile128<T, true, true, false>(p, int(blockIdx.x), lds);
+    run_tile128<T, true, true, false, GATED>(p, int(blockIdx.x), lds);
 }
 
 // dX's product d and G's g in one grid, where each alone is a single round (2048^3:

@@ -94,7 +94,45 @@ __device__ __forceinline__ uint32_t finish_wave(const v16i (&acc)[4][4], int8_t 
     return top;
 }
 
-template <class T, bool A_KM, bool B_KM, bool LINEAR>
+// The same of a gated layer's sums: a wavefront has 64 outputs, their gate sums
+// in acc[.][0..1] and the up sums in acc[.][2..3]; 64 rows at a time.
+template <class T, int ACT>
+__device__ __forceinline__ uint32_t finish_wave_gated(const v16i (&acc)[4][4], int8_t *lds, const Epi &ep, int e2,
+                                                      int64_t m0, int n0, int M, int H, int lane) {
+    uint32_t top = 0;
+    v4i *buf = reinterpret_cast<v4i *>(lds);
+    const int c = 2 * (lane & 7), n = n0 + 8 * (lane & 7);
+    float bg[8], bu[8];
+    load_bias2(ep, n, H, bg, bu);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v16i &a = acc[2 * h + i][j];
+                    const int r = 32 * i + (lane & 31), p = 8 * j + 2 * q + (lane >> 5);
+                    buf[32 * r + (p ^ (r & 15))] = v4i{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the wavefront's own writes
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+        for (int k = 0; k < 8; ++k) {
+            const int r = 8 * k + (lane >> 3);
+            const auto at = [&](int i) __attribute__((always_inline)) { return buf[32 * r + ((c + i) ^ (r & 15))]; };
+            top = max(top, finish_gated8<T, ACT>(at(0), at(1), at(16), at(17), ep, e2, bg, bu, m0 + 64 * h + r, n, M, H));
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    return top;
+}
+
+// GATED: N outputs of B's 2 N rows.  A tile is 128 outputs, 64 of each column of
+// wavefronts, whose 128 rows of B are their gate rows and then their up rows; so
+// a lane's sums of an output's two halves meet without an exchange.
+template <class T, bool A_KM, bool B_KM, bool LINEAR, bool GATED = false>
 __global__ __launch_bounds__(g256::NT, 1) void tile256_kernel(const int8_t *__restrict__ A, int64_t lda,
                                                               const int8_t *__restrict__ B, int64_t ldb,
                                                               uint32_t a_bytes, uint32_t b_bytes, Epi ep, int M, int N,
@@ -109,13 +147,15 @@ __global__ __launch_bounds__(g256::NT, 1) void tile256_kernel(const int8_t *__re
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int tm, tn;
-    gemm::tile_coords(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    constexpr int kCols = GATED ? BN / 2 : BN;  // outputs of a tile
+    gemm::tile_coords(blockIdx.x, (M + BM - 1) / BM, (N + kCols - 1) / kCols, tm, tn);
+    const int m0 = tm * BM, n0 = tn * kCols;
 
     EdgeSrc<A_KM> ta;
     EdgeSrc<B_KM> tb;
     ta.init_edge(A, int(lda), a_bytes, m0, wave, lane);
     tb.init_edge(B, int(ldb), b_bytes, n0, wave, lane);
+    if (GATED) tb.wave_off = uint32_t(n0 + 64 * (wave >> 1) + (wave & 1) * N) * uint32_t(ldb);
     FragSrc<A_KM> fa;
     FragSrc<B_KM> fb;
     fa.init(wm * 128, lane);
@@ -216,7 +256,11 @@ __global__ __launch_bounds__(g256::NT, 1) void tile256_kernel(const int8_t *__re
     int8_t *mine = wave == 0 ? sA0 : wave == 1 ? sB0 : wave == 2 ? sA1 : sB1;
     uint32_t top = 0;
     with_act(LINEAR ? int(IONN_ACT_NONE) : ep.act, [&](auto ac) __attribute__((always_inline)) {
-        top = finish_wave<T, decltype(ac)::value, LINEAR>(acc, mine, ep, e2, int64_t(m0) + wm * 128, n0 + wn * 128, M, N,
+        if constexpr (GATED)
+            top = finish_wave_gated<T, decltype(ac)::value>(acc, mine, ep, e2, int64_t(m0) + wm * 128, n0 + wn * 64, M, N,
+                                                            lane);
+        else
+            top = finish_wave<T, decltype(ac)::value, LINEAR>(acc, mine, ep, e2, int64_t(m0) + wm * 128, n0 + wn * 128, M, N,
                                                           lane);
     });
     if (!LINEAR && ep.absmax) {

@@ -676,6 +676,45 @@ def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None
         check(rc, "dfp8_linear_bwd")
 
 
+def dfp8_gated_fwd_workspace_bytes(B, IN, H):
+    return int(lib().dfp8_gated_fwd_workspace_bytes(int(B), int(IN), int(H)))
+
+
+def dfp8_gated_fwd(X, eX, W, eW, Y, bias=None, act="silu", Z=None, absmax_Y=None, workspace=None, stream=None):
+    """W: [2 H][IN], the gate's rows and then the up projection's; Z: [B][2 H]."""
+    xs, dt = X.shape, Y.dtype
+    B, IN = xs
+    H = W.shape[0] // 2
+    ws, nws = _space(workspace)
+    rc = lib().dfp8_gated_fwd(_m(X, i8, xs, "X"), _s(eX, i32, "eX"), _m(W, i8, (2 * H, IN), "W"), _s(eW, i32, "eW"),
+                              _v(bias, f32, 2 * H, "bias"), _act(act), _m(Z, dt, (B, 2 * H), "Z"),
+                              _m(Y, dt, (B, H), "Y"), _dtype(Y, "Y"), B, IN, H, _s(absmax_Y, u32, "absmax_Y"), ws, nws,
+                              _on(stream, Y))
+    if rc:
+        check(rc, "dfp8_gated_fwd")
+
+
+def dfp8_gated_bwd_workspace_bytes(B, IN, H):
+    return int(lib().dfp8_gated_bwd_workspace_bytes(int(B), int(IN), int(H)))
+
+
+def dfp8_gated_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None, workspace=None, status_out=None,
+                   stream=None):
+    """X and eX are read for G, W and eW for dX."""
+    ys, dt = dY.shape, dY.dtype
+    B, H = ys
+    IN = (X if X is not None else W).shape[1]
+    xs, zs, gs = (B, IN), (B, 2 * H), (2 * H, IN)
+    ws, nws = _space(workspace)
+    rc = lib().dfp8_gated_bwd(_m(dY, dt, ys, "dY"), _m(Z, dt, zs, "Z"), _act(act), _dtype(dY, "dY"),
+                              _m(X, i8, xs, "X"), _s(eX, i32, "eX"), _m(W, i8, gs, "W"), _s(eW, i32, "eW"),
+                              _m(dZ8, i8, zs, "dZ8"), _s(edZ, i32, "edZ"), _m(dX, dt, xs, "dX"), _m(G, dt, gs, "G"),
+                              _v(gb, f32, 2 * H, "gb"), B, IN, H, _s(status_out, i32, "status_out"), ws, nws,
+                              _on(stream, dY))
+    if rc:
+        check(rc, "dfp8_gated_bwd")
+
+
 def dfp8_linear_path(product, B, IN, OUT):
     """"rows", "tiles 256", "tiles 128", "tiles" or "narrow", for product "fwd", "dX" or "G"."""
     p = lib().dfp8_linear_path(("fwd", "dX", "G").index(product), int(B), int(IN), int(OUT))

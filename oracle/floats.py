@@ -75,6 +75,22 @@ def linear_fwd(X, eX, W, eW, bias, kind, residual):
     return y, z
 
 
+def gated_fwd(X, eX, W, eW, bias, kind):
+    """(y, z) in float64; W: the gate's rows and then the up projection's."""
+    z = np.ldexp(product(X, W).astype(np.float64), eX + eW)
+    if bias is not None:
+        z = z + bias.astype(np.float64)
+    H = W.shape[0] // 2
+    return act(z[:, :H], kind) * z[:, H:], z
+
+
+def gated_error(dY, Z, kind):
+    """The error of z, in float64."""
+    H = Z.shape[1] // 2
+    g, u = np.asarray(Z[:, :H], np.float64), np.asarray(Z[:, H:], np.float64)
+    return np.concatenate([dY * u * act_grad(g, kind), dY * act(g, kind)], 1)
+
+
 def layer_norm_fwd(x, gamma, beta, eps):
     """(y, mean, rstd) in float64."""
     x = np.asarray(x, np.float64)
