@@ -840,6 +840,59 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
                         int64_t rows, int64_t cols, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/* What lies between two blocks of a residual stream: the norm after a block's
+ * output a, its gate, the scaled residual, and the norm before the next block,
+ *   p = N_a(a),  y[r][c] = alpha * x[r][c] + gate[r / gate_rows][c] * p[r][c],
+ *   n = N_y(y)
+ * with the statistics of y and n taken from y before it is rounded.  norm_a,
+ * norm_y: IONN_NORM_NONE (the row itself), _LAYER (as ionn_layer_norm_fwd) or
+ * _RMS: N(v)[c] = v[c] * rstd * gamma[c], rstd = 1 / sqrt(sum_c v[c]^2 / cols +
+ * eps).  a, x, y, n: dtype [rows][cols]; gamma_* (nullable: 1), beta_* (nullable:
+ * 0; layer norms only): float [cols]; gate (nullable: 1): float
+ * [ceil(rows / gate_rows)][cols], gate_rows rows share a gate (0, or rows and
+ * more: all); mean_* (layer norms only), rstd_* (nullable): float [rows], written
+ * for the backward pass.  a NULL: y = alpha * x (the norm before the first
+ * block).  y NULL or n NULL: not written (without n nor are
+ * its norm's other results); n NULL where norm_y is IONN_NORM_NONE.  y and n may be a or x.  absmax_n as in dfp8_linear_fwd.
+ * rows >= 0 and below 2^31, 0 <= cols <= 16384; eps >= 0; alpha finite. */
+enum { IONN_NORM_NONE = 0, IONN_NORM_LAYER = 1, IONN_NORM_RMS = 2 };
+int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a,
+                           const float *gamma_a, const float *beta_a,
+                           const float *gate, int64_t gate_rows, double alpha,
+                           int norm_y, const float *gamma_y,
+                           const float *beta_y, double eps, void *y, void *n,
+                           float *mean_a, float *rstd_a, float *mean_y,
+                           float *rstd_y, int dtype, int64_t rows, int64_t cols,
+                           uint32_t *absmax_n, void *stream);
+
+/* Its gradient, for the errors dy of y (nullable: 0) and dn of n, with h_a, h_y
+ * the normalised rows ((v - mean) * rstd; without a norm v itself):
+ *   t  = dy + N_y'(dn)      (float32, not stored; N_y' as dx in
+ *                            ionn_layer_norm_bwd, without mean_c(d) for _RMS)
+ *   dx = alpha * t,  da = N_a'(gate * t)
+ *   dgate[g][c] = sum over the rows of g of t * p
+ *   dgamma_a[c] = sum_r gate * t * h_a,  dbeta_a[c] = sum_r gate * t
+ *   dgamma_y[c] = sum_r dn * h_y,        dbeta_y[c] = sum_r dn
+ * y: as the forward stored it; the statistics: as it left them.  Every output is
+ * nullable; da and dx may be dy, dn, a or y, but not each other.  The vectors'
+ * gradients are float32, summed in an order that the sizes fix (0 for rows = 0);
+ * beta_a is read for dgate.  workspace: 16-byte aligned,
+ * ionn_residual_norm_bwd_workspace_bytes(rows, cols, gate_rows) bytes (needed
+ * where a vector's gradient is asked for; gate_rows = 0 without a gate). */
+size_t ionn_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t cols,
+                                              int64_t gate_rows);
+int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a,
+                           const void *y, int norm_a, const float *gamma_a,
+                           const float *beta_a, const float *gate,
+                           int64_t gate_rows, double alpha, int norm_y,
+                           const float *gamma_y, const float *mean_a,
+                           const float *rstd_a, const float *mean_y,
+                           const float *rstd_y, void *da, void *dx,
+                           float *dgamma_a, float *dbeta_a, float *dgate,
+                           float *dgamma_y, float *dbeta_y, int dtype,
+                           int64_t rows, int64_t cols, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* One AdamW step of L tensors, in place.  Per element, each operation
  * rounded to float32 on its own (none fused):
  *   g = G * grad_scale

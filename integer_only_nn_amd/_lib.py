@@ -88,6 +88,11 @@ SIGNATURES = {
     "ionn_layer_norm_fwd": (_I, [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I, _I64, _I64, _P, _P]),
     "ionn_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "ionn_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "ionn_residual_norm_fwd": (_I, [_P, _P, _I, _P, _P, _P, _I64, ctypes.c_double, _I, _P, _P, ctypes.c_double, _P, _P, _P,
+                                    _P, _P, _P, _I, _I64, _I64, _P, _P]),
+    "ionn_residual_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "ionn_residual_norm_bwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _I64, ctypes.c_double, _I, _P, _P, _P, _P, _P, _P, _P,
+                                    _P, _P, _P, _P, _P, _I, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "ionn_adamw_step": (_I, [_I, _P, _P, _I, _P, _P, _P, _I, _P, _I64] + [ctypes.c_double] * 5 + [_P, _P, _P, _P, _P]),
     "ionn_adamw_step_carried": (_I, [_I, _P, _P, _I, _P, _P, _P, _P, _P, _I64] + [ctypes.c_double] * 5 +
                                 [_P, _P, _P, _P, _P]),

@@ -1,0 +1,723 @@
+// What lies between two blocks of a residual stream, in one pass: the norm after
+// a block, its gate, the scaled residual and the norm before the next block; and
+// the gradient of it all ("Mixed Precision Training of Convolutional Neural
+// Networks using Integer Operations", section 4: the operations around the
+// integer kernels run in floating point).
+//
+//   p = N_a(a),  y = alpha x + gate p,  n = N_y(y)
+//   t = dy + N_y'(dn),  dx = alpha t,  da = N_a'(gate t),
+//   dgate = sum t p,  dgamma_a = sum gate t h_a,  dbeta_a = sum gate t,
+//   dgamma_y = sum dn h_y,  dbeta_y = sum dn
+//
+// with N a layer norm, an RMS norm or nothing, h the normalised row, and a gate
+// of each `gate_rows` rows.  As single operations they would move the stream
+// through memory once each; together a and x are read and y and n written once
+// (forward), a, y, dy and dn read and da and dx written once (backward), and HBM
+// bounds both.  A row lies in registers, up to eight columns a thread, and the
+// next row's loads are in flight while a row's sums are taken.
+//
+// The backward pass needs only four column sums for its five vectors: S1 = sum t
+// and Sh = sum t h_a of the rows that share a gate give that gate's gradient
+// (gamma_a Sh + beta_a S1) and, times the gate, dgamma_a and dbeta_a.  A
+// workgroup takes a run of rows that share a gate and leaves one partial row of
+// each, added in a second, fixed-order pass; where there are more gates than
+// workgroups it takes whole gates, whose gradients it writes itself.
+#include "float_ops.h"
+
+namespace ionn {
+namespace {
+
+constexpr int64_t kMaxCols = 16384;
+constexpr int kMaxGroups = 512;  // workgroups of the backward pass
+
+// Sums of v over the TPR threads that share a row (whole wavefronts); every one
+// of them gets them.  buf: the wavefronts' sums, twice over, so that one barrier
+// per call suffices (ph alternates).
+template <int TPR, int V>
+__device__ __forceinline__ void row_sums(float (&v)[V], float (*buf)[V][TPR / 64 + 1], int &ph) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = wave_sum(v[k]);
+    if (TPR == 64) return;
+    float(*b)[TPR / 64 + 1] = buf[ph];
+    ph ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) b[k][threadIdx.x >> 6] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        v[k] = b[k][0];
+#pragma unroll
+        for (int w = 1; w < TPR / 64; ++w) v[k] += b[k][w];
+    }
+}
+
+struct Norm {
+    int kind;  // IONN_NORM_*
+    const float *gamma, *beta;
+    float *mean, *rstd;
+};
+
+struct Forward {
+    const void *a, *x;
+    void *y, *n;
+    Norm na, ny;
+    const float *gate;
+    int64_t rows;
+    uint32_t gate_rows;
+    int cols;
+    float alpha, eps;
+    uint32_t *absmax;
+};
+
+// The columns of a thread: (i TPR + t) VE .. + VE - 1, i < NV.
+template <int VE, int TPR, int NV>
+struct Cols {
+    float v[NV][VE];
+    // a float vector, or `none` without one; zeros past the end
+    __device__ __forceinline__ void load(const float *p, int cols, int t, float none) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE;
+            const auto r = load_raw<float, VE>(p + c, p ? cols - c : 0);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] = p || c + e >= cols ? r[e] : none;
+        }
+    }
+};
+
+// v := the normalised row (zeros past its end); returns mean and rstd.
+template <int VE, int TPR, int NV>
+__device__ __forceinline__ void normalise(float (&v)[NV][VE], int kind, float eps, int cols, int t,
+                                          float (*buf)[1][TPR / 64 + 1], int &ph, float &mean, float &rstd) {
+    const float n = float(cols);
+    mean = 0.0f;
+    if (kind == IONN_NORM_LAYER) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) s[0] += v[i][e];
+        row_sums<TPR, 1>(s, buf, ph);
+        mean = s[0] / n;
+    }
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const float d = (i * TPR + t) * VE + e < cols ? v[i][e] - mean : 0.0f;
+            v[i][e] = d;
+            q[0] += d * d;
+        }
+    row_sums<TPR, 1>(q, buf, ph);
+    rstd = 1.0f / sqrtf(q[0] / n + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[i][e] *= rstd;
+}
+
+constexpr int fwd_threads(int tpr) { return tpr == 64 ? 256 : tpr; }
+
+template <class T, int VE, int TPR, int NV>
+__global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(Forward f) {
+    __shared__ float buf[2][1][TPR / 64 + 1];
+    constexpr int kRows = fwd_threads(TPR) / TPR;  // rows a workgroup takes at once
+    constexpr bool kHold = NV * VE <= 8;           // the vectors stay in registers
+    typedef Cols<VE, TPR, NV> Vector;
+    const T *a = static_cast<const T *>(f.a), *x = static_cast<const T *>(f.x);
+    T *y = static_cast<T *>(f.y), *n = static_cast<T *>(f.n);
+    const int t = threadIdx.x % TPR, cols = f.cols;
+    const int64_t step = int64_t(gridDim.x) * kRows;
+    int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
+    int ph = 0;
+    uint32_t top = 0;
+    typename Vec<T, VE>::type ra[NV], rx[NV];
+    const auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE, valid = row < f.rows ? cols - c : 0;
+            if (a) ra[i] = load_raw<T, VE>(a + row * cols + c, valid);
+            rx[i] = load_raw<T, VE>(x + row * cols + c, valid);
+        }
+    };
+    load_row(r);
+    Vector ga, ba, gy, by, gate;
+    const auto load_norms = [&]() __attribute__((always_inline)) {
+        ga.load(f.na.gamma, cols, t, 1.0f);
+        ba.load(f.na.beta, cols, t, 0.0f);
+        gy.load(f.ny.gamma, cols, t, 1.0f);
+        by.load(f.ny.beta, cols, t, 0.0f);
+    };
+    if (kHold) load_norms();
+    uint32_t group = ~0u;
+    for (; r < f.rows; r += step) {
+        float v[NV][VE], w[NV][VE];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                v[i][e] = a ? float(ra[i][e]) : 0.0f;
+                w[i][e] = f.alpha * float(rx[i][e]);
+            }
+        if (r + step < f.rows) load_row(r + step);
+        if (!kHold) load_norms();
+        const uint32_t g = f.gate ? uint32_t(r) / f.gate_rows : 0u;
+        if (!kHold || g != group) gate.load(f.gate ? f.gate + int64_t(g) * cols : nullptr, cols, t, 1.0f);
+        group = g;
+        if (a) {
+            if (f.na.kind != IONN_NORM_NONE) {
+                float mean, rstd;
+                normalise<VE, TPR, NV>(v, f.na.kind, f.eps, cols, t, buf, ph, mean, rstd);
+                if (t == 0) {
+                    if (f.na.mean) f.na.mean[r] = mean;
+                    if (f.na.rstd) f.na.rstd[r] = rstd;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) w[i][e] += gate.v[i][e] * (v[i][e] * ga.v[i][e] + ba.v[i][e]);
+        }
+        if (y) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * VE;
+                if (c < cols) store_vec<T, VE>(y + r * cols + c, w[i], cols - c);
+            }
+        }
+        if (n == nullptr) continue;
+        float mean, rstd;
+        normalise<VE, TPR, NV>(w, f.ny.kind, f.eps, cols, t, buf, ph, mean, rstd);
+        if (t == 0) {
+            if (f.ny.mean) f.ny.mean[r] = mean;
+            if (f.ny.rstd) f.ny.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE, valid = cols - c;
+            if (valid <= 0) continue;
+            float o[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                o[e] = w[i][e] * gy.v[i][e] + by.v[i][e];
+                if (e < valid) top = max(top, mag_bits(o[e]));
+            }
+            store_vec<T, VE>(n + r * cols + c, o, valid);
+        }
+    }
+    if (f.absmax) {
+        top = wave_max_u32(top);
+        if ((threadIdx.x & 63) == 0) publish_max_u32(f.absmax, top);
+    }
+}
+
+// ---- backward ------------------------------------------------------------------
+
+struct Backward {
+    const void *dy, *dn, *a, *y;
+    void *da, *dx;
+    Norm na, ny;
+    const float *gate;
+    int64_t rows;
+    uint32_t gate_rows, chunks;  // rows that share a gate; runs that they are cut into
+    uint32_t chunk_rows, units;  // rows of a run; runs of all gates
+    int cols;
+    float alpha;
+    // [units][2][cols] (Sh, S1; with whole gates [workgroups][2][cols], dgamma_a
+    // and dbeta_a), [workgroups][2][cols] (dgamma_y, dbeta_y); nullable
+    float *part_a, *part_y;
+    float *dgate;  // with whole gates; nullable
+};
+
+constexpr int bwd_threads(int tpr) { return tpr == 64 ? 512 : tpr; }
+
+// h := the normalised rows of v (zeros past the end).
+template <class T, int VE, int TPR, int NV>
+__device__ __forceinline__ void rows_of(const typename Vec<T, VE>::type (&raw)[NV], float mean, float rstd, int cols,
+                                        int t, float (&h)[NV][VE]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VE;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) h[i][e] = c + e < cols ? (float(raw[i][e]) - mean) * rstd : 0.0f;
+    }
+}
+
+// d := rstd (d - mean(d) - h mean(d h)), the first mean for a layer norm only.
+template <int VE, int TPR, int NV>
+__device__ __forceinline__ void project(float (&d)[NV][VE], const float (&h)[NV][VE], int kind, float rstd, float n,
+                                        float (*buf)[2][TPR / 64 + 1], int &ph) {
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            s[0] += d[i][e];
+            s[1] += d[i][e] * h[i][e];
+        }
+    row_sums<TPR, 2>(s, buf, ph);
+    const float c1 = kind == IONN_NORM_LAYER ? s[0] / n : 0.0f, c2 = s[1] / n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) d[i][e] = rstd * (d[i][e] - c1 - h[i][e] * c2);
+}
+
+// WHOLE: a unit is a gate's rows, taken by one of a workgroup's row groups.
+template <class T, int VE, int TPR, int NV, bool WHOLE>
+__global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Backward b) {
+    constexpr int kRows = bwd_threads(TPR) / TPR;
+    typedef Cols<VE, TPR, NV> Vector;
+    __shared__ float buf[2][2][TPR / 64 + 1];
+    __shared__ float fold[kRows > 1 ? kRows * NV * VE * TPR : 1];
+    const T *dy = static_cast<const T *>(b.dy), *dn = static_cast<const T *>(b.dn);
+    const T *a = static_cast<const T *>(b.a), *y = static_cast<const T *>(b.y);
+    T *da = static_cast<T *>(b.da), *dx = static_cast<T *>(b.dx);
+    const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR, cols = b.cols;
+    const float n = float(cols);
+    int ph = 0;
+    // S: Sh, S1 of the run at hand; Y: dgamma_y, dbeta_y of all runs; A (WHOLE): dgamma_a, dbeta_a of all runs
+    Vector gy, ga, S[2], Y[2], A[WHOLE ? 2 : 1];
+    gy.load(b.ny.gamma, cols, t, 1.0f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) Y[k].v[i][e] = A[WHOLE ? k : 0].v[i][e] = 0.0f;
+
+    // the row groups of a workgroup one after the other, to two rows of partial sums
+    const auto leave = [&](Vector (&s)[2], float *to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (kRows > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) fold[((rg * NV + i) * VE + e) * TPR + t] = s[k].v[i][e];
+                __syncthreads();
+            }
+            if (rg > 0) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * VE;
+                float o[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    o[e] = s[k].v[i][e];
+#pragma unroll
+                    for (int g = 1; g < kRows; ++g) o[e] += fold[((g * NV + i) * VE + e) * TPR + t];
+                }
+                if (c < cols) store_vec<float, VE>(to + int64_t(k) * cols + c, o, cols - c);
+            }
+        }
+    };
+
+    typename Vec<T, VE>::type r_dy[NV], r_dn[NV], r_a[NV], r_y[NV];
+    float mean_a = 0.0f, rstd_a = 1.0f, mean_y = 0.0f, rstd_y = 1.0f;
+    const auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+        if (b.na.rstd) rstd_a = b.na.rstd[row];
+        if (b.na.mean) mean_a = b.na.mean[row];
+        if (b.ny.rstd) rstd_y = b.ny.rstd[row];
+        if (b.ny.mean) mean_y = b.ny.mean[row];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE;
+            if (dy) r_dy[i] = load_raw<T, VE>(dy + row * cols + c, cols - c);
+            if (dn) r_dn[i] = load_raw<T, VE>(dn + row * cols + c, cols - c);
+            if (dn) r_y[i] = load_raw<T, VE>(y + row * cols + c, cols - c);
+            if (a) r_a[i] = load_raw<T, VE>(a + row * cols + c, cols - c);
+        }
+    };
+    constexpr uint32_t kEach = WHOLE ? kRows : 1;  // units of a workgroup at once
+    constexpr int kStep = WHOLE ? 1 : kRows;
+    for (uint32_t unit = blockIdx.x * kEach + (WHOLE ? rg : 0); unit < b.units; unit += gridDim.x * kEach) {
+        const uint32_t group = unit / b.chunks, chunk = unit - group * b.chunks;
+        const int64_t first = int64_t(group) * b.gate_rows;
+        const int64_t last = min(b.rows, first + min(int64_t(b.gate_rows), int64_t(chunk + 1) * b.chunk_rows));
+        int64_t r = first + int64_t(chunk) * b.chunk_rows + (WHOLE ? 0 : rg);
+        // gate and gamma_a as one factor
+        {
+            Vector g;
+            g.load(b.gate ? b.gate + int64_t(group) * cols : nullptr, cols, t, 1.0f);
+            ga.load(b.na.gamma, cols, t, 1.0f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    ga.v[i][e] *= g.v[i][e];
+                    S[0].v[i][e] = S[1].v[i][e] = 0.0f;
+                }
+        }
+        if (r < last) load_row(r);
+        for (; r < last; r += kStep) {
+            float d[NV][VE], h[NV][VE], past[NV][VE];
+            const float mu_a = mean_a, rs_a = rstd_a, rs_y = rstd_y;
+            if (dn) {
+                rows_of<T, VE, TPR, NV>(r_y, mean_y, rs_y, cols, t, h);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float v = float(r_dn[i][e]);
+                        Y[0].v[i][e] += v * h[i][e];
+                        Y[1].v[i][e] += v;
+                        d[i][e] = v * gy.v[i][e];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) past[i][e] = dy ? float(r_dy[i][e]) : 0.0f;
+            typename Vec<T, VE>::type row_a[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) row_a[i] = r_a[i];
+            if (r + kStep < last) load_row(r + kStep);
+            if (dn) {
+                project<VE, TPR, NV>(d, h, b.ny.kind, rs_y, n, buf, ph);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) past[i][e] += d[i][e];
+            }
+            if (dx) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * TPR + t) * VE;
+                    float o[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) o[e] = b.alpha * past[i][e];
+                    if (c < cols) store_vec<T, VE>(dx + r * cols + c, o, cols - c);
+                }
+            }
+            if (!a) continue;
+            rows_of<T, VE, TPR, NV>(row_a, mu_a, rs_a, cols, t, h);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    S[0].v[i][e] += past[i][e] * h[i][e];
+                    S[1].v[i][e] += past[i][e];
+                    d[i][e] = past[i][e] * ga.v[i][e];
+                }
+            if (da) {
+                if (b.na.kind != IONN_NORM_NONE) project<VE, TPR, NV>(d, h, b.na.kind, rs_a, n, buf, ph);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * TPR + t) * VE;
+                    if (c < cols) store_vec<T, VE>(da + r * cols + c, d[i], cols - c);
+                }
+            }
+        }
+        if (!WHOLE) {
+            if (b.part_a) leave(S, b.part_a + int64_t(unit) * 2 * cols);
+            continue;
+        }
+        Vector g, gamma, beta;
+        g.load(b.gate + int64_t(group) * cols, cols, t, 1.0f);
+        gamma.load(b.na.gamma, cols, t, 1.0f);
+        beta.load(b.na.beta, cols, t, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VE;
+            float o[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                o[e] = gamma.v[i][e] * S[0].v[i][e] + beta.v[i][e] * S[1].v[i][e];
+                A[0].v[i][e] += g.v[i][e] * S[0].v[i][e];
+                A[WHOLE ? 1 : 0].v[i][e] += g.v[i][e] * S[1].v[i][e];
+            }
+            if (b.dgate && c < cols) store_vec<float, VE>(b.dgate + int64_t(group) * cols + c, o, cols - c);
+        }
+    }
+    if constexpr (WHOLE) {
+        if (b.part_a) leave(A, b.part_a + int64_t(blockIdx.x) * 2 * cols);
+    }
+    if (b.part_y) leave(Y, b.part_y + int64_t(blockIdx.x) * 2 * cols);
+}
+
+// The partial rows added up, 64 columns a workgroup, in an order that the sizes
+// fix: workgroups of blockIdx.y = 0 those of the gates, of 1 those of N_y.  Where
+// a gate's rows were cut into many runs, 16 groups of threads share a gate's runs;
+// elsewhere they share the gates.
+constexpr int kSumGroups = 16;
+
+struct Sums {
+    const float *part_a, *part_y;
+    const float *gate, *gamma_a, *beta_a;
+    float *dgate, *dgamma_a, *dbeta_a, *dgamma_y, *dbeta_y;
+    uint32_t groups, chunks, parts;  // parts: workgroups of the first pass
+    int cols;
+    bool whole, a, y;  // part_a is of whole gates; asked for
+};
+
+__global__ __launch_bounds__(64 * kSumGroups) void residual_norm_sum_kernel(Sums s) {
+    __shared__ float red[2][kSumGroups][64];
+    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int64_t cols = s.cols, c = int64_t(blockIdx.x) * 64 + lane;
+    const bool in = c < cols;
+    // both sums of `count` partial rows from p on, every kSumGroups-th (in all groups' threads alike)
+    const auto run = [&](const float *p, uint32_t from, uint32_t count, uint32_t by, float (&v)[2])
+        __attribute__((always_inline)) {
+            v[0] = v[1] = 0.0f;
+            if (!in) return;
+#pragma unroll 8
+            for (uint32_t k = from; k < count; k += by) {
+                v[0] += p[int64_t(k) * 2 * cols + c];
+                v[1] += p[int64_t(k) * 2 * cols + cols + c];
+            }
+        };
+    // v of all groups, in order (every group gets it)
+    const auto join = [&](float (&v)[2]) __attribute__((always_inline)) {
+        __syncthreads();
+        red[0][grp][lane] = v[0];
+        red[1][grp][lane] = v[1];
+        __syncthreads();
+        v[0] = v[1] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSumGroups; ++k) {
+            v[0] += red[0][k][lane];
+            v[1] += red[1][k][lane];
+        }
+    };
+    float v[2];
+    if (blockIdx.y == 1 ? !s.y : !s.a) return;
+    if (blockIdx.y == 1 || s.whole) {
+        run(blockIdx.y == 1 ? s.part_y : s.part_a, grp, s.parts, kSumGroups, v);
+        join(v);
+        float *to0 = blockIdx.y == 1 ? s.dgamma_y : s.dgamma_a, *to1 = blockIdx.y == 1 ? s.dbeta_y : s.dbeta_a;
+        if (grp == 0 && in) {
+            if (to0) to0[c] = v[0];
+            if (to1) to1[c] = v[1];
+        }
+        return;
+    }
+    const float gamma = s.gamma_a && in ? s.gamma_a[c] : 1.0f, beta = s.beta_a && in ? s.beta_a[c] : 0.0f;
+    float all[2] = {0.0f, 0.0f};
+    const auto add = [&](uint32_t g, const float (&w)[2], bool write) __attribute__((always_inline)) {
+        if (!in) return;
+        if (s.dgate && write) s.dgate[int64_t(g) * cols + c] = gamma * w[0] + beta * w[1];
+        const float gate = s.gate ? s.gate[int64_t(g) * cols + c] : 1.0f;
+        all[0] += gate * w[0];
+        all[1] += gate * w[1];
+    };
+    if (s.chunks >= uint32_t(kSumGroups)) {
+        for (uint32_t g = 0; g < s.groups; ++g) {
+            run(s.part_a + int64_t(g) * s.chunks * 2 * cols, grp, s.chunks, kSumGroups, v);
+            join(v);
+            add(g, v, grp == 0);
+        }
+    } else {
+        for (uint32_t g = grp; g < s.groups; g += kSumGroups) {
+            run(s.part_a + int64_t(g) * s.chunks * 2 * cols, 0, s.chunks, 1, v);
+            add(g, v, true);
+        }
+        join(all);
+    }
+    if (grp == 0 && in) {
+        if (s.dgamma_a) s.dgamma_a[c] = all[0];
+        if (s.dbeta_a) s.dbeta_a[c] = all[1];
+    }
+}
+
+// f(threads per row, vectors per thread) for a row of cols columns: one wavefront
+// per row while that takes few vectors a lane (no barrier), then the fewest
+// threads that hold it in eight columns each.
+template <int VE, bool BWD, class F>
+void with_shape(int64_t cols, F &&f) {
+    const int64_t v = (cols + VE - 1) / VE;
+    constexpr bool kWide = VE == 8 && !BWD;
+    if (v <= 64) f(IntC<64>{}, IntC<1>{});
+    else if (v <= 128) f(IntC<kWide ? 128 : 64>{}, IntC<kWide ? 1 : 2>{});
+    else if (v <= 256) f(IntC<256>{}, IntC<1>{});
+    else if (v <= 512) f(IntC<VE == 8 ? 512 : 256>{}, IntC<VE == 8 ? 1 : 2>{});
+    else if (v <= 1024) f(IntC<VE == 8 ? 1024 : 512>{}, IntC<VE == 8 ? 1 : 2>{});
+    else if (v <= 2048) f(IntC<1024>{}, IntC<2>{});
+    else if constexpr (VE == 4) f(IntC<1024>{}, IntC<4>{});
+}
+
+// How the rows are cut for the backward pass.
+struct Runs {
+    uint32_t groups, chunks, chunk_rows;
+    uint32_t units() const { return groups * chunks; }
+    bool whole() const { return groups > uint32_t(kMaxGroups); }
+};
+Runs runs_of(int64_t rows, int64_t cols, int64_t gate_rows) {
+    const int64_t groups = (rows + gate_rows - 1) / gate_rows, least = cols <= 1024 ? 8 : 4;
+    int64_t chunks = kMaxGroups / groups;
+    if (chunks > (gate_rows + least - 1) / least) chunks = (gate_rows + least - 1) / least;
+    if (chunks < 1) chunks = 1;
+    const int64_t chunk_rows = (gate_rows + chunks - 1) / chunks;
+    return Runs{uint32_t(groups), uint32_t((gate_rows + chunk_rows - 1) / chunk_rows), uint32_t(chunk_rows)};
+}
+
+bool sizes_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 0 && rows <= kMaxDim && cols <= kMaxCols; }
+
+// Whether a tensor of `bytes` is another or lies apart from it.
+bool same_or_apart(const void *a, const void *b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || x == y || x + bytes <= y || y + bytes <= x;
+}
+bool apart(const void *a, const void *b, size_t bytes) { return !a || (a != b && same_or_apart(a, b, bytes)); }
+
+bool kind_ok(int kind) { return kind == IONN_NORM_NONE || kind == IONN_NORM_LAYER || kind == IONN_NORM_RMS; }
+
+}  // namespace
+}  // namespace ionn
+
+using namespace ionn;
+
+extern "C" {
+
+int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a, const float *gamma_a, const float *beta_a,
+                           const float *gate, int64_t gate_rows, double alpha, int norm_y, const float *gamma_y,
+                           const float *beta_y, double eps, void *y, void *n, float *mean_a, float *rstd_a,
+                           float *mean_y, float *rstd_y, int dtype, int64_t rows, int64_t cols, uint32_t *absmax_n,
+                           void *stream) {
+    clear_error();
+    IONN_REQUIRE(dtype_ok(dtype), IONN_ERR_ARG, "ionn_residual_norm_fwd: dtype = %d", dtype);
+    IONN_REQUIRE(kind_ok(norm_a) && kind_ok(norm_y), IONN_ERR_ARG, "ionn_residual_norm_fwd: norms %d and %d", norm_a,
+                 norm_y);
+    IONN_REQUIRE(sizes_ok(rows, cols), IONN_ERR_SHAPE, "ionn_residual_norm_fwd: rows = %lld, cols = %lld (at most %lld)",
+                 (long long)rows, (long long)cols, (long long)kMaxCols);
+    IONN_REQUIRE(eps >= 0.0 && eps <= 3.0e38 && alpha >= -3.0e38 && alpha <= 3.0e38, IONN_ERR_RANGE,
+                 "ionn_residual_norm_fwd: eps = %g, alpha = %g", eps, alpha);
+    IONN_REQUIRE(gate_rows >= 0 && gate_rows <= kMaxDim, IONN_ERR_RANGE, "ionn_residual_norm_fwd: gate_rows = %lld",
+                 (long long)gate_rows);
+    IONN_REQUIRE(norm_a != IONN_NORM_NONE || (!gamma_a && !beta_a && !mean_a && !rstd_a), IONN_ERR_ARG,
+                 "ionn_residual_norm_fwd: parameters or statistics of no norm of a");
+    IONN_REQUIRE(norm_y != IONN_NORM_NONE || (!n && !gamma_y && !beta_y && !mean_y && !rstd_y && !absmax_n), IONN_ERR_ARG,
+                 "ionn_residual_norm_fwd: parameters or results of no norm of y");
+    IONN_REQUIRE((norm_a == IONN_NORM_LAYER || (!beta_a && !mean_a)) && (norm_y == IONN_NORM_LAYER || (!beta_y && !mean_y)),
+                 IONN_ERR_ARG, "ionn_residual_norm_fwd: only a layer norm has a mean and a beta");
+    if (rows == 0 || cols == 0) return IONN_OK;
+    IONN_REQUIRE(a || (norm_a == IONN_NORM_NONE && !gate), IONN_ERR_ARG,
+                 "ionn_residual_norm_fwd: a norm or a gate of no block");
+    IONN_REQUIRE(x && (y || n), IONN_ERR_ARG, "ionn_residual_norm_fwd: NULL tensor");
+    IONN_REQUIRE(n || (!mean_y && !rstd_y && !absmax_n), IONN_ERR_ARG,
+                 "ionn_residual_norm_fwd: results of a norm of y that is not asked for");
+    const size_t es = dtype_size(dtype), bytes = size_t(rows) * cols * es;
+    IONN_REQUIRE(aligned(a, es) && aligned(x, es) && aligned(y, es) && aligned(n, es) && aligned(gamma_a, 4) &&
+                     aligned(beta_a, 4) && aligned(gate, 4) && aligned(gamma_y, 4) && aligned(beta_y, 4) &&
+                     aligned(mean_a, 4) && aligned(rstd_a, 4) && aligned(mean_y, 4) && aligned(rstd_y, 4) &&
+                     aligned(absmax_n, 4),
+                 IONN_ERR_ALIGN, "ionn_residual_norm_fwd: tensors must be aligned to their element size");
+    IONN_REQUIRE(apart(n, y, bytes) && same_or_apart(y, a, bytes) && same_or_apart(y, x, bytes) &&
+                     same_or_apart(n, a, bytes) && same_or_apart(n, x, bytes),
+                 IONN_ERR_ARG, "ionn_residual_norm_fwd: y and n may be a or x, but not overlap them or each other otherwise");
+    const int64_t share = gate && gate_rows > 0 && gate_rows < rows ? gate_rows : rows;
+    const Forward f{a, x, y, n, {norm_a, gamma_a, beta_a, mean_a, rstd_a}, {norm_y, gamma_y, beta_y, mean_y, rstd_y},
+                    gate, rows, uint32_t(share), int(cols), float(alpha), float(eps), absmax_n};
+    with_dtype(dtype, [&](auto tag) {
+        using T = decltype(tag);
+        constexpr int VE = 16 / sizeof(T);
+        with_shape<VE, false>(cols, [&](auto tpr, auto nv) {
+            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = fwd_threads(TPR);
+            // as many workgroups as are resident at once: rows are dealt out evenly
+            int64_t blocks = (rows + kBlock / TPR - 1) / (kBlock / TPR);
+            const int64_t most = int64_t(device_cus()) * (kBlock < 1024 ? 1024 / kBlock : 1);
+            if (blocks > most) blocks = most;
+            residual_norm_fwd_kernel<T, VE, TPR, NV><<<dim3(unsigned(blocks)), dim3(kBlock), 0, as_stream(stream)>>>(f);
+        });
+    });
+    return check_launch("ionn_residual_norm_fwd");
+}
+
+size_t ionn_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {
+    if (!sizes_ok(rows, cols) || gate_rows < 0 || gate_rows > kMaxDim || rows == 0 || cols == 0) return 0;
+    const int64_t share = gate_rows > 0 && gate_rows < rows ? gate_rows : rows;
+    const Runs r = runs_of(rows, cols, share);
+    return (size_t(r.whole() ? uint32_t(kMaxGroups) : r.units()) + kMaxGroups) * 2 * size_t(cols) * sizeof(float);
+}
+
+int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a, const void *y, int norm_a,
+                           const float *gamma_a, const float *beta_a, const float *gate, int64_t gate_rows, double alpha,
+                           int norm_y, const float *gamma_y, const float *mean_a, const float *rstd_a,
+                           const float *mean_y, const float *rstd_y, void *da, void *dx, float *dgamma_a, float *dbeta_a,
+                           float *dgate, float *dgamma_y, float *dbeta_y, int dtype, int64_t rows, int64_t cols,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    clear_error();
+    IONN_REQUIRE(dtype_ok(dtype), IONN_ERR_ARG, "ionn_residual_norm_bwd: dtype = %d", dtype);
+    IONN_REQUIRE(kind_ok(norm_a) && kind_ok(norm_y), IONN_ERR_ARG, "ionn_residual_norm_bwd: norms %d and %d", norm_a,
+                 norm_y);
+    IONN_REQUIRE(sizes_ok(rows, cols), IONN_ERR_SHAPE, "ionn_residual_norm_bwd: rows = %lld, cols = %lld (at most %lld)",
+                 (long long)rows, (long long)cols, (long long)kMaxCols);
+    IONN_REQUIRE(alpha >= -3.0e38 && alpha <= 3.0e38, IONN_ERR_RANGE, "ionn_residual_norm_bwd: alpha = %g", alpha);
+    IONN_REQUIRE(gate_rows >= 0 && gate_rows <= kMaxDim, IONN_ERR_RANGE, "ionn_residual_norm_bwd: gate_rows = %lld",
+                 (long long)gate_rows);
+    const bool sums_a = dgamma_a || dbeta_a || dgate, sums_y = dgamma_y || dbeta_y;
+    IONN_REQUIRE(norm_a != IONN_NORM_NONE || (!gamma_a && !beta_a && !mean_a && !rstd_a && !dgamma_a && !dbeta_a),
+                 IONN_ERR_ARG, "ionn_residual_norm_bwd: parameters or gradients of no norm of a");
+    IONN_REQUIRE(norm_y != IONN_NORM_NONE || (!dn && !gamma_y && !mean_y && !rstd_y && !sums_y), IONN_ERR_ARG,
+                 "ionn_residual_norm_bwd: parameters or gradients of no norm of y");
+    IONN_REQUIRE((norm_a == IONN_NORM_LAYER || (!beta_a && !mean_a && !dbeta_a)) &&
+                     (norm_y == IONN_NORM_LAYER || (!mean_y && !dbeta_y)),
+                 IONN_ERR_ARG, "ionn_residual_norm_bwd: only a layer norm has a mean and a beta");
+    IONN_REQUIRE(gate || !dgate, IONN_ERR_ARG, "ionn_residual_norm_bwd: dgate of no gate");
+    if (cols == 0) return IONN_OK;
+    const bool some = rows > 0;
+    IONN_REQUIRE(!some || ((dy || dn) && (da || dx || sums_a || sums_y)), IONN_ERR_ARG,
+                 "ionn_residual_norm_bwd: no error, or nothing to compute");
+    IONN_REQUIRE(!some || norm_y == IONN_NORM_NONE ||
+                     (dn && y && rstd_y && (mean_y || norm_y == IONN_NORM_RMS)),
+                 IONN_ERR_ARG, "ionn_residual_norm_bwd: the norm of y needs dn, y and its statistics");
+    IONN_REQUIRE(!some || (a ? norm_a == IONN_NORM_NONE || (rstd_a && (mean_a || norm_a == IONN_NORM_RMS))
+                             : !da && !sums_a && !gate && norm_a == IONN_NORM_NONE),
+                 IONN_ERR_ARG, "ionn_residual_norm_bwd: a's gradients need a and its statistics");
+    const size_t es = dtype_size(dtype), bytes = size_t(rows) * cols * es;
+    IONN_REQUIRE(aligned(dy, es) && aligned(dn, es) && aligned(a, es) && aligned(y, es) && aligned(da, es) &&
+                     aligned(dx, es) && aligned(gamma_a, 4) && aligned(beta_a, 4) && aligned(gate, 4) &&
+                     aligned(gamma_y, 4) && aligned(mean_a, 4) && aligned(rstd_a, 4) && aligned(mean_y, 4) &&
+                     aligned(rstd_y, 4) && aligned(dgamma_a, 4) && aligned(dbeta_a, 4) && aligned(dgate, 4) &&
+                     aligned(dgamma_y, 4) && aligned(dbeta_y, 4),
+                 IONN_ERR_ALIGN, "ionn_residual_norm_bwd: tensors must be aligned to their element size");
+    IONN_REQUIRE(!some || apart(da, dx, bytes), IONN_ERR_ARG, "ionn_residual_norm_bwd: da and dx overlap");
+    for (const void *in : {dy, dn, a, y})
+        IONN_REQUIRE(!some || (same_or_apart(da, in, bytes) && same_or_apart(dx, in, bytes)), IONN_ERR_ARG,
+                     "ionn_residual_norm_bwd: da and dx may be an input, but not overlap one in part");
+    const int64_t share = gate && gate_rows > 0 && gate_rows < rows ? gate_rows : rows;
+    const size_t need = ionn_residual_norm_bwd_workspace_bytes(rows, cols, share);
+    IONN_REQUIRE(!(sums_a || sums_y) || need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need),
+                 IONN_ERR_WORKSPACE, "ionn_residual_norm_bwd: needs a 16-byte aligned workspace of %zu bytes", need);
+    hipStream_t st = as_stream(stream);
+    const Runs runs = some ? runs_of(rows, cols, share) : Runs{0, 0, 0};
+    int64_t blocks = 0;
+    float *part_a = sums_a ? static_cast<float *>(workspace) : nullptr;
+    float *part_y = nullptr;
+    if (some) {
+        if (sums_y)
+            part_y = static_cast<float *>(workspace) + size_t(runs.whole() ? uint32_t(kMaxGroups) : runs.units()) * 2 * cols;
+        const Backward b{dy, dn, a, y, da, dx,
+                         {norm_a, gamma_a, beta_a, const_cast<float *>(mean_a), const_cast<float *>(rstd_a)},
+                         {norm_y, gamma_y, nullptr, const_cast<float *>(mean_y), const_cast<float *>(rstd_y)},
+                         gate, rows, uint32_t(share), runs.chunks, runs.chunk_rows, runs.units(), int(cols), float(alpha),
+                         part_a, part_y, dgate};
+        with_dtype(dtype, [&](auto tag) {
+            using T = decltype(tag);
+            constexpr int VE = 16 / sizeof(T);
+            with_shape<VE, true>(cols, [&](auto tpr, auto nv) {
+                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = bwd_threads(TPR);
+                const int64_t each = runs.whole() ? kBlock / TPR : 1;
+                blocks = (runs.units() + each - 1) / each;
+                if (blocks > kMaxGroups) blocks = kMaxGroups;
+                const dim3 grid{unsigned(blocks)}, block{unsigned(kBlock)};
+                if (runs.whole()) residual_norm_bwd_kernel<T, VE, TPR, NV, true><<<grid, block, 0, st>>>(b);
+                else residual_norm_bwd_kernel<T, VE, TPR, NV, false><<<grid, block, 0, st>>>(b);
+            });
+        });
+        if (int rc = check_launch("ionn_residual_norm_bwd")) return rc;
+    }
+    if (sums_a || sums_y) {  // (of no rows: zeros)
+        const Sums s{part_a, part_y, gate, gamma_a, beta_a, dgate, dgamma_a, dbeta_a, dgamma_y, dbeta_y,
+                     runs.groups, runs.chunks, uint32_t(blocks), int(cols), runs.whole(), sums_a, sums_y};
+        residual_norm_sum_kernel<<<dim3(unsigned((cols + 63) / 64), 2), dim3(64 * kSumGroups), 0, st>>>(s);
+        return check_launch("ionn_residual_norm_bwd");
+    }
+    return IONN_OK;
+}
+
+}  // extern "C"

@@ -750,6 +750,64 @@ def ionn_layer_norm_bwd(dy, x, mean, rstd, dx, gamma=None, dres=None, dgamma=Non
         check(rc, "ionn_layer_norm_bwd")
 
 
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+
+
+def _norm(kind):
+    """The library's number of a norm, given by number or name."""
+    return NORMS[kind] if isinstance(kind, str) else int(kind)
+
+
+def _gate_groups(gate, gate_rows, rows):
+    """Rows of the gate tensor."""
+    if gate is None:
+        return 0
+    return -(-rows // gate_rows) if 0 < gate_rows < rows else 1
+
+
+def ionn_residual_norm_fwd(a, x, y, n, norm_a="rms", gamma_a=None, beta_a=None, gate=None, gate_rows=0, alpha=1.0,
+                           norm_y="rms", gamma_y=None, beta_y=None, eps=1e-5, mean_a=None, rstd_a=None, mean_y=None,
+                           rstd_y=None, absmax_n=None, stream=None):
+    """a None (with norm_a "none"): the norm of alpha x alone; y or n None: not written."""
+    xs, dt = x.shape, x.dtype
+    rows, cols = xs
+    rc = lib().ionn_residual_norm_fwd(
+        _m(a, dt, xs, "a"), _m(x, dt, xs, "x"), _norm(norm_a), _v(gamma_a, f32, cols, "gamma_a"),
+        _v(beta_a, f32, cols, "beta_a"), _v(gate, f32, _gate_groups(gate, gate_rows, rows) * cols, "gate"), gate_rows,
+        alpha, _norm(norm_y), _v(gamma_y, f32, cols, "gamma_y"), _v(beta_y, f32, cols, "beta_y"), eps,
+        _m(y, dt, xs, "y"), _m(n, dt, xs, "n"), _v(mean_a, f32, rows, "mean_a"), _v(rstd_a, f32, rows, "rstd_a"),
+        _v(mean_y, f32, rows, "mean_y"), _v(rstd_y, f32, rows, "rstd_y"), _dtype(x, "x"), rows, cols,
+        _s(absmax_n, u32, "absmax_n"), _on(stream, x))
+    if rc:
+        check(rc, "ionn_residual_norm_fwd")
+
+
+def ionn_residual_norm_bwd_workspace_bytes(rows, cols, gate_rows=0):
+    return int(lib().ionn_residual_norm_bwd_workspace_bytes(int(rows), int(cols), int(gate_rows)))
+
+
+def ionn_residual_norm_bwd(dy, dn, a, y, da, dx, norm_a="rms", gamma_a=None, beta_a=None, gate=None, gate_rows=0,
+                           alpha=1.0, norm_y="rms", gamma_y=None, mean_a=None, rstd_a=None, mean_y=None, rstd_y=None,
+                           dgamma_a=None, dbeta_a=None, dgate=None, dgamma_y=None, dbeta_y=None, workspace=None,
+                           stream=None):
+    """dy or dn None: no such error; every output may be None."""
+    err = dy if dy is not None else dn
+    xs, dt = err.shape, err.dtype
+    rows, cols = xs
+    gates = _gate_groups(gate, gate_rows, rows) * cols
+    ws, nws = _space(workspace)
+    rc = lib().ionn_residual_norm_bwd(
+        _m(dy, dt, xs, "dy"), _m(dn, dt, xs, "dn"), _m(a, dt, xs, "a"), _m(y, dt, xs, "y"), _norm(norm_a),
+        _v(gamma_a, f32, cols, "gamma_a"), _v(beta_a, f32, cols, "beta_a"), _v(gate, f32, gates, "gate"), gate_rows,
+        alpha, _norm(norm_y), _v(gamma_y, f32, cols, "gamma_y"), _v(mean_a, f32, rows, "mean_a"),
+        _v(rstd_a, f32, rows, "rstd_a"), _v(mean_y, f32, rows, "mean_y"), _v(rstd_y, f32, rows, "rstd_y"),
+        _m(da, dt, xs, "da"), _m(dx, dt, xs, "dx"), _v(dgamma_a, f32, cols, "dgamma_a"),
+        _v(dbeta_a, f32, cols, "dbeta_a"), _v(dgate, f32, gates, "dgate"), _v(dgamma_y, f32, cols, "dgamma_y"),
+        _v(dbeta_y, f32, cols, "dbeta_y"), _dtype(err, "dy"), rows, cols, ws, nws, _on(stream, err))
+    if rc:
+        check(rc, "ionn_residual_norm_bwd")
+
+
 def _state_ptrs(ts, bits, name):
     """Pointers of optimiser states: float32, or one byte per element (uint8,
     int8 or float8_e4m3fn tensors of codes)."""

@@ -1,6 +1,6 @@
 """CPU oracle of the floating-point operations around the DFP-8 products:
-the Linear layer's epilogue and its backward pass, layer norm, AdamW and the
-DFP-8 and E4M3 conversions, each the definition written out in numpy.  Test
+the Linear layer's epilogue and its backward pass, the gated layer, layer norm,
+the norms around a block, AdamW and the DFP-8 and E4M3 conversions, each the definition written out in numpy.  Test
 infrastructure only.
 
 Everything is in float64 except AdamW, whose definition fixes the rounding of
@@ -114,6 +114,68 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma, dres):
     if dres is not None:
         dx = dx + np.asarray(dres, np.float64)
     return dx, (dy * h).sum(0), dy.sum(0)
+
+
+def _norm(v, kind, gamma, beta, eps):
+    """(output, mean, rstd, normalised rows); kind "none": the rows themselves."""
+    if kind == "none":
+        return v, None, None, v
+    mean = v.mean(1) if kind == "layer" else np.zeros(len(v))
+    rstd = 1.0 / np.sqrt(np.square(v - mean[:, None]).mean(1) + eps)
+    h = (v - mean[:, None]) * rstd[:, None]
+    out = h if gamma is None else h * gamma.astype(np.float64)
+    return out if beta is None else out + beta.astype(np.float64), mean, rstd, h
+
+
+def _per_row(gate, gate_rows, rows):
+    if gate is None:
+        return 1.0
+    return gate.astype(np.float64)[np.arange(rows) // (gate_rows if 0 < gate_rows < rows else max(rows, 1))]
+
+
+def residual_norm_fwd(a, x, norm_a, gamma_a, beta_a, gate, gate_rows, alpha, norm_y, gamma_y, beta_y, eps):
+    """{y, n, mean_a, rstd_a, mean_y, rstd_y} in float64."""
+    y = alpha * np.asarray(x, np.float64)
+    mean_a = rstd_a = None
+    if a is not None:
+        p, mean_a, rstd_a, _ = _norm(np.asarray(a, np.float64), norm_a, gamma_a, beta_a, eps)
+        y = y + _per_row(gate, gate_rows, len(y)) * p
+    n, mean_y, rstd_y, _ = _norm(y, norm_y, gamma_y, beta_y, eps)
+    return dict(y=y, n=n, mean_a=mean_a, rstd_a=rstd_a, mean_y=mean_y, rstd_y=rstd_y)
+
+
+def residual_norm_bwd(dy, dn, a, y, norm_a, gamma_a, beta_a, gate, gate_rows, alpha, norm_y, gamma_y, mean_a, rstd_a,
+                      mean_y, rstd_y):
+    """{dx, da, dgate, dgamma_a, dbeta_a, dgamma_y, dbeta_y} in float64, from the given statistics."""
+    wide = lambda v: None if v is None else np.asarray(v, np.float64)  # noqa: E731
+    one = lambda v: 1.0 if v is None else wide(v)  # noqa: E731
+
+    def rows(v, kind, mean, rstd):
+        return v if kind == "none" else (v - (0.0 if kind == "rms" else wide(mean)[:, None])) * wide(rstd)[:, None]
+
+    def back(d, h, kind, rstd):
+        if kind == "none":
+            return d
+        off = h * (d * h).mean(1, keepdims=True) + (d.mean(1, keepdims=True) if kind == "layer" else 0.0)
+        return wide(rstd)[:, None] * (d - off)
+
+    out = {}
+    t = 0.0 if dy is None else wide(dy)
+    if norm_y != "none":
+        hy = rows(wide(y), norm_y, mean_y, rstd_y)
+        t = t + back(wide(dn) * one(gamma_y), hy, norm_y, rstd_y)
+        out.update(dgamma_y=(wide(dn) * hy).sum(0), dbeta_y=wide(dn).sum(0))
+    out["dx"] = alpha * t
+    if a is not None:
+        ha = rows(wide(a), norm_a, mean_a, rstd_a)
+        e = t * _per_row(gate, gate_rows, len(t))
+        out["da"] = back(e * one(gamma_a), ha, norm_a, rstd_a)
+        out.update(dgamma_a=(e * ha).sum(0), dbeta_a=e.sum(0))
+        if gate is not None:
+            p = ha * one(gamma_a) + (0.0 if beta_a is None else wide(beta_a))
+            out["dgate"] = np.zeros(gate.shape)
+            np.add.at(out["dgate"], np.arange(len(t)) // (gate_rows if 0 < gate_rows < len(t) else max(len(t), 1)), t * p)
+    return out
 
 
 # ---- 8-bit optimiser states --------------------------------------------------
