@@ -958,6 +958,34 @@ int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
                             const float *lr_dev, const float *grad_scale,
                             uint32_t *absmax_P, void *stream);
 
+/* One Muon step of L matrices, in place:
+ *   g = G * grad_scale,  M = momentum * M + g
+ *   u = g + momentum * M (nesterov) or M
+ *   X = u / (|u| + eps), |u| the root of the sum of squares (in float64)
+ *   ns_steps times:  A = X X^T,  X = a X + (b A + c A A) X
+ *     (a, b, c = 3.4445, -4.7750, 2.0315; of a matrix of more rows than columns,
+ *     X^T in the place of X)
+ *   P = P * (1 - lr * weight_decay) - lr * scale[l] * X
+ * P, M: float32 [rows[l]][cols[l]]; G: the same of type g_dtype.  The products'
+ * operands are held as pairs of float16 terms (22 bits) and summed in float32, so
+ * X is right to about 1e-6 of its size.  A u of zeros leaves X = 0; one that is
+ * not finite everywhere makes the whole of P not a number.  scale (nullable, HOST
+ * [L]): sqrt(max(1, rows / cols)).  lr_dev (nullable, device float) gives lr when
+ * the kernels run; grad_scale (nullable, device float): 1.  absmax_P (nullable,
+ * device uint32 [L]): max-combined with the float32 bits of |P| after the step,
+ * for dfp8_from_float.  L >= 1; P, G, M, rows, cols are HOST arrays; rows, cols
+ * >= 1, their product of multiples of 256 at most 2^28; 0 <= momentum < 1; eps >=
+ * 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
+ * aligned, ionn_muon_workspace_bytes(L, rows, cols) bytes (0 on invalid sizes). */
+size_t ionn_muon_workspace_bytes(int L, const int64_t *rows, const int64_t *cols);
+int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype,
+                   float *const *M, const int64_t *rows, const int64_t *cols,
+                   double lr, double momentum, int nesterov, double eps,
+                   double weight_decay, int ns_steps, const double *scale,
+                   const float *lr_dev, const float *grad_scale,
+                   uint32_t *absmax_P, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,14 +22,6 @@ namespace dfp8 {
 constexpr int kRowWaves = 8;
 constexpr int kRowsMinK = 16;
 
-// LDS operations of a wavefront take effect in program order; this keeps the
-// compiler to it where lanes exchange values.
-__device__ __forceinline__ void in_order() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // K >= 16; RG groups of 16 rows, NG groups of 16 outputs.  GATED: N outputs of
 // W's 2 N rows; the first NG / 2 groups are gate rows, the others the up rows of
 // the same outputs.

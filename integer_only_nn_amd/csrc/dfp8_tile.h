@@ -44,6 +44,14 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 
 constexpr int BK = 128, NT = 256;
 
+// LDS operations of a wavefront take effect in program order; this keeps the
+// compiler to it where lanes exchange values.
+__device__ __forceinline__ void in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The epilogue of a product.  z = fl(s) 2^(ea + eb) (+ bias), y = act(z) (+
 // residual): outputs of type T at row pitch N (rows are contiguous).
 struct Epi {

@@ -1,0 +1,235 @@
+// Products of matrices held as pairs of float16 terms, for the orthogonalisation
+// of an update (muon.hip): float32-like precision on the float16 matrix cores
+// (gfx950, v_mfma_f32_32x32x16_f16).
+//
+// A value x is hi + lo, hi = fl16(x), lo = fl16(x - hi): 22 bits.  A product is
+// hi hi + hi lo + lo hi (lo lo is below float32's last bit), three matrix
+// instructions where the float32 ones take the time of eight.  32 values of a row
+// lie as 64 bytes of hi and 64 of lo, so that a 128-byte K step of the int8
+// kernels' loaders (gemm256.h, dfp8_tile128.h) brings both terms of both operands
+// and LDS hands out each fragment once for three products.
+//
+// Both operands are K-major, their rows padded with zeros to whole tiles, so no
+// edge is checked.  A product is `tiles` tiles of S double steps (64 values of K)
+// each; the workgroups take runs of `chunk` double steps of that sequence, across
+// tiles, and leave each piece's float32 sums in a slot of their own in the order
+// of the registers.  The pass that follows adds a tile's pieces in order
+// (muon.hip), so which workgroup took what decides the rounding and nothing else
+// does.
+#pragma once
+
+#include "dfp8_tile128.h"
+
+namespace ionn {
+namespace muon {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// C = A B^T by tiles, A [rows][K] and B [cols][K] pairs (4 K bytes a row).
+struct Work {
+    const int8_t *A, *B;
+    float *part;            // [groups][slots][side * side]
+    int rows, cols, K;      // rows, cols in tiles' sides, K in 64
+    int tri;                // the lower triangle of tiles alone (rows = cols)
+    int tiles, S, chunk, slots, groups;
+};
+
+// Tile t's row and column: the triangle row by row, else four rows of tiles at a
+// time (neighbours in t share operands in an XCD's L2).
+__host__ __device__ __forceinline__ void tile_at(const Work &w, int side, int t, int &ti, int &tj) {
+    if (w.tri) {
+        ti = int((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
+        while (ti * (ti + 1) / 2 > t) --ti;
+        while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+        tj = t - ti * (ti + 1) / 2;
+        return;
+    }
+    const int tm = w.rows / side, tn = w.cols / side, group = t / (4 * tn), first = 4 * group;
+    const int size = tm - first < 4 ? tm - first : 4, local = t - group * 4 * tn;
+    ti = first + local % size;
+    tj = local / size;
+}
+
+__device__ __forceinline__ v16f mfma(const v4i &b, const v4i &a, const v16f &c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, b), __builtin_bit_cast(v8h, a), c, 0, 0, 0);
+}
+
+// A wavefront's sums to its share of a slot, [i][j][q][lane] of four values.
+template <int F>
+__device__ __forceinline__ void leave(const v16f (&acc)[F][F], float *to, int lane) {
+    v4f *p = reinterpret_cast<v4f *>(to) + lane;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v16f &a = acc[i][j];
+                p[64 * ((i * F + j) * 4 + q)] = v4f{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            }
+}
+
+// ---- tiles of 128 ----------------------------------------------------------------
+
+// Steps [k0, k1) of tile (ti, tj).
+__device__ __forceinline__ void piece128(const Work &w, int ti, int tj, int k0, int k1, float *to, int8_t *lds) {
+    using namespace dfp8;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int wm = 64 * (wave >> 1), wn = 64 * (wave & 1), m0 = 128 * ti, n0 = 128 * tj, ld = 4 * w.K;
+    Src128<true> sa, sb;
+    sa.init(w.A, ld, uint32_t(w.rows) * uint32_t(ld), m0, m0 + 32 * wave, wave, lane);
+    sb.init(w.B, ld, uint32_t(w.cols) * uint32_t(ld), n0, n0 + 32 * wave, wave, lane);
+    const uint32_t base = g256::lds_addr(lds);
+    v16f acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
+    const auto load = [&](int kt, int stage) __attribute__((always_inline)) {
+        const uint32_t at = base + uint32_t(stage) * uint32_t(kStage128);
+        sa.template load<false>(kt, ld, at, wave);
+        sb.template load<false>(kt, ld, at + 128 * BK, wave);
+    };
+    load(k0, 0);
+    for (int kt = k0; kt < k1; ++kt) {
+        const int stage = (kt - k0) & 1;
+        wait_and_meet<0>();
+        if (kt + 1 < k1) load(kt + 1, stage ^ 1);
+        const int8_t *As = lds + stage * kStage128, *Bs = As + 128 * BK;
+        // slices 0 and 1: the high terms of 16 values each, 2 and 3: the low ones
+        v4i a[4][2], b[4][2];
+#pragma unroll
+        for (int sl = 0; sl < 4; ++sl)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[sl][i] = read_frag<128, true>(As, wm + 32 * i, sl, lane);
+                b[sl][i] = read_frag<128, true>(Bs, wn + 32 * i, sl, lane);
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = mfma(b[t == 1 ? 2 + h : h][j], a[t == 2 ? 2 + h : h][i], acc[i][j]);
+    }
+    leave<2>(acc, to + wave * 4096, lane);
+    wait_and_meet<0>();  // the next piece loads over the stages
+}
+
+// ---- tiles of 256 ----------------------------------------------------------------
+
+// The fragments of 16 values of K: both terms of a wavefront's four row blocks of each operand.
+struct Terms {
+    v4i a[2][4], b[2][4];  // [term]
+    __device__ __forceinline__ void read(int idx, const int8_t *As, const int8_t *Bs, const g256::FragSrc<true> &fa,
+                                         const g256::FragSrc<true> &fb, int sl) {
+        const int term = idx >> 3, i = idx & 3;
+        if (idx & 4) b[term][i] = fb.read(Bs, i, sl + 2 * term);
+        else a[term][i] = fa.read(As, i, sl + 2 * term);
+    }
+};
+
+// Product t (0 .. 47) of 16 values of K: hi hi, then hi lo, then lo hi, each over the 4 x 4 blocks.
+__device__ __forceinline__ void product(const Terms &f, int t, v16f (&acc)[4][4]) {
+    const int term = t >> 4, i = (t >> 2) & 3, j = t & 3;
+    acc[i][j] = mfma(f.b[term == 1][j], f.a[term == 2][i], acc[i][j]);
+}
+
+// Steps [k0, k1) of tile (ti, tj), an even number of them, on the operand layouts
+// and in the manner of gemm256.h: four wavefronts of 128 x 128, two LDS stages of
+// 64 KiB, a step's second half of fragments read while its first half multiplies,
+// and the next step's first half behind the barrier in the middle of the second.
+__device__ __forceinline__ void piece256(const Work &w, int ti, int tj, int k0, int k1, float *to, int8_t *sA0,
+                                         int8_t *sB0, int8_t *sA1, int8_t *sB1) {
+    using namespace g256;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int wm = wave >> 1, wn = wave & 1, ld = 4 * w.K;
+    TileSrc<true> ta, tb;
+    ta.init(w.A, ld, uint32_t(w.rows) * uint32_t(ld), 256 * ti, wave, lane);
+    tb.init(w.B, ld, uint32_t(w.cols) * uint32_t(ld), 256 * tj, wave, lane);
+    FragSrc<true> fa, fb;
+    fa.init(wm * 128, lane);
+    fb.init(wn * 128, lane);
+    v16f acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
+    Terms F[2];
+    // load pair q (0 .. 7) of step kt
+    const auto dma = [&](int q, int kt, int8_t *Ad, int8_t *Bd) __attribute__((always_inline)) {
+        if (q < 4) ta.issue_two(kt * g256::BK, Ad, wave, 2 * q);
+        else tb.issue_two(kt * g256::BK, Bd, wave, 2 * (q - 4));
+    };
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dma(q, k0, sA0, sB0);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    dma(0, k0 + 1, sA1, sB1);
+    dma(1, k0 + 1, sA1, sB1);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) F[0].read(r, sA0, sB0, fa, fb, 0);
+    const auto step = [&](const int8_t *Ac, const int8_t *Bc, int8_t *An, int8_t *Bn, int kt) __attribute__((always_inline)) {
+        const bool more1 = kt + 1 < k1, more2 = kt + 2 < k1;
+#pragma unroll
+        for (int t = 0; t < 48; ++t) {
+            product(F[0], t, acc);
+            IONN_SCHED_FENCE();
+            if (t % 3 == 0) F[1].read(t / 3, Ac, Bc, fa, fb, 1);
+            if (t % 4 == 1 && t / 4 < 6) {
+                if (more1) dma(2 + t / 4, kt + 1, An, Bn);
+            }
+            IONN_SCHED_FENCE();
+        }
+#pragma unroll
+        for (int t = 0; t < 30; ++t) product(F[1], t, acc);
+        IONN_SCHED_FENCE();
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        IONN_SCHED_FENCE();
+#pragma unroll
+        for (int t = 30; t < 48; ++t) {
+            product(F[1], t, acc);
+            IONN_SCHED_FENCE();
+            if (t - 30 < 16) F[0].read(t - 30, An, Bn, fa, fb, 0);
+            if (t == 36 || t == 42) {
+                if (more2) dma(t == 36 ? 0 : 1, kt + 2, const_cast<int8_t *>(Ac), const_cast<int8_t *>(Bc));
+            }
+            IONN_SCHED_FENCE();
+        }
+    };
+    for (int kt = k0; kt < k1; kt += 2) {
+        step(sA0, sB0, sA1, sB1, kt);
+        step(sA1, sB1, sA0, sB0, kt + 1);
+    }
+    leave<4>(acc, to + wave * 16384, lane);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();  // the next piece loads over the stages
+}
+
+// The pieces of workgroup g of a product: piece(tile row, tile column, first step, last step, slot).
+template <int SIDE, class F>
+__device__ __forceinline__ void pieces(const Work &w, int g, F &&piece) {
+    const int total = w.tiles * w.S;
+    int at = g * w.chunk, slot = 0;
+    const int end = min(total, at + w.chunk);
+    float *to = w.part + int64_t(g) * w.slots * (SIDE * SIDE);
+    while (at < end) {
+        const int t = at / w.S, from = at - t * w.S, upto = min(w.S, from + end - at);
+        int ti, tj;
+        tile_at(w, SIDE, t, ti, tj);
+        piece(ti, tj, 2 * from, 2 * upto, to + int64_t(slot) * (SIDE * SIDE));
+        at += upto - from;
+        ++slot;
+    }
+}
+
+}  // namespace muon
+}  // namespace ionn

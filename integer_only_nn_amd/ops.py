@@ -840,3 +840,34 @@ def ionn_adamw_step(Ps, Gs, Ms, Vs, t, lr, beta1=0.9, beta2=0.999, eps=1e-8, wei
         rc = lib().ionn_adamw_step_carried(*head, _ptr_array(Rs, i8, "R"), *tail)
     if rc:
         check(rc, "ionn_adamw_step" if Rs is None else "ionn_adamw_step_carried")
+
+
+def _shapes(ts):
+    """Rows and columns of matrices, as host arrays."""
+    return tuple((ctypes.c_int64 * len(ts))(*[int(t.shape[d]) for t in ts]) for d in (0, 1))
+
+
+def ionn_muon_workspace_bytes(shapes):
+    """shapes: (rows, columns) of each matrix."""
+    rows, cols = ((ctypes.c_int64 * len(shapes))(*[int(s[d]) for s in shapes]) for d in (0, 1))
+    return int(lib().ionn_muon_workspace_bytes(len(shapes), rows, cols))
+
+
+def ionn_muon_step(Ps, Gs, Ms, lr, workspace, momentum=0.95, nesterov=True, eps=1e-7, weight_decay=0.0, ns_steps=5,
+                   scale=None, lr_dev=None, grad_scale=None, absmax_P=None, stream=None):
+    """One step of every matrix (lists of 2-d device tensors); scale: a number
+    for each (None: sqrt(max(1, rows / columns)))."""
+    L = len(Ps)
+    _same(len(Gs) == L and len(Ms) == L and (scale is None or len(scale) == L), "lists of matrices")
+    _same(all(p.dim() == 2 and p.shape == g.shape == m.shape for p, g, m in zip(Ps, Gs, Ms)), "P, G and M of a matrix")
+    if L == 0:
+        return
+    rows, cols = _shapes(Ps)
+    ws, nws = _space(workspace)
+    rc = lib().ionn_muon_step(
+        L, _ptr_array(Ps, f32, "P"), _ptr_array(Gs, Gs[0].dtype, "G"), _dtype(Gs[0], "G"), _ptr_array(Ms, f32, "M"), rows,
+        cols, lr, momentum, int(nesterov), eps, weight_decay, int(ns_steps),
+        None if scale is None else (ctypes.c_double * L)(*[float(v) for v in scale]), _s(lr_dev, f32, "lr_dev"),
+        _s(grad_scale, f32, "grad_scale"), _v(absmax_P, u32, L, "absmax_P"), ws, nws, _on(stream, Ps[0]))
+    if rc:
+        check(rc, "ionn_muon_step")

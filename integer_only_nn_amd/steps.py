@@ -11,6 +11,7 @@ writes the output delta, then the backward pass per layer from the last:
 delta propagation with the pre-update weights (ReLU mask, requantised to
 target_bits = 7) and the weight gradient followed by the NITI update.
 """
+import ctypes
 from dataclasses import dataclass, field
 from typing import List, Optional
 
@@ -538,6 +539,75 @@ class AdamW:
         on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(on):
             self.step_dev.add_(by)
+
+
+# ---------------------------------------------------------------------------
+# Muon over a model's weight matrices (ionn_muon_step).
+# ---------------------------------------------------------------------------
+
+class Muon:
+    """The optimiser of a list of float32 weight matrices, updated in place: the
+    momentum, orthogonalised by Newton-Schulz products, takes the gradient's
+    place.  (Vectors, embeddings and a head's weights go to AdamW.)  Ms: the
+    momenta, float32.  scale: a factor of each matrix's step (None: sqrt(max(1,
+    rows / columns))).  The workspace and the ctypes arrays are made once
+    (bind_grads for the gradient buffers), so a step costs one library call.
+
+    With on_device the learning rate lives in a device scalar (self.lr_dev), so
+    that steps can be captured in a graph and replayed.  Steps that overlap (two
+    streams, two graphs) need an optimiser, and so a workspace, each."""
+
+    def __init__(self, Ps, Ms, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, eps=1e-7, ns_steps=5, scale=None,
+                 on_device=False):
+        self.P, self.M = list(Ps), list(Ms)
+        ops._same(len(self.M) == len(self.P) and all(p.dim() == 2 and m.shape == p.shape for p, m in zip(self.P, self.M)),
+                  "weight matrices and momenta")
+        ops._same(scale is None or len(scale) == len(self.P), "a scale for each matrix")
+        self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
+        self.eps, self.ns_steps = eps, ns_steps
+        self._G = self.lr_dev = self.ws = None
+        if not self.P:
+            return
+        L, dev = len(self.P), self.P[0].device
+        self._Pp = ops._ptr_array(self.P, torch.float32, "P")
+        self._Mp = ops._ptr_array(self.M, torch.float32, "M")
+        self._rows, self._cols = ops._shapes(self.P)
+        self._scale = None if scale is None else (ctypes.c_double * L)(*[float(v) for v in scale])
+        need = ops.ionn_muon_workspace_bytes([p.shape for p in self.P])
+        if need == 0:
+            raise ValueError("a matrix of no or of too many elements")
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if on_device:
+            self.lr_dev = torch.tensor([lr], dtype=torch.float32, device=dev)
+
+    @staticmethod
+    def make(Ps, **kw):
+        """Cleared momenta for these matrices."""
+        return Muon(Ps, [torch.zeros_like(p) for p in Ps], **kw)
+
+    def bind_grads(self, Gs):
+        """Fix the gradient buffers (device tensors of one floating type, one
+        per matrix) that step() reads when it is given none."""
+        if len(Gs) != len(self.P) or any(g.shape != p.shape for g, p in zip(Gs, self.P)):
+            raise ValueError("one gradient per weight matrix, of its shape")
+        if self.P:
+            self._G = (list(Gs), ops._ptr_array(Gs, Gs[0].dtype, "G"), ops._dtype(Gs[0], "G"))
+
+    def step(self, Gs=None, grad_scale=None, absmax_P=None, stream=None):
+        """One step with gradients Gs (None: the bound buffers)."""
+        if not self.P:
+            return
+        if Gs is not None:
+            self.bind_grads(Gs)
+        if self._G is None:
+            raise ValueError("no gradient buffers")
+        L = len(self.P)
+        ops.check(ops.lib().ionn_muon_step(
+            L, self._Pp, self._G[1], self._G[2], self._Mp, self._rows, self._cols, self.lr, self.momentum,
+            int(self.nesterov), self.eps, self.weight_decay, int(self.ns_steps), self._scale,
+            ops._s(self.lr_dev, torch.float32, "lr_dev"), ops._s(grad_scale, torch.float32, "grad_scale"),
+            ops._v(absmax_P, torch.int32, L, "absmax_P"), self.ws.data_ptr(), self.ws.nbytes, ops._on(stream, self.P[0])),
+            "ionn_muon_step")
 
 
 # ---------------------------------------------------------------------------

@@ -1,6 +1,6 @@
 """CPU oracle of the floating-point operations around the DFP-8 products:
 the Linear layer's epilogue and its backward pass, the gated layer, layer norm,
-the norms around a block, AdamW and the DFP-8 and E4M3 conversions, each the definition written out in numpy.  Test
+the norms around a block, Muon, AdamW and the DFP-8 and E4M3 conversions, each the definition written out in numpy.  Test
 infrastructure only.
 
 Everything is in float64 except AdamW, whose definition fixes the rounding of
@@ -176,6 +176,34 @@ def residual_norm_bwd(dy, dn, a, y, norm_a, gamma_a, beta_a, gate, gate_rows, al
             out["dgate"] = np.zeros(gate.shape)
             np.add.at(out["dgate"], np.arange(len(t)) // (gate_rows if 0 < gate_rows < len(t) else max(len(t), 1)), t * p)
     return out
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(x, steps, rounded=None):
+    """steps times x = a x + (b A + c A A) x, A = x x^T, the shorter side first.
+    rounded(product, terms): a model of a product's rounding, for tolerances."""
+    a, b, c = NEWTON_SCHULZ
+    rounded = rounded or (lambda p, q: p @ q)
+    tall = x.shape[0] > x.shape[1]
+    x = x.T if tall else x
+    for _ in range(steps):
+        A = rounded(x, x.T)
+        x = a * x + rounded(b * A + c * rounded(A, A), x)
+    return x.T if tall else x
+
+
+def muon_step(P, G, M, lr, momentum, nesterov, eps, weight_decay, steps, scale=None, rounded=None):
+    """(P, M, X) in float64."""
+    P, G, M = (np.asarray(t, np.float64) for t in (P, G, M))
+    M = momentum * M + G
+    u = G + momentum * M if nesterov else M
+    norm = np.sqrt(np.square(u).sum()) + eps
+    x = newton_schulz(u / norm if norm else u, steps, rounded)
+    if scale is None:
+        scale = math.sqrt(max(1.0, P.shape[0] / P.shape[1]))
+    return P * (1 - lr * weight_decay) - lr * scale * x, M, x
 
 
 # ---- 8-bit optimiser states --------------------------------------------------

@@ -1,0 +1,66 @@
+"""The Muon step's host-side checks (no GPU needed: none of these calls reaches
+one), and the oracle's orthogonalisation against singular values."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from integer_only_nn_amd import _lib, ops, steps
+from oracle import floats as of
+
+lib = _lib.lib()
+OK, ARG, SHAPE, RANGE, ALIGN, UNSUP, HIP, WS = range(8)
+P = ctypes.c_void_p
+NAN, INF = float("nan"), float("inf")
+
+
+def test_step():
+    arr = lambda v: (ctypes.c_void_p * 1)(v)  # noqa: E731
+    i64 = lambda v: (ctypes.c_int64 * 1)(v)  # noqa: E731
+    need = lib.ionn_muon_workspace_bytes(1, i64(8), i64(8))
+    assert need > 0
+
+    def f(L=1, p=arr(0x1000), g=arr(0x1000), dt=0, m=arr(0x1000), r=i64(8), c=i64(8), lr=0.1, mu=0.9, nes=1, eps=1e-7, wd=0.0,
+          k=5, sc=None, lrd=None, gs=None, top=None, ws=P(0x10000), wb=need):
+        return lib.ionn_muon_step(L, p, g, dt, m, r, c, lr, mu, nes, eps, wd, k, sc, lrd, gs, top, ws, wb, None)
+    assert f(L=0) == SHAPE and f(r=i64(0)) == SHAPE and f(c=i64(-1)) == SHAPE and f(r=i64(1 << 15), c=i64(1 << 14)) == SHAPE
+    assert f(dt=3) == ARG and f(p=None) == ARG and f(g=None) == ARG and f(m=None) == ARG and f(r=None) == ARG
+    assert f(p=arr(0)) == ARG and f(g=arr(0)) == ARG and f(m=arr(0)) == ARG
+    assert f(p=arr(0x1002)) == ALIGN and f(m=arr(0x1001)) == ALIGN and f(g=arr(0x1001), dt=1) == ALIGN
+    assert f(lrd=P(0x1001)) == ALIGN and f(gs=P(0x1002)) == ALIGN and f(top=P(0x1001)) == ALIGN
+    assert f(mu=1.0) == RANGE and f(mu=-0.1) == RANGE and f(mu=NAN) == RANGE and f(eps=-1.0) == RANGE and f(lr=INF) == RANGE
+    assert f(wd=NAN) == RANGE and f(k=0) == RANGE and f(k=33) == RANGE and f(sc=(ctypes.c_double * 1)(NAN)) == RANGE
+    assert f(ws=None) == WS and f(wb=need - 1) == WS and f(ws=P(0x10080)) == WS
+
+
+def test_workspace_of_a_list_is_that_of_its_largest_part():
+    one = ops.ionn_muon_workspace_bytes([(4096, 4096)])
+    assert one > 4096 * 4096 * 16
+    assert ops.ionn_muon_workspace_bytes([(4096, 4096)] * 5 + [(10, 10)]) == one
+    assert ops.ionn_muon_workspace_bytes([(4096, 4096), (0, 4)]) == 0
+
+
+def test_the_binding_refuses_before_the_library():
+    w = torch.zeros(4, 5)
+    with pytest.raises(ValueError):
+        steps.Muon([w], [torch.zeros(5, 4)])
+    with pytest.raises(ValueError):
+        steps.Muon([torch.zeros(4)], [torch.zeros(4)])
+    with pytest.raises(ValueError):
+        steps.Muon([w], [w], scale=[1.0, 2.0])
+    with pytest.raises(ValueError):
+        ops.ionn_muon_step([w], [torch.zeros(5, 4)], [w], 0.1, None)
+    steps.Muon([], []).step()  # nothing to do
+
+
+def test_oracle_orthogonalises():
+    """The matrix's singular vectors with the polynomial's values of its singular values."""
+    rng = np.random.default_rng(0)
+    for shape in ((5, 9), (9, 5), (6, 6), (1, 4)):
+        x = rng.standard_normal(shape)
+        x /= np.linalg.norm(x)
+        u, s, v = np.linalg.svd(x, full_matrices=False)
+        for _ in range(5):
+            s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+        np.testing.assert_allclose(of.newton_schulz(x, 5), (u * s) @ v, atol=1e-10)
