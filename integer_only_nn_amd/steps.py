@@ -699,3 +699,168 @@ class ResidualMlp:
         st = self.operand_status
         ops.dfp8_from_float(self.W1, self.W1_8, self.e[2:3], absmax=self.top[2:3], status_out=st[2:3], stream=stream)
         ops.dfp8_from_float(self.W2, self.W2_8, self.e[3:4], absmax=self.top[3:4], status_out=st[3:4], stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward blocks on a residual stream, on DFP-8 products.
+# ---------------------------------------------------------------------------
+
+class GatedMlps:
+    """L gated feed-forward blocks with norms before and after each, over a
+    batch of B rows: with n_0 = N_0(x), y_0 = x and for each block
+      (g | u) = W1 n + b1,  a = W2 (act(g) u) + b2,
+      y = alpha y + gate * N'(a),  n = N(y)
+    trained like ResidualMlp: integer products on DFP-8 copies of activations,
+    weights and errors, everything around them in floating point, FP32 master
+    weights.  The norm after a block, its gate, the residual and the norm before
+    the next block are one pass in each direction.
+
+    Matrices are updated by Muon (the gate's and the up projection's halves of W1
+    each as a matrix of its own) or, with matrices="adamw", by AdamW; vectors by
+    AdamW, without decay.  All buffers are allocated here, so a step only enqueues
+    kernels (and can be captured in a graph with on_device)."""
+
+    def __init__(self, blocks, gamma, B, norm="rms", beta=None, alpha=1.0, dtype=torch.bfloat16, act="silu", eps=1e-5,
+                 matrices="muon", state_bits=8, lr=0.02, lr_vectors=1e-3, momentum=0.95, betas=(0.9, 0.999),
+                 weight_decay=0.01, on_device=False):
+        """blocks: dicts of float32 device tensors, updated in place: W1 [2 H][D],
+        W2 [D][H] and, each optional, b1 [2 H], b2 [D], gamma and (norm "layer")
+        beta [D] of the norm after the block (no norm without gamma), gate [D].
+        gamma, beta: lists of the L + 1 gains and (norm "layer") shifts of the
+        norms before the blocks and behind the last."""
+        L, D = len(blocks), gamma[0].numel()
+        dev = gamma[0].device
+        new = lambda *shape, dt=dtype: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+        f32, i8, i32 = torch.float32, torch.int8, torch.int32
+        if norm not in ("layer", "rms"):
+            raise ValueError(f"norm = {norm} (layer or rms)")
+        if matrices not in ("muon", "adamw"):
+            raise ValueError(f"matrices = {matrices} (muon or adamw)")
+        ops._same(L >= 1 and len(gamma) == L + 1 and all(v.numel() == D for v in gamma), "the norms' gains")
+        ops._same(beta is None or (norm == "layer" and len(beta) == L + 1 and all(v.numel() == D for v in beta)),
+                  "the norms' shifts")
+        self.B, self.norm, self.alpha, self.act, self.eps = B, norm, alpha, act, eps
+        self.blocks, self.gamma = [dict(b) for b in blocks], list(gamma)
+        self.beta = [None] * (L + 1) if beta is None else list(beta)
+        layer = norm == "layer"
+        zero = lambda n: torch.zeros(n, dtype=i32, device=dev)  # noqa: E731
+        # per block: norm output, hidden activation, W1, W2, the two errors
+        self.e, self.status = zero(6 * L), zero(6 * L)
+        self.top = zero(2 * L)  # largest magnitudes: norm output, hidden activation (float32 bits)
+        self.bufs, vectors, vector_grads, mats, mat_grads = [], [], [], [], []
+        need = [ops.dfp8_from_float_workspace_bytes(), ops.ionn_residual_norm_bwd_workspace_bytes(B, D)]
+
+        def grad(of):
+            """A gradient buffer of a vector, given to its optimiser."""
+            if of is None:
+                return None
+            g = new(of.numel(), dt=f32)
+            vectors.append(of)
+            vector_grads.append(g)
+            return g
+
+        self.ggamma = [grad(v) for v in self.gamma]
+        self.gbeta = [grad(v) for v in self.beta]
+        for blk in self.blocks:
+            W1, W2 = blk["W1"], blk["W2"]
+            H = W2.shape[1]
+            for k, n in (("b1", 2 * H), ("b2", D), ("gamma", D), ("beta", D), ("gate", D)):
+                ops._same(blk.setdefault(k, None) is None or blk[k].numel() == n, f"{k} of a block")
+            ops._same(W1.shape == (2 * H, D) and W2.shape == (D, H), "a block's weights")
+            ops._same(blk["beta"] is None or (layer and blk["gamma"] is not None), "a shift of no layer norm")
+            post = norm if blk["gamma"] is not None else "none"
+            t = dict(H=H, post=post, W1_8=new(2 * H, D, dt=i8), W2_8=new(D, H, dt=i8), n=new(B, D), n8=new(B, D, dt=i8),
+                     z=new(B, 2 * H), h=new(B, H), h8=new(B, H, dt=i8), a=new(B, D), y=new(B, D),
+                     mean_n=new(B, dt=f32) if layer else None, rstd_n=new(B, dt=f32),
+                     mean_a=new(B, dt=f32) if post == "layer" else None, rstd_a=new(B, dt=f32) if post != "none" else None,
+                     da=new(B, D), da8=new(B, D, dt=i8), dh=new(B, H), dz8=new(B, 2 * H, dt=i8), dn=new(B, D), dy=new(B, D),
+                     gW1=new(2 * H, D), gW2=new(D, H), gb1=grad(blk["b1"]), gb2=grad(blk["b2"]),
+                     ggamma=grad(blk["gamma"]), gbeta=grad(blk["beta"]), ggate=grad(blk["gate"]))
+            self.bufs.append(t)
+            for W, g in ((W1[:H], t["gW1"][:H]), (W1[H:], t["gW1"][H:]), (W2, t["gW2"])) if matrices == "muon" else (
+                    (W1, t["gW1"]), (W2, t["gW2"])):
+                mats.append(W)
+                mat_grads.append(g)
+            need += [ops.dfp8_gated_fwd_workspace_bytes(B, D, H), ops.dfp8_gated_bwd_workspace_bytes(B, D, H),
+                     ops.dfp8_linear_fwd_workspace_bytes(B, H, D), ops.dfp8_linear_bwd_workspace_bytes(B, H, D)]
+        # behind the last norm
+        self.n, self.mean, self.rstd = new(B, D), new(B, dt=f32) if layer else None, new(B, dt=f32)
+        self.dx = new(B, D)
+        self.ws = new(max(need), dt=torch.uint8)
+        adam = dict(bits=state_bits, betas=betas, on_device=on_device, Rs=None)
+        if matrices == "muon":
+            self.opt = Muon.make(mats, lr=lr, momentum=momentum, weight_decay=weight_decay, on_device=on_device)
+        else:
+            self.opt = AdamW.make(mats, lr=lr, weight_decay=weight_decay, **adam)
+        self.opt.bind_grads(mat_grads)
+        self.opt_vectors = AdamW.make(vectors, lr=lr_vectors, weight_decay=0.0, **adam)
+        self.opt_vectors.bind_grads(vector_grads)
+        self._convert_weights(None)
+
+    def _scalars(self, l):
+        """Exponents and reports of block l: norm output, hidden activation, W1, W2, the two errors."""
+        return [[v[6 * l + i:6 * l + i + 1] for i in range(6)] for v in (self.e, self.status)]
+
+    def _convert_weights(self, stream):
+        for l, (blk, t) in enumerate(zip(self.blocks, self.bufs)):
+            e, st = self._scalars(l)
+            for i, k in ((2, "W1"), (3, "W2")):
+                ops.dfp8_from_float(blk[k], t[k + "_8"], e[i], workspace=self.ws, status_out=st[i], stream=stream)
+
+    def _norm_args(self, l):
+        """The norm behind block l - 1 (0: before the first): where it leaves its output and statistics."""
+        t = self.bufs[l] if l < len(self.bufs) else None
+        n, mean, rstd = (t["n"], t["mean_n"], t["rstd_n"]) if t else (self.n, self.mean, self.rstd)
+        return n, dict(norm_y=self.norm, gamma_y=self.gamma[l]), dict(mean_y=mean, rstd_y=rstd)
+
+    def forward(self, x, stream=None):
+        """The normed stream behind the last block, of a batch x [B][D]; the
+        stream itself is bufs[-1]["y"].  Keeps what backward() reads."""
+        kw, L = dict(stream=stream), len(self.blocks)
+        ops.ionn_fill_u32(self.top, 0, **kw)
+        top = lambda i: self.top[i:i + 1] if i < 2 * L else None  # noqa: E731
+        n, pre, stats = self._norm_args(0)
+        ops.ionn_residual_norm_fwd(None, x, None, n, norm_a="none", beta_y=self.beta[0], eps=self.eps, absmax_n=top(0), **pre,
+                                   **stats, **kw)
+        y = x
+        for l, (blk, t) in enumerate(zip(self.blocks, self.bufs)):
+            e, st = self._scalars(l)
+            ops.dfp8_from_float(t["n"], t["n8"], e[0], absmax=top(2 * l), status_out=st[0], **kw)
+            ops.dfp8_gated_fwd(t["n8"], e[0], t["W1_8"], e[2], t["h"], bias=blk["b1"], act=self.act, Z=t["z"],
+                               absmax_Y=top(2 * l + 1), workspace=self.ws, **kw)
+            ops.dfp8_from_float(t["h"], t["h8"], e[1], absmax=top(2 * l + 1), status_out=st[1], **kw)
+            ops.dfp8_linear_fwd(t["h8"], e[1], t["W2_8"], e[3], t["a"], bias=blk["b2"], workspace=self.ws, **kw)
+            n, pre, stats = self._norm_args(l + 1)
+            ops.ionn_residual_norm_fwd(t["a"], y, t["y"], n, norm_a=t["post"], gamma_a=blk["gamma"], beta_a=blk["beta"],
+                                       gate=blk["gate"], alpha=self.alpha, beta_y=self.beta[l + 1], eps=self.eps,
+                                       mean_a=t["mean_a"], rstd_a=t["rstd_a"], absmax_n=top(2 * l + 2), **pre, **stats, **kw)
+            y = t["y"]
+        return self.n
+
+    def backward(self, x, dn, dy=None, stream=None):
+        """dx, and every parameter's gradient, for the errors dn of the last
+        forward(x)'s output and dy (None: 0) of the stream behind it."""
+        kw = dict(workspace=self.ws, stream=stream)
+        for l in reversed(range(len(self.blocks))):
+            blk, t = self.blocks[l], self.bufs[l]
+            e, st = self._scalars(l)
+            _, pre, stats = self._norm_args(l + 1)
+            ops.ionn_residual_norm_bwd(dy, dn, t["a"], t["y"], t["da"], t["dy"], norm_a=t["post"], gamma_a=blk["gamma"],
+                                       beta_a=blk["beta"], gate=blk["gate"], alpha=self.alpha, mean_a=t["mean_a"],
+                                       rstd_a=t["rstd_a"], dgamma_a=t["ggamma"], dbeta_a=t["gbeta"], dgate=t["ggate"],
+                                       dgamma_y=self.ggamma[l + 1], dbeta_y=self.gbeta[l + 1], **pre, **stats, **kw)
+            ops.dfp8_linear_bwd(t["da"], None, "none", t["h8"], e[1], t["W2_8"], e[3], t["da8"], e[4], dX=t["dh"],
+                                G=t["gW2"], gb=t["gb2"], status_out=st[4], **kw)
+            ops.dfp8_gated_bwd(t["dh"], t["z"], self.act, t["n8"], e[0], t["W1_8"], e[2], t["dz8"], e[5], dX=t["dn"],
+                               G=t["gW1"], gb=t["gb1"], status_out=st[5], **kw)
+            dy, dn = t["dy"], t["dn"]
+        _, pre, stats = self._norm_args(0)
+        ops.ionn_residual_norm_bwd(dy, dn, None, x, None, self.dx, norm_a="none", dgamma_y=self.ggamma[0],
+                                   dbeta_y=self.gbeta[0], **pre, **stats, **kw)
+        return self.dx
+
+    def update(self, stream=None):
+        """The optimisers' steps on the last backward's gradients, and the new DFP-8 weights."""
+        self.opt.step(stream=stream)
+        self.opt_vectors.step(stream=stream)
+        self._convert_weights(stream)
