@@ -978,6 +978,10 @@ int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
  * 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
  * aligned, ionn_muon_workspace_bytes(L, rows, cols) bytes (0 on invalid sizes). */
 size_t ionn_muon_workspace_bytes(int L, const int64_t *rows, const int64_t *cols);
+/* The side of the tiles that matrix l is worked in, with those that share its
+ * launches: 32, 64, 128 or 256; -1: sizes out of range.  (Which one decides how
+ * sums are rounded and nothing else.) */
+int ionn_muon_tile(int L, const int64_t *rows, const int64_t *cols, int l);
 int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype,
                    float *const *M, const int64_t *rows, const int64_t *cols,
                    double lr, double momentum, int nesterov, double eps,

@@ -97,6 +97,7 @@ SIGNATURES = {
     "ionn_adamw_step_carried": (_I, [_I, _P, _P, _I, _P, _P, _P, _P, _P, _I64] + [ctypes.c_double] * 5 +
                                 [_P, _P, _P, _P, _P]),
     "ionn_muon_workspace_bytes": (ctypes.c_size_t, [_I, _P, _P]),
+    "ionn_muon_tile": (_I, [_I, _P, _P, _I]),
     "ionn_muon_step": (_I, [_I, _P, _P, _I, _P, _P, _P, ctypes.c_double, ctypes.c_double, _I, ctypes.c_double,
                             ctypes.c_double, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "ionn_model_backward": (_I, [_P, _I, _P, _I64, _P, _P, _P, _I, _I, _I, _P, ctypes.c_size_t, _P, _P]),

@@ -21,6 +21,7 @@
 // the end P.  Matrices of a batch share every launch.
 #include "muon_tile.h"
 
+#include <climits>
 #include <cmath>
 
 namespace ionn {
@@ -32,7 +33,7 @@ using muon::Work;
 
 constexpr int kTable = 8;  // matrices of a launch
 constexpr int kThreads = 256;
-constexpr int kSumBlocks = 256;  // workgroups of a matrix that take |u|
+constexpr int kSumBlocks = 1024;  // workgroups of a matrix that take |u|, at most
 constexpr float kScale = 4096.0f;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr int64_t kMaxElements = int64_t(1) << 28;  // of the padded matrix: its pairs stay below 2^30 bytes
@@ -41,6 +42,7 @@ struct Mat {
     float *P, *M;
     const void *G;
     int8_t *X, *XT, *A, *B;  // pairs: [mp][np], [np][mp], [mp][mp], [mp][mp]
+    int8_t *XTn;             // where the next X^T goes: XT itself unless the product that reads it writes it too
     double *sums;            // [blocks]
     float *part;
     int64_t count;
@@ -55,7 +57,7 @@ enum Product { XX = 0, AA = 1, BX = 2 };
 
 struct Table {
     Mat mat[kTable];
-    int first[kTable + 1];  // of a launch's workgroups or wavefronts
+    int first[kTable];  // of a launch's workgroups; INT_MAX past the last matrix
     int L;
 };
 
@@ -67,9 +69,11 @@ struct Hyper {
     uint32_t *absmax;
 };
 
+// (without a loop whose every turn would wait for its load)
 __device__ __forceinline__ int find(const Table &t, int id) {
     int l = 0;
-    while (l + 1 < t.L && id >= t.first[l + 1]) ++l;
+#pragma unroll
+    for (int i = 1; i < kTable; ++i) l += id >= t.first[i];
     return l;
 }
 
@@ -85,6 +89,7 @@ __global__ __launch_bounds__(kThreads) void momentum_kernel(Table t, Hyper h) {
     const T *G = static_cast<const T *>(a.G);
     const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
     double s = 0.0;
+#pragma unroll 4
     for (int64_t i = (int64_t(b) * kThreads + threadIdx.x) * 4; i < a.count; i += int64_t(a.blocks) * kThreads * 4) {
         const int valid = int(a.count - i < 4 ? a.count - i : 4);
         const auto g = load_raw<T, 4>(G + i, valid);
@@ -106,97 +111,103 @@ __global__ __launch_bounds__(kThreads) void momentum_kernel(Table t, Hyper h) {
     if (threadIdx.x == 0) a.sums[b] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// ---- blocks of 32 x 32 ---------------------------------------------------------
-// A lane holds row lane % 32, columns 8 q + 4 (lane / 32) .. + 3 in v[4 q ..], as
-// the matrix instructions leave them.
+// ---- tiles of 32 F x 32 F, 16 threads a row ----------------------------------------
+// A thread holds V = 2 F consecutive values of a row, so that a row's terms leave
+// in whole 128-byte lines.
 
-typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-
-// Where a lane's values of block (r0, c0) lie in a matrix of pairs with rows of K.
-__device__ __forceinline__ _Float16 *pair_at(int8_t *base, int K, int r0, int c0, int lane) {
-    return reinterpret_cast<_Float16 *>(base) + int64_t(r0 + (lane & 31)) * 2 * K + 2 * c0 + 4 * (lane >> 5);
-}
-
-__device__ __forceinline__ void store_pairs(int8_t *base, int K, int r0, int c0, int lane, const float (&v)[16]) {
-    _Float16 *p = pair_at(base, K, r0, c0, lane);
+// V consecutive values of a row of pairs.
+template <int V>
+struct Few {
+    typedef _Float16 type __attribute__((ext_vector_type(V)));
+    type hi, lo;
+    static __device__ __forceinline__ _Float16 *at(int8_t *base, int K, int r, int c) {
+        return reinterpret_cast<_Float16 *>(base) + int64_t(r) * 2 * K + 2 * (c & ~31) + (c & 31);
+    }
+    __device__ __forceinline__ void load(int8_t *base, int K, int r, int c) {
+        const _Float16 *p = at(base, K, r, c);
+        hi = *reinterpret_cast<const type *>(p);
+        lo = *reinterpret_cast<const type *>(p + 32);
+    }
+    static __device__ __forceinline__ void store(int8_t *base, int K, int r, int c, const float (&v)[V]) {
+        type hi, lo;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        v4h hi, lo;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = _Float16(v[4 * q + e]);
-            lo[e] = _Float16(v[4 * q + e] - float(hi[e]));
+        for (int e = 0; e < V; ++e) {
+            hi[e] = _Float16(v[e]);
+            lo[e] = _Float16(v[e] - float(hi[e]));
         }
-        *reinterpret_cast<v4h *>(p + 8 * q) = hi;
-        *reinterpret_cast<v4h *>(p + 8 * q + 32) = lo;
+        _Float16 *p = at(base, K, r, c);
+        *reinterpret_cast<type *>(p) = hi;
+        *reinterpret_cast<type *>(p + 32) = lo;
     }
+};
+
+// A tile's transpose in LDS: the pitch spreads a column over the banks.
+template <int F>
+constexpr int kTurnPitch = 32 * F + (F == 1 ? 2 : 1);
+template <int F>
+constexpr int kTurn = 32 * F * kTurnPitch<F>;
+
+template <int F>
+__device__ __forceinline__ void turn_in(float *turned, int row, int c, const float (&v)[2 * F]) {
+#pragma unroll
+    for (int e = 0; e < 2 * F; ++e) turned[(c + e) * kTurnPitch<F> + row] = v[e];
+}
+template <int F>
+__device__ __forceinline__ void turn_out(const float *turned, int row, int c, float (&v)[2 * F]) {
+#pragma unroll
+    for (int e = 0; e < 2 * F; ++e) v[e] = turned[row * kTurnPitch<F> + c + e];
 }
 
-__device__ __forceinline__ void load_pairs(int8_t *base, int K, int r0, int c0, int lane, float (&v)[16]) {
-    const _Float16 *p = pair_at(base, K, r0, c0, lane);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const v4h hi = *reinterpret_cast<const v4h *>(p + 8 * q), lo = *reinterpret_cast<const v4h *>(p + 8 * q + 32);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q + e] = float(hi[e]) + float(lo[e]);
-    }
-}
-
-// The block's transpose, through a wavefront's own LDS.
-__device__ __forceinline__ void transpose(float (&v)[16], float (*buf)[33], int lane) {
-    const int r = lane & 31, c = 4 * (lane >> 5);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) buf[r][8 * q + c + e] = v[4 * q + e];
-    dfp8::in_order();
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q + e] = buf[8 * q + c + e][r];
-    dfp8::in_order();
-}
-
-// X = u / (|u| + eps) and X^T as pairs, zeros in the padding: a wavefront a block
-// of u (of P's layout).
+// X = u / (|u| + eps) and X^T as pairs, zeros in the padding: a workgroup a tile
+// of 64 x 64 of u (of P's layout).
 template <class T>
 __global__ __launch_bounds__(kThreads) void scale_kernel(Table t, Hyper h) {
-    __shared__ float buf[kThreads / 64][32][33];
+    constexpr int F = 2, V = 2 * F, kRows = kThreads / 16, kPasses = 32 * F / kRows;
+    __shared__ float turned[kTurn<F>];
     __shared__ double red[kThreads / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l = find(t, int(blockIdx.x));
     const Mat &a = t.mat[l];
+    // rows and columns of P, and of its padded form
+    const int rows = a.tall ? a.n : a.m, cols = a.cols, rp = a.tall ? a.np : a.mp, cp = a.tall ? a.mp : a.np;
+    const int across = (cp + 63) / 64, b = int(blockIdx.x) - t.first[l];
+    const int r0 = 64 * (b / across), c0 = 64 * (b % across), r = int(threadIdx.x) / 16, c = V * (int(threadIdx.x) % 16);
+    const T *G = static_cast<const T *>(a.G);
+    const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
+    float v[kPasses][V];
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        const int row = r0 + kRows * k + r, valid = row < rows ? cols - c0 - c : 0;
+        const int64_t at = int64_t(row) * cols + c0 + c;
+        const auto m = load_raw<float, V>(a.M + at, valid);
+        const auto g = load_raw<T, V>(G + at, h.nesterov ? valid : 0);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = e < valid ? update_of(m[e], float(g[e]) * gs, h) : 0.0f;
+    }
     double s = 0.0;
     for (int i = threadIdx.x; i < a.blocks; i += kThreads) s += a.sums[i];
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-    if (lane == 0) red[wave] = s;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
     s = (red[0] + red[1]) + (red[2] + red[3]);
     const double norm = sqrt(s) + double(h.eps);
     const double factor = norm > 0.0 ? double(kScale) / norm : (norm == 0.0 ? 0.0 : norm);  // (NaN stays one)
-    // rows and columns of P, and of its padded form
-    const int rows = a.tall ? a.n : a.m, cols = a.cols, rp = a.tall ? a.np : a.mp, cp = a.tall ? a.mp : a.np;
-    const int across = cp / 32, b = (int(blockIdx.x) - t.first[l]) * (kThreads / 64) + wave;
-    const int r0 = 32 * (b / across), c0 = 32 * (b % across);
-    if (r0 >= rp) return;
-    const int r = r0 + (lane & 31);
-    const T *G = static_cast<const T *>(a.G);
-    const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
-    float v[16];
+    int8_t *to = a.tall ? a.XT : a.X, *to_turned = a.tall ? a.X : a.XT;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int c = c0 + 8 * q + 4 * (lane >> 5), valid = r < rows ? cols - c : 0;
-        const int64_t at = int64_t(r) * cols + c;
-        const auto m = load_raw<float, 4>(a.M + at, valid);
-        typename Vec<T, 4>::type g = load_raw<T, 4>(G + at, h.nesterov ? valid : 0);
+    for (int k = 0; k < kPasses; ++k) {
+        const int row = kRows * k + r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[4 * q + e] = e < valid ? float(double(update_of(m[e], float(g[e]) * gs, h)) * factor) : 0.0f;
+        for (int e = 0; e < V; ++e) v[k][e] = float(double(v[k][e]) * factor);
+        turn_in<F>(turned, row, c, v[k]);
+        if (r0 + row < rp && c0 + c < cp) Few<V>::store(to, cp, r0 + row, c0 + c, v[k]);
     }
-    store_pairs(a.tall ? a.XT : a.X, cp, r0, c0, lane, v);
-    transpose(v, buf[wave], lane);
-    store_pairs(a.tall ? a.X : a.XT, rp, c0, r0, lane, v);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        const int row = kRows * k + r;
+        turn_out<F>(turned, row, c, v[k]);
+        if (c0 + row < cp && r0 + c < rp) Few<V>::store(to_turned, rp, c0 + row, r0 + c, v[k]);
+    }
 }
 
 // ---- products ------------------------------------------------------------------
@@ -214,7 +225,7 @@ __host__ __device__ __forceinline__ Work work_of(const Mat &a, int product, int 
     w.tri = product != BX;
     const int tm = w.rows / SIDE, tn = w.cols / SIDE;
     w.tiles = w.tri ? tm * (tm + 1) / 2 : tm * tn;
-    w.S = w.K / 64;
+    w.S = w.K < 64 ? 1 : w.K / 64;
     w.chunk = chunk;
     w.slots = (chunk + w.S - 1) / w.S + 1;
     w.groups = int((int64_t(w.tiles) * w.S + chunk - 1) / chunk);
@@ -244,91 +255,177 @@ __global__ __launch_bounds__(g256::NT, 1) void product256_kernel(Mat a, int prod
     });
 }
 
-// What follows a product: a wavefront a block of 32 x 32.
+// V values of P's row r from column c on; returns their largest magnitude's bits.
+template <int V>
+__device__ __forceinline__ uint32_t update(const Mat &a, float keep, float rate, int r, int c, const float (&x)[V]) {
+    const int rows = a.tall ? a.n : a.m, valid = r < rows ? a.cols - c : 0;
+    if (valid <= 0) return 0u;
+    float *p = a.P + int64_t(r) * a.cols + c, o[V];
+    const auto old = load_raw<float, V>(p, valid);
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        o[e] = old[e] * keep - x[e] * rate;
+        if (e < valid) top = max(top, mag_bits(o[e]));
+    }
+    store_vec<float, V>(p, o, valid);
+    return top;
+}
+
+// What follows a product, by NT threads: tile (r0, c0) of its sums (NSUM of them,
+// in LDS as lay_small lays them) to the next operand (a symmetric one with the
+// tile's mirror image, unless it is on the diagonal) or to P.
+template <int F, int NT, int NSUM>
+struct Finish {
+    static constexpr int V = 2 * F, kRows = NT / 16, kPasses = 32 * F / kRows;
+    static_assert(32 * F % kRows == 0, "whole passes");
+    Few<V> own[kPasses];  // the block of A or X that goes into the polynomial, loaded ahead of the product
+
+    __device__ __forceinline__ void load(const Mat &a, int product, int r0, int c0) {
+        const int r = int(threadIdx.x) / 16, c = V * (int(threadIdx.x) % 16);
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            if (product == AA) own[k].load(a.A, a.mp, r0 + kRows * k + r, c0 + c);
+            if (product == BX) own[k].load(a.X, a.np, r0 + kRows * k + r, c0 + c);
+        }
+    }
+
+    __device__ __forceinline__ void run(const Mat &a, const Hyper &h, int l, int product, bool mirror, bool last, int r0,
+                                        int c0, const float *sums, float *turned) const {
+        const int r = int(threadIdx.x) / 16, c = V * (int(threadIdx.x) % 16);
+        const bool end = product == BX && last, turn = product == BX ? !end || a.tall : mirror;
+        int8_t *to = product == XX ? a.A : product == AA ? a.B : a.X, *to_turned = product == BX ? a.XTn : to;
+        const int K = product == BX ? a.np : a.mp;
+        const double lr = h.lr_dev ? double(*h.lr_dev) : h.lr;
+        const float keep = float(1.0 - lr * h.wd), rate = float(lr * double(a.scale) / double(kScale));
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            const int row = kRows * k + r;
+            float v[V];
+            const float *p = sums + row * muon::kSmallPitch<F> + c;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = p[e];
+#pragma unroll
+            for (int o = 1; o < NSUM; ++o)
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += p[o * muon::kSmallTile<F> + e];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float x = float(own[k].hi[e]) + float(own[k].lo[e]);
+                v[e] *= 1.0f / kScale;
+                if (product == AA) v[e] = fmaf(kC, v[e], kB * x);
+                if (product == BX) v[e] = fmaf(kA, x, v[e]);
+            }
+            if (turn) turn_in<F>(turned, row, c, v);
+            if (!end) Few<V>::store(to, K, r0 + row, c0 + c, v);
+            else if (!a.tall) top = max(top, update<V>(a, keep, rate, r0 + row, c0 + c, v));
+        }
+        if (turn) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+                const int row = kRows * k + r;
+                float v[V];
+                turn_out<F>(turned, row, c, v);
+                if (!end) Few<V>::store(to_turned, a.mp, c0 + row, r0 + c, v);
+                else top = max(top, update<V>(a, keep, rate, c0 + row, r0 + c, v));
+            }
+        }
+        if (end && h.absmax) {
+            top = wave_max_u32(top);
+            if ((threadIdx.x & 63) == 0) publish_max_u32(h.absmax + l, top);
+        }
+    }
+};
+
+// The pieces of a product in tiles of 128 or 256 added up and finished: a
+// workgroup 64 x 64 of a wavefront's share, a wavefront of it a block of 32 x 32.
 template <int SIDE>
 __global__ __launch_bounds__(kThreads) void finish_kernel(Table t, Hyper h, int product, int chunk, int last) {
-    constexpr int F = SIDE / 64, kBlocks = (SIDE / 32) * (SIDE / 32);  // of a wavefront's side; of a tile
-    __shared__ float buf[kThreads / 64][32][33];
+    constexpr int F = SIDE / 64, kGroups = SIDE * SIDE / 4096, kAcross = F / 2;  // blocks of a wavefront's side; groups
+    __shared__ float sums[muon::kSmallTile<2>];
+    __shared__ float turned[kTurn<2>];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l = find(t, int(blockIdx.x));
     const Mat &a = t.mat[l];
     const Work w = work_of<SIDE>(a, product, chunk);
-    const int id = (int(blockIdx.x) - t.first[l]) * (kThreads / 64) + wave;
-    const int tile = id / kBlocks, k = id % kBlocks;  // k: [wavefront][i][j] of the slot
-    uint32_t top = 0;
-    if (tile < w.tiles) {
-        int ti, tj;
-        muon::tile_at(w, SIDE, tile, ti, tj);
-        const int part = k / (F * F), i = k % (F * F) / F, j = k % F;
-        const int r0 = SIDE * ti + (SIDE / 2) * (part >> 1) + 32 * i, c0 = SIDE * tj + (SIDE / 2) * (part & 1) + 32 * j;
-        float v[16] = {};
-        const int first = tile * w.S / chunk, end = ((tile + 1) * w.S - 1) / chunk;
-        for (int g = first; g <= end; ++g) {
-            const int slot = tile - g * chunk / w.S;
-            const v4f *p = reinterpret_cast<const v4f *>(w.part + (int64_t(g) * w.slots + slot) * (SIDE * SIDE)) +
-                           (k * 4) * 64 + lane;
+    const int id = int(blockIdx.x) - t.first[l], tile = id / kGroups, k = id % kGroups;
+    const int part = k / (kAcross * kAcross), i = k % (kAcross * kAcross) / kAcross, j = k % kAcross;
+    int ti, tj;
+    muon::tile_at(w, SIDE, tile, ti, tj);
+    const int r0 = SIDE * ti + (SIDE / 2) * (part >> 1) + 64 * i, c0 = SIDE * tj + (SIDE / 2) * (part & 1) + 64 * j;
+    Finish<2, kThreads, 1> f;
+    f.load(a, product, r0, c0);
+    v4f v[4] = {};
+    const int block = (part * F + 2 * i + (wave >> 1)) * F + 2 * j + (wave & 1);
+    const int first = tile * w.S / chunk, end = ((tile + 1) * w.S - 1) / chunk;
+    for (int g = first; g <= end; ++g) {
+        const int slot = tile - g * chunk / w.S;
+        const v4f *p =
+            reinterpret_cast<const v4f *>(w.part + (int64_t(g) * w.slots + slot) * (SIDE * SIDE)) + block * 256 + lane;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const v4f s = p[64 * q];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * q + e] += s[e];
-            }
-        }
-        float x[16];
-        if (product == AA) load_pairs(a.A, a.mp, r0, c0, lane, x);
-        if (product == BX) load_pairs(a.X, a.np, r0, c0, lane, x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            v[e] *= 1.0f / kScale;
-            if (product == AA) v[e] = fmaf(kC, v[e], kB * x[e]);
-            if (product == BX) v[e] = fmaf(kA, x[e], v[e]);
-        }
-        if (product != BX) {
-            int8_t *to = product == XX ? a.A : a.B;
-            store_pairs(to, a.mp, r0, c0, lane, v);
-            if (ti != tj) {
-                transpose(v, buf[wave], lane);
-                store_pairs(to, a.mp, c0, r0, lane, v);
-            }
-        } else if (!last) {
-            store_pairs(a.X, a.np, r0, c0, lane, v);
-            transpose(v, buf[wave], lane);
-            store_pairs(a.XT, a.mp, c0, r0, lane, v);
-        } else {
-            if (a.tall) transpose(v, buf[wave], lane);
-            const int pr = (a.tall ? c0 : r0) + (lane & 31), pc = (a.tall ? r0 : c0) + 4 * (lane >> 5);
-            const int rows = a.tall ? a.n : a.m, cols = a.cols;
-            const double lr = h.lr_dev ? double(*h.lr_dev) : h.lr;
-            const float keep = float(1.0 - lr * h.wd), rate = float(lr * double(a.scale) / double(kScale));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = pc + 8 * q, valid = pr < rows ? cols - c : 0;
-                if (valid <= 0) continue;
-                float *p = a.P + int64_t(pr) * cols + c;
-                const auto old = load_raw<float, 4>(p, valid);
-                float o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[e] = old[e] * keep - v[4 * q + e] * rate;
-                    if (e < valid) top = max(top, mag_bits(o[e]));
-                }
-                store_vec<float, 4>(p, o, valid);
-            }
-        }
+        for (int q = 0; q < 4; ++q) v[q] += p[64 * q];
     }
-    if (last && h.absmax) {
-        top = wave_max_u32(top);
-        if (lane == 0) publish_max_u32(h.absmax + l, top);
+    float *to = sums + (32 * (wave >> 1) + (lane & 31)) * muon::kSmallPitch<2> + 32 * (wave & 1) + 4 * (lane >> 5);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<v4f *>(to + 8 * q) = v[q];
+    __syncthreads();
+    f.run(a, h, l, product, ti != tj, last, r0, c0, sums, turned);
+}
+
+// A product in small tiles, whole: tile 32 F a side, W wavefronts.
+template <int F, int W>
+__global__ __launch_bounds__(64 * W) void product_small_kernel(Table t, Hyper h, int product, int last) {
+    constexpr int TS = 32 * F;
+    static_assert((W * muon::kSmallTile<F> + kTurn<F>)*4 <= muon::kSmallLds<F, W>,
+                  "the sums and a transpose fit where the stages were");
+    __shared__ __attribute__((aligned(1024))) int8_t lds[muon::kSmallLds<F, W>];
+    const int l = find(t, int(blockIdx.x));
+    const Mat &a = t.mat[l];
+    const Work w = work_of<TS>(a, product, 1);
+    int ti, tj;
+    muon::tile_at(w, TS, int(blockIdx.x) - t.first[l], ti, tj);
+    Finish<F, 64 * W, W> f;
+    f.load(a, product, TS * ti, TS * tj);
+    float *sums = reinterpret_cast<float *>(lds);
+    {
+        v16f acc[F][F];
+        muon::sums_small<F, W>(w, ti, tj, lds, acc);
+        __syncthreads();  // every wavefront has read its stages
+        muon::lay_small<F>(acc, sums);
+        __syncthreads();
     }
+    f.run(a, h, l, product, ti != tj, last, TS * ti, TS * tj, sums, sums + W * muon::kSmallTile<F>);
 }
 
 // ---- host ------------------------------------------------------------------------
 
 int64_t up(int64_t a, int64_t to) { return (a + to - 1) / to * to; }
 
-// Whether a matrix is worked in tiles of 256, by itself, rather than in tiles of
-// 128 with others.
-bool large(int64_t m, int64_t n) { return up(m, 256) * up(n, 256) >= int64_t(64) * 256 * 256; }
+// The side of the tiles that a batch's matrices are worked in, by the sum of m^2 n
+// (a step's operations go with it) and the longest side; in us a step:
+//   32 (of a whole reduction each): 256 x 256 90 against 110 in tiles of 64 and 210
+//     in 128, 512 x 512 105 against 144; three of 512 x 512 (4.0e8) 165 and 143
+//   64 (the same): 1024 x 1024 190 against 308 in tiles of 128, 1536 x 1536 (3.6e9)
+//     509 and 529, four of 1000 x 1000 (4.0e9) 608 and 574
+//   128 (the reduction cut into runs): 2048 x 2048 (8.6e9) 811 against 876 in tiles
+//     of 256; with a long side also few operations, 128 x 32768 488 against 635
+//     in tiles of 32 (128 x 8192: 282 and 210)
+//   256, a matrix at a time: 2304 x 2304 (1.2e10) 1076 against 1320, 4096 x 4096
+//     3823 against 4866
+constexpr double kLarge = 1.15e10;
+double weight_of(const Mat &a) { return double(a.m) * a.m * a.n; }
+int side_of(const Mat *mats, int L) {
+    double sum = 0.0;
+    int longest = 0;
+    for (int l = 0; l < L; ++l) {
+        sum += weight_of(mats[l]);
+        if (mats[l].n > longest) longest = mats[l].n;
+    }
+    if (L == 1 && sum >= kLarge) return 256;
+    return longest > 8192 || sum > 3.7e9 ? 128 : sum > 3.0e8 ? 64 : 32;
+}
 
 // The run of double steps that each workgroup takes of a product, over all
 // matrices of a launch: one workgroup per compute unit and 256 x 256 tile, two and
@@ -346,7 +443,8 @@ struct Layout {
 
 // Lays the matrices of a batch out in one workspace (base may be NULL for the bytes alone).
 Layout lay_out(Mat *mats, int L, char *base) {
-    Layout y{large(mats[0].m, mats[0].n) ? 256 : 128, {}, 0};
+    Layout y{side_of(mats, L), {}, 0};
+    const bool whole = y.side < 128;  // products and what follows them in one launch
     const auto take = [&](size_t bytes) {
         char *p = base ? base + y.bytes : nullptr;
         y.bytes += size_t(up(int64_t(bytes), 1024));
@@ -359,10 +457,12 @@ Layout lay_out(Mat *mats, int L, char *base) {
         const size_t x = size_t(a.mp) * a.np * 4, s = size_t(a.mp) * a.mp * 4;
         a.X = reinterpret_cast<int8_t *>(take(x));
         a.XT = reinterpret_cast<int8_t *>(take(x));
+        a.XTn = whole ? reinterpret_cast<int8_t *>(take(x)) : a.XT;
         a.A = reinterpret_cast<int8_t *>(take(s));
         a.B = reinterpret_cast<int8_t *>(take(s));
         a.sums = reinterpret_cast<double *>(take(kSumBlocks * sizeof(double)));
     }
+    if (whole) return y;
     size_t most[kTable] = {};
     for (int p = 0; p < 3; ++p) {
         int64_t total = 0;
@@ -391,7 +491,7 @@ Mat mat_of(int64_t rows, int64_t cols) {
     a.n = int(a.tall ? rows : cols);
     a.cols = int(cols);
     a.count = rows * cols;
-    const int64_t b = (a.count + kThreads * 16 - 1) / (kThreads * 16);
+    const int64_t b = (a.count + kThreads * 4 - 1) / (kThreads * 4);
     a.blocks = int(b < kSumBlocks ? b : kSumBlocks);
     return a;
 }
@@ -401,14 +501,29 @@ bool size_ok(int64_t rows, int64_t cols) {
            up(rows, 256) * up(cols, 256) <= kMaxElements;
 }
 
-// Matrices from l on that share their launches.
-int batch_of(int L, const int64_t *rows, const int64_t *cols, int l) {
-    const auto m = [&](int i) { return rows[i] < cols[i] ? rows[i] : cols[i]; };
-    const auto n = [&](int i) { return rows[i] < cols[i] ? cols[i] : rows[i]; };
-    if (large(m(l), n(l))) return 1;
-    int k = 1;
-    while (k < kTable && l + k < L && !large(m(l + k), n(l + k))) ++k;
+// Takes the matrices from l on that share their launches; returns their number.
+int take_batch(int L, const int64_t *rows, const int64_t *cols, int l, Mat *mats) {
+    int k = 0;
+    for (; k < kTable && l + k < L; ++k) {
+        mats[k] = mat_of(rows[l + k], cols[l + k]);
+        if (weight_of(mats[k]) >= kLarge) return k ? k : 1;
+    }
     return k;
+}
+
+template <int F, int W>
+void launch_small(Table &t, const Hyper &h, int p, bool last, hipStream_t st) {
+    int groups = 0;
+    for (int l = 0; l < t.L; ++l) {
+        t.first[l] = groups;
+        groups += work_of<32 * F>(t.mat[l], p, 1).tiles;
+    }
+    product_small_kernel<F, W><<<dim3(unsigned(groups)), dim3(64 * W), 0, st>>>(t, h, p, last);
+    for (int l = 0; p == BX && l < t.L; ++l) {
+        int8_t *xt = t.mat[l].XT;
+        t.mat[l].XT = t.mat[l].XTn;
+        t.mat[l].XTn = xt;
+    }
 }
 
 template <int SIDE>
@@ -418,16 +533,14 @@ void launch_product(Table &t, const Hyper &h, const Layout &y, int p, bool last,
         t.first[l] = groups;
         groups += work_of<SIDE>(t.mat[l], p, y.chunk[p]).groups;
     }
-    t.first[t.L] = groups;
     if (SIDE == 256) product256_kernel<<<dim3(unsigned(groups)), dim3(g256::NT), 0, st>>>(t.mat[0], p, y.chunk[p]);
     else product128_kernel<<<dim3(unsigned(groups)), dim3(kThreads), 0, st>>>(t, p, y.chunk[p]);
-    constexpr int kBlocks = (SIDE / 32) * (SIDE / 32) / (kThreads / 64);  // workgroups of a tile
+    constexpr int kGroups = SIDE * SIDE / 4096;  // workgroups of a tile
     groups = 0;
     for (int l = 0; l < t.L; ++l) {
         t.first[l] = groups;
-        groups += work_of<SIDE>(t.mat[l], p, y.chunk[p]).tiles * kBlocks;
+        groups += work_of<SIDE>(t.mat[l], p, y.chunk[p]).tiles * kGroups;
     }
-    t.first[t.L] = groups;
     finish_kernel<SIDE><<<dim3(unsigned(groups)), dim3(kThreads), 0, st>>>(t, h, p, y.chunk[p], last);
 }
 
@@ -444,14 +557,23 @@ size_t ionn_muon_workspace_bytes(int L, const int64_t *rows, const int64_t *cols
         if (!size_ok(rows[l], cols[l])) return 0;
     size_t most = 0;
     for (int l = 0; l < L;) {
-        const int k = batch_of(L, rows, cols, l);
         Mat mats[kTable];
-        for (int i = 0; i < k; ++i) mats[i] = mat_of(rows[l + i], cols[l + i]);
+        const int k = take_batch(L, rows, cols, l, mats);
         const Layout y = lay_out(mats, k, nullptr);
         most = y.bytes > most ? y.bytes : most;
         l += k;
     }
     return most;
+}
+
+int ionn_muon_tile(int L, const int64_t *rows, const int64_t *cols, int l) {
+    if (L < 1 || l < 0 || l >= L || ionn_muon_workspace_bytes(L, rows, cols) == 0) return -1;
+    for (int first = 0;;) {
+        Mat mats[kTable];
+        const int k = take_batch(L, rows, cols, first, mats);
+        if (l < first + k) return side_of(mats, k);
+        first += k;
+    }
 }
 
 int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype, float *const *M, const int64_t *rows,
@@ -484,10 +606,10 @@ int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype, fl
     hipStream_t st = as_stream(stream);
     for (int l = 0; l < L;) {
         Table t{};
-        t.L = batch_of(L, rows, cols, l);
+        t.L = take_batch(L, rows, cols, l, t.mat);
+        for (int i = t.L; i < kTable; ++i) t.first[i] = INT_MAX;
         for (int i = 0; i < t.L; ++i) {
             Mat &a = t.mat[i];
-            a = mat_of(rows[l + i], cols[l + i]);
             a.P = P[l + i];
             a.M = M[l + i];
             a.G = G[l + i];
@@ -502,23 +624,23 @@ int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype, fl
             t.first[i] = blocks;
             blocks += t.mat[i].blocks;
         }
-        t.first[t.L] = blocks;
         with_dtype(g_dtype, [&](auto tag) {
             momentum_kernel<decltype(tag)><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(t, h);
         });
         blocks = 0;
         for (int i = 0; i < t.L; ++i) {
             t.first[i] = blocks;
-            blocks += (t.mat[i].mp / 32) * (t.mat[i].np / 32) / (kThreads / 64);
+            blocks += ((t.mat[i].mp + 63) / 64) * ((t.mat[i].np + 63) / 64);
         }
-        t.first[t.L] = blocks;
         with_dtype(g_dtype, [&](auto tag) {
             scale_kernel<decltype(tag)><<<dim3(unsigned(blocks)), dim3(kThreads), 0, st>>>(t, h);
         });
         for (int k = 0; k < ns_steps; ++k)
             for (int p = 0; p < 3; ++p) {
                 const bool last = p == BX && k + 1 == ns_steps;
-                if (y.side == 256) launch_product<256>(t, h, y, p, last, st);
+                if (y.side == 32) launch_small<1, 8>(t, h, p, last, st);
+                else if (y.side == 64) launch_small<2, 4>(t, h, p, last, st);
+                else if (y.side == 256) launch_product<256>(t, h, y, p, last, st);
                 else launch_product<128>(t, h, y, p, last, st);
             }
         if (int rc = check_launch("ionn_muon_step")) return rc;

@@ -122,6 +122,109 @@ __device__ __forceinline__ void piece128(const Work &w, int ti, int tj, int k0, 
     wait_and_meet<0>();  // the next piece loads over the stages
 }
 
+// ---- small tiles -------------------------------------------------------------------
+
+// A tile of 32 F x 32 F by a workgroup of W wavefronts that split the reduction:
+// each loads its own 32 values of K at a time, straight into LDS that no other
+// wavefront uses (two stages, no barrier), and their sums meet in LDS.  For
+// matrices of which tiles of 128 would be few: a product is then about one trip to
+// memory, and its epilogue is in the same launch.  (Through registers, four steps
+// in flight, 512 x 512 took 106 us a step against 101.)
+template <int F, int W>
+constexpr int kSmallLds = W * 2 * 2 * 32 * F * 128;
+
+// The sums of a wavefront's share of K, of tile (ti, tj).
+template <int F, int W>
+__device__ __forceinline__ void sums_small(const Work &w, int ti, int tj, int8_t *lds, v16f (&acc)[F][F]) {
+    using namespace dfp8;
+    constexpr int kOperand = 32 * F * 128, kStage = 2 * kOperand;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int ld = 4 * w.K, steps = w.K / 32, per = (steps + W - 1) / W, k0 = wave * per, k1 = min(steps, k0 + per);
+    const auto rsrc = [&](const int8_t *b, int rows) __attribute__((always_inline)) {
+        const uint64_t a = uint64_t(uintptr_t(b));
+        return v4i{__builtin_amdgcn_readfirstlane(int(uint32_t(a))),
+                   __builtin_amdgcn_readfirstlane(int(uint32_t(a >> 32) & 0xffffu)),
+                   __builtin_amdgcn_readfirstlane(int(uint32_t(rows) * uint32_t(ld))), 0x00020000};
+    };
+    const v4i ra = rsrc(w.A, w.rows), rb = rsrc(w.B, w.cols);
+    // an instruction takes eight rows of 128 bytes; piece c of row r lies at c ^ fK(r & 15)
+    const int sub = lane >> 3, at = lane & 7;
+    uint32_t off[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) off[p] = uint32_t(sub) * uint32_t(ld) + 16u * uint32_t(at ^ g256::fK(8 * p + sub));
+    const uint32_t base = g256::lds_addr(lds) + uint32_t(wave) * uint32_t(2 * kStage);
+    const auto load = [&](int k) __attribute__((always_inline)) {
+        const uint32_t to = base + uint32_t((k - k0) & 1) * uint32_t(kStage), kb = 128u * uint32_t(k);
+#pragma unroll
+        for (int q = 0; q < 4 * F; ++q)
+            g256::dma16(ra, off[q & 1] + uint32_t(32 * F * ti + 8 * q) * uint32_t(ld) + kb, 0u, to + 1024u * uint32_t(q));
+#pragma unroll
+        for (int q = 0; q < 4 * F; ++q)
+            g256::dma16(rb, off[q & 1] + uint32_t(32 * F * tj + 8 * q) * uint32_t(ld) + kb, 0u,
+                        to + uint32_t(kOperand) + 1024u * uint32_t(q));
+    };
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = v16f{};
+    if (k0 < k1) load(k0);
+    for (int k = k0; k < k1; ++k) {
+        // the stage that the next step goes to has been read (lgkmcnt(0)); then this step's loads are in
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        if (k + 1 < k1) {
+            load(k + 1);
+            __builtin_amdgcn_s_waitcnt(((8 * F) & 15) | (7 << 4) | (15 << 8) | (((8 * F) >> 4) << 14));  // vmcnt(8 F)
+        } else {
+            __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0)
+        }
+        asm volatile("" ::: "memory");
+        const int8_t *As = lds + wave * (2 * kStage) + ((k - k0) & 1) * kStage, *Bs = As + kOperand;
+        v4i a[4][F], b[4][F];
+#pragma unroll
+        for (int sl = 0; sl < 4; ++sl)
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                a[sl][i] = read_frag<32 * F, true>(As, 32 * i, sl, lane);
+                b[sl][i] = read_frag<32 * F, true>(Bs, 32 * i, sl, lane);
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+#pragma unroll
+                    for (int j = 0; j < F; ++j)
+                        acc[i][j] = mfma(b[t == 1 ? 2 + h : h][j], a[t == 2 ? 2 + h : h][i], acc[i][j]);
+    }
+}
+
+// The tile's sums of all wavefronts: rows of 32 F + 4 floats in LDS, one tile for
+// each wavefront, so that a thread adds up neighbouring values of a row.  (The pad
+// spreads the rows of a column over the banks.)
+template <int F>
+constexpr int kSmallPitch = 32 * F + 4;
+template <int F>
+constexpr int kSmallTile = 32 * F * kSmallPitch<F>;
+
+template <int F>
+__device__ __forceinline__ void lay_small(const v16f (&acc)[F][F], float *lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float *to = lds + wave * kSmallTile<F> + (lane & 31) * kSmallPitch<F> + 4 * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v16f &a = acc[i][j];
+                *reinterpret_cast<v4f *>(to + 32 * i * kSmallPitch<F> + 32 * j + 8 * q) =
+                    v4f{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            }
+}
+
 // ---- tiles of 256 ----------------------------------------------------------------
 
 // The fragments of 16 values of K: both terms of a wavefront's four row blocks of each operand.

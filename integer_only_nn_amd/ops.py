@@ -853,6 +853,15 @@ def ionn_muon_workspace_bytes(shapes):
     return int(lib().ionn_muon_workspace_bytes(len(shapes), rows, cols))
 
 
+def ionn_muon_tile(shapes, l=0):
+    """Side of the tiles that matrix l of these shapes is worked in."""
+    rows, cols = ((ctypes.c_int64 * len(shapes))(*[int(s[d]) for s in shapes]) for d in (0, 1))
+    side = lib().ionn_muon_tile(len(shapes), rows, cols, int(l))
+    if side < 0:
+        raise ValueError(f"shapes = {shapes}, l = {l}")
+    return side
+
+
 def ionn_muon_step(Ps, Gs, Ms, lr, workspace, momentum=0.95, nesterov=True, eps=1e-7, weight_decay=0.0, ns_steps=5,
                    scale=None, lr_dev=None, grad_scale=None, absmax_P=None, stream=None):
     """One step of every matrix (lists of 2-d device tensors); scale: a number

@@ -70,7 +70,11 @@ def _step(ds, name, absmax=True, lr=0.5, weight_decay=0.1, **kw):
 
 SHAPES = [(1, 1), (1, 5), (7, 1), (3, 3), (33, 2), (10, 128), (64, 64), (128, 256), (100, 30), (129, 127), (256, 784),
           (784, 256), (300, 513), (128, 3000), (700, 1000)]
-LARGE = [(2048, 2048), (2000, 2100), (2100, 1990), (1024, 4096), (1030, 4500), (4100, 1300)]
+LARGE = [(2048, 2048), (2000, 2100), (2100, 1990), (1024, 4096), (1030, 4500), (4100, 1300), (2304, 2304), (2250, 2500),
+         (2500, 2300), (1300, 8000), (20000, 40), (1100, 1000)]
+# tiles by sizes, as the CPU test holds them to
+TILES = {32: [(1, 1), (256, 784), (512, 512), (30, 8192)], 64: [(700, 1000), (1100, 1000)],
+         128: [(2048, 2048), (2100, 1990), (1024, 4096), (20000, 40)], 256: [(2304, 2304), (2500, 2300), (1300, 8000)]}
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -89,6 +93,13 @@ def test_step_of_a_large_matrix(rows, cols):
     _check(P[0], M[0], d, "bf16")
 
 
+@pytest.mark.parametrize("rows,cols", [(30, 8192), (512, 512)])
+def test_step_of_a_long_reduction(rows, cols):
+    d = _case(rows, cols)
+    P, M = _step([d], "f16")
+    _check(P[0], M[0], d, "f16")
+
+
 @pytest.mark.parametrize("rows,cols", [(64, 64), (200, 300), (400, 100), (2048, 2048)])
 def test_step_of_few_strong_directions(rows, cols):
     d = _case(rows, cols, "strong")
@@ -99,7 +110,7 @@ def test_step_of_few_strong_directions(rows, cols):
 def test_many_matrices_at_once():
     """More than a launch takes, small and large ones in any order, each as it is by itself."""
     shapes = [(10, 128), (300, 200), (2048, 2050), (1, 9), (128, 256), (5, 5), (256, 784), (64, 1), (90, 90), (33, 70), (70, 33),
-              (2, 2)]
+              (2, 2), (2400, 2300), (3, 4), (600, 800), (900, 700)]
     ds = [_case(*s, seed=i) for i, s in enumerate(shapes)]
     P, M = _step(ds, "bf16")
     for p, m, d in zip(P, M, ds):
@@ -131,7 +142,7 @@ def test_updates_of_any_size():
 
 def test_what_is_not_finite_stays_in_its_matrix():
     for bad in (np.nan, np.inf):
-        for shape in ((40, 50), (2048, 2048)):
+        for shape in ((40, 50), (2048, 2048), (2304, 2304)):
             ds = [_case(20, 30), _case(*shape), _case(30, 20)]
             ds[1]["G"][3, 4] = bad
             P, M = _step(ds, "f32", absmax=False)
@@ -178,7 +189,7 @@ def test_orthogonal_after_many_steps_of_the_polynomial():
 
 
 def test_optimiser_over_several_steps_and_on_another_stream():
-    ds = [_case(40, 70), _case(2048, 2048), _case(90, 33)]
+    ds = [_case(40, 70), _case(2304, 2304), _case(90, 33)]
     Ps, Ms = [d["P"].astype(np.float64) for d in ds], [0 * d["M"].astype(np.float64) for d in ds]
     P = [to_dev(d["P"]) for d in ds]
     opt = steps.Muon.make(P, lr=0.01, weight_decay=0.1)
@@ -199,7 +210,7 @@ def test_optimiser_over_several_steps_and_on_another_stream():
 
 
 def test_repeatable_and_captured():
-    ds = [_case(40, 70), _case(300, 200), _case(2050, 2048)]
+    ds = [_case(40, 70), _case(300, 200), _case(2350, 2304), _case(900, 1000), _case(33, 10)]
     a, b = _step(ds, "bf16"), _step(ds, "bf16")
     assert all(torch.equal(p, q) for p, q in zip(a[0] + a[1], b[0] + b[1]))
     P, Q = ([to_dev(d["P"]) for d in ds] for _ in range(2))

@@ -8,6 +8,7 @@ import torch
 
 from integer_only_nn_amd import _lib, ops, steps
 from oracle import floats as of
+from test_gpu_muon import TILES
 
 lib = _lib.lib()
 OK, ARG, SHAPE, RANGE, ALIGN, UNSUP, HIP, WS = range(8)
@@ -39,6 +40,20 @@ def test_workspace_of_a_list_is_that_of_its_largest_part():
     assert one > 4096 * 4096 * 16
     assert ops.ionn_muon_workspace_bytes([(4096, 4096)] * 5 + [(10, 10)]) == one
     assert ops.ionn_muon_workspace_bytes([(4096, 4096), (0, 4)]) == 0
+
+
+@pytest.mark.parametrize("side", list(TILES))
+def test_sizes_take_their_tiles(side):
+    for shape in TILES[side]:
+        assert ops.ionn_muon_tile([shape]) == side, shape
+
+
+def test_tiles_of_a_list():
+    shapes = [(10, 10)] * 3 + [(4096, 4096)] + [(1000, 1000)] * 9
+    assert [ops.ionn_muon_tile(shapes, l) for l in (0, 2, 3, 4, 11, 12)] == [32, 32, 256, 128, 128, 64]
+    for bad in (([(0, 4)], 0), ([(4, 4)], 1), ([(4, 4)], -1)):
+        with pytest.raises(ValueError):
+            ops.ionn_muon_tile(*bad)
 
 
 def test_the_binding_refuses_before_the_library():
