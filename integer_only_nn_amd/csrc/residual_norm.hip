@@ -14,7 +14,9 @@
 // through memory once each; together a and x are read and y and n written once
 // (forward), a, y, dy and dn read and da and dx written once (backward), and HBM
 // bounds both.  A row lies in registers, up to eight columns a thread, and the
-// next row's loads are in flight while a row's sums are taken.
+// next row's loads are in flight while a row's sums are taken.  Measured: forward 8192
+// x 4096 bf16 51 us (5.2 TB/s, a large copy reaches 5.1); backward 84 us in the first
+// pass (4.8 TB/s) and 8 in the second; 25088 x 256 float32 with 128 gates 28 and 5.
 //
 // The backward pass needs only four column sums for its five vectors: S1 = sum t
 // and Sh = sum t h_a of the rows that share a gate give that gate's gradient
@@ -29,6 +31,21 @@ namespace {
 
 constexpr int64_t kMaxCols = 16384;
 constexpr int kMaxGroups = 512;  // workgroups of the backward pass
+
+// store_vec, past the caches where `stream`: tensors larger than an XCD's L2.  2048
+// x 2048 bf16 forward 10.2 against 12.5 us, 8192 x 4096 51.1 against 55.1, backward
+// 92.5 and 94.1, 25088 x 256 float32 backward 35.8 and 39.3; smaller ones take as
+// long either way (1024 x 1024 8.8 and 13.8 us) and stay where the next kernel finds
+// them.
+constexpr size_t kStreamBytes = size_t(4) << 20;
+template <class T, int VE>
+__device__ __forceinline__ void put_vec(T *p, const float (&x)[VE], int valid, bool stream) {
+    if (!stream || valid < VE) return store_vec<T, VE>(p, x, valid);
+    typename Vec<T, VE>::type v;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] = T(x[i]);
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Vec<T, VE>::loose *>(p));
+}
 
 // Sums of v over the TPR threads that share a row (whole wavefronts); every one
 // of them gets them.  buf: the wavefronts' sums, twice over, so that one barrier
@@ -69,6 +86,7 @@ struct Forward {
     int cols;
     float alpha, eps;
     uint32_t *absmax;
+    bool stream;
 };
 
 // The columns of a thread: (i TPR + t) VE .. + VE - 1, i < NV.
@@ -131,7 +149,8 @@ __global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(For
     T *y = static_cast<T *>(f.y), *n = static_cast<T *>(f.n);
     const int t = threadIdx.x % TPR, cols = f.cols;
     const int64_t step = int64_t(gridDim.x) * kRows;
-    int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
+    // (a wavefront has one row: addresses are scalar but for the column)
+    int64_t r = int64_t(blockIdx.x) * kRows + __builtin_amdgcn_readfirstlane(int(threadIdx.x) / TPR);
     int ph = 0;
     uint32_t top = 0;
     typename Vec<T, VE>::type ra[NV], rx[NV];
@@ -185,7 +204,7 @@ __global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(For
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TPR + t) * VE;
-                if (c < cols) store_vec<T, VE>(y + r * cols + c, w[i], cols - c);
+                if (c < cols) put_vec<T, VE>(y + r * cols + c, w[i], cols - c, f.stream);
             }
         }
         if (n == nullptr) continue;
@@ -205,7 +224,7 @@ __global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(For
                 o[e] = w[i][e] * gy.v[i][e] + by.v[i][e];
                 if (e < valid) top = max(top, mag_bits(o[e]));
             }
-            store_vec<T, VE>(n + r * cols + c, o, valid);
+            put_vec<T, VE>(n + r * cols + c, o, valid, f.stream);
         }
     }
     if (f.absmax) {
@@ -226,10 +245,12 @@ struct Backward {
     uint32_t chunk_rows, units;  // rows of a run; runs of all gates
     int cols;
     float alpha;
+    // (kSums of two rows each are written)
     // [units][2][cols] (Sh, S1; with whole gates [workgroups][2][cols], dgamma_a
     // and dbeta_a), [workgroups][2][cols] (dgamma_y, dbeta_y); nullable
     float *part_a, *part_y;
     float *dgate;  // with whole gates; nullable
+    bool stream;
 };
 
 constexpr int bwd_threads(int tpr) { return tpr == 64 ? 512 : tpr; }
@@ -247,52 +268,57 @@ __device__ __forceinline__ void rows_of(const typename Vec<T, VE>::type (&raw)[N
 }
 
 // d := rstd (d - mean(d) - h mean(d h)), the first mean for a layer norm only.
-template <int VE, int TPR, int NV>
+template <int VE, int TPR, int NV, bool SHIFT>
 __device__ __forceinline__ void project(float (&d)[NV][VE], const float (&h)[NV][VE], int kind, float rstd, float n,
-                                        float (*buf)[2][TPR / 64 + 1], int &ph) {
-    float s[2] = {0.0f, 0.0f};
+                                        float (*buf)[SHIFT ? 2 : 1][TPR / 64 + 1], int &ph) {
+    constexpr int kLast = SHIFT ? 1 : 0;
+    float s[SHIFT ? 2 : 1] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            s[0] += d[i][e];
-            s[1] += d[i][e] * h[i][e];
+            if (SHIFT) s[0] += d[i][e];
+            s[kLast] += d[i][e] * h[i][e];
         }
-    row_sums<TPR, 2>(s, buf, ph);
-    const float c1 = kind == IONN_NORM_LAYER ? s[0] / n : 0.0f, c2 = s[1] / n;
+    row_sums<TPR, SHIFT ? 2 : 1>(s, buf, ph);
+    const float c1 = SHIFT && kind == IONN_NORM_LAYER ? s[0] / n : 0.0f, c2 = s[kLast] / n;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < VE; ++e) d[i][e] = rstd * (d[i][e] - c1 - h[i][e] * c2);
 }
 
-// WHOLE: a unit is a gate's rows, taken by one of a workgroup's row groups.
-template <class T, int VE, int TPR, int NV, bool WHOLE>
-__global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Backward b) {
+// WHOLE: a unit is a gate's rows, taken by one of a workgroup's row groups.  SHIFT:
+// one of the norms is a layer norm, so that the sums S1 and dbeta_y are needed
+// (without their registers two workgroups of 512 threads share a compute unit).
+template <class T, int VE, int TPR, int NV, bool WHOLE, bool SHIFT>
+__global__ __launch_bounds__(bwd_threads(TPR), NV * VE <= 8 && !(WHOLE && SHIFT) ? 4 : 1) void residual_norm_bwd_kernel(Backward b) {
     constexpr int kRows = bwd_threads(TPR) / TPR;
     typedef Cols<VE, TPR, NV> Vector;
-    __shared__ float buf[2][2][TPR / 64 + 1];
+    __shared__ float buf[2][SHIFT ? 2 : 1][TPR / 64 + 1];
     __shared__ float fold[kRows > 1 ? kRows * NV * VE * TPR : 1];
     const T *dy = static_cast<const T *>(b.dy), *dn = static_cast<const T *>(b.dn);
     const T *a = static_cast<const T *>(b.a), *y = static_cast<const T *>(b.y);
     T *da = static_cast<T *>(b.da), *dx = static_cast<T *>(b.dx);
-    const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR, cols = b.cols;
+    // (a wavefront has one row: addresses are scalar but for the column)
+    const int t = threadIdx.x % TPR, rg = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / TPR), cols = b.cols;
     const float n = float(cols);
     int ph = 0;
     // S: Sh, S1 of the run at hand; Y: dgamma_y, dbeta_y of all runs; A (WHOLE): dgamma_a, dbeta_a of all runs
-    Vector gy, ga, S[2], Y[2], A[WHOLE ? 2 : 1];
+    constexpr int kSums = SHIFT ? 2 : 1;
+    Vector gy, ga, S[kSums], Y[kSums], A[WHOLE ? kSums : 1];
     gy.load(b.ny.gamma, cols, t, 1.0f);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < kSums; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VE; ++e) Y[k].v[i][e] = A[WHOLE ? k : 0].v[i][e] = 0.0f;
 
     // the row groups of a workgroup one after the other, to two rows of partial sums
-    const auto leave = [&](Vector (&s)[2], float *to) __attribute__((always_inline)) {
+    const auto leave = [&](Vector *s, float *to) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kSums; ++k) {
             if (kRows > 1) {
                 __syncthreads();
 #pragma unroll
@@ -350,7 +376,8 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
                     ga.v[i][e] *= g.v[i][e];
-                    S[0].v[i][e] = S[1].v[i][e] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kSums; ++k) S[k].v[i][e] = 0.0f;
                 }
         }
         if (r < last) load_row(r);
@@ -358,14 +385,14 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
             float d[NV][VE], h[NV][VE], past[NV][VE];
             const float mu_a = mean_a, rs_a = rstd_a, rs_y = rstd_y;
             if (dn) {
-                rows_of<T, VE, TPR, NV>(r_y, mean_y, rs_y, cols, t, h);
+                rows_of<T, VE, TPR, NV>(r_y, SHIFT ? mean_y : 0.0f, rs_y, cols, t, h);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
                         const float v = float(r_dn[i][e]);
                         Y[0].v[i][e] += v * h[i][e];
-                        Y[1].v[i][e] += v;
+                        if (SHIFT) Y[kSums - 1].v[i][e] += v;
                         d[i][e] = v * gy.v[i][e];
                     }
             }
@@ -378,7 +405,7 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
             for (int i = 0; i < NV; ++i) row_a[i] = r_a[i];
             if (r + kStep < last) load_row(r + kStep);
             if (dn) {
-                project<VE, TPR, NV>(d, h, b.ny.kind, rs_y, n, buf, ph);
+                project<VE, TPR, NV, SHIFT>(d, h, b.ny.kind, rs_y, n, buf, ph);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -391,25 +418,25 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
                     float o[VE];
 #pragma unroll
                     for (int e = 0; e < VE; ++e) o[e] = b.alpha * past[i][e];
-                    if (c < cols) store_vec<T, VE>(dx + r * cols + c, o, cols - c);
+                    if (c < cols) put_vec<T, VE>(dx + r * cols + c, o, cols - c, b.stream);
                 }
             }
             if (!a) continue;
-            rows_of<T, VE, TPR, NV>(row_a, mu_a, rs_a, cols, t, h);
+            rows_of<T, VE, TPR, NV>(row_a, SHIFT ? mu_a : 0.0f, rs_a, cols, t, h);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
                     S[0].v[i][e] += past[i][e] * h[i][e];
-                    S[1].v[i][e] += past[i][e];
+                    if (SHIFT) S[kSums - 1].v[i][e] += past[i][e];
                     d[i][e] = past[i][e] * ga.v[i][e];
                 }
             if (da) {
-                if (b.na.kind != IONN_NORM_NONE) project<VE, TPR, NV>(d, h, b.na.kind, rs_a, n, buf, ph);
+                if (b.na.kind != IONN_NORM_NONE) project<VE, TPR, NV, SHIFT>(d, h, b.na.kind, rs_a, n, buf, ph);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = (i * TPR + t) * VE;
-                    if (c < cols) store_vec<T, VE>(da + r * cols + c, d[i], cols - c);
+                    if (c < cols) put_vec<T, VE>(da + r * cols + c, d[i], cols - c, b.stream);
                 }
             }
         }
@@ -420,16 +447,17 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
         Vector g, gamma, beta;
         g.load(b.gate + int64_t(group) * cols, cols, t, 1.0f);
         gamma.load(b.na.gamma, cols, t, 1.0f);
-        beta.load(b.na.beta, cols, t, 0.0f);
+        if (SHIFT) beta.load(b.na.beta, cols, t, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VE;
             float o[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                o[e] = gamma.v[i][e] * S[0].v[i][e] + beta.v[i][e] * S[1].v[i][e];
-                A[0].v[i][e] += g.v[i][e] * S[0].v[i][e];
-                A[WHOLE ? 1 : 0].v[i][e] += g.v[i][e] * S[1].v[i][e];
+                o[e] = gamma.v[i][e] * S[0].v[i][e];
+                if (SHIFT) o[e] += beta.v[i][e] * S[kSums - 1].v[i][e];
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) A[WHOLE ? k : 0].v[i][e] += g.v[i][e] * S[k].v[i][e];
             }
             if (b.dgate && c < cols) store_vec<float, VE>(b.dgate + int64_t(group) * cols + c, o, cols - c);
         }
@@ -440,11 +468,13 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void residual_norm_bwd_kernel(Bac
     if (b.part_y) leave(Y, b.part_y + int64_t(blockIdx.x) * 2 * cols);
 }
 
-// The partial rows added up, 64 columns a workgroup, in an order that the sizes
-// fix: workgroups of blockIdx.y = 0 those of the gates, of 1 those of N_y.  Where
-// a gate's rows were cut into many runs, 16 groups of threads share a gate's runs;
-// elsewhere they share the gates.
-constexpr int kSumGroups = 16;
+// The partial rows added up, 16 columns a workgroup, in an order that the sizes
+// fix: workgroups of blockIdx.y = 0 those of the gates, of 1 those of N_y.  64
+// groups of threads share a gate's runs where there are as many, elsewhere the
+// gates.  (64 columns and 16 groups: 16 us at 4096 columns and 512 partial rows, and at
+// 256 columns, which were four workgroups; so 8 and 5.)
+constexpr uint32_t kAtOnce = 2;
+constexpr int kSumCols = 16, kSumGroups = 64, kSumWaves = kSumCols * kSumGroups / 64;
 
 struct Sums {
     const float *part_a, *part_y;
@@ -452,15 +482,15 @@ struct Sums {
     float *dgate, *dgamma_a, *dbeta_a, *dgamma_y, *dbeta_y;
     uint32_t groups, chunks, parts;  // parts: workgroups of the first pass
     int cols;
-    bool whole, a, y;  // part_a is of whole gates; asked for
+    bool whole, a, y, shift;  // part_a is of whole gates; asked for; the second sums are there
 };
 
-__global__ __launch_bounds__(64 * kSumGroups) void residual_norm_sum_kernel(Sums s) {
-    __shared__ float red[2][kSumGroups][64];
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    const int64_t cols = s.cols, c = int64_t(blockIdx.x) * 64 + lane;
+__global__ __launch_bounds__(kSumCols *kSumGroups) void residual_norm_sum_kernel(Sums s) {
+    __shared__ float red[2][kSumWaves][kSumCols];
+    const int lane = threadIdx.x & (kSumCols - 1), grp = threadIdx.x / kSumCols;
+    const int64_t cols = s.cols, c = int64_t(blockIdx.x) * kSumCols + lane;
     const bool in = c < cols;
-    // both sums of `count` partial rows from p on, every kSumGroups-th (in all groups' threads alike)
+    // both sums of partial rows from, from + by .. of `count` from p on
     const auto run = [&](const float *p, uint32_t from, uint32_t count, uint32_t by, float (&v)[2])
         __attribute__((always_inline)) {
             v[0] = v[1] = 0.0f;
@@ -468,18 +498,24 @@ __global__ __launch_bounds__(64 * kSumGroups) void residual_norm_sum_kernel(Sums
 #pragma unroll 8
             for (uint32_t k = from; k < count; k += by) {
                 v[0] += p[int64_t(k) * 2 * cols + c];
-                v[1] += p[int64_t(k) * 2 * cols + cols + c];
+                if (s.shift) v[1] += p[int64_t(k) * 2 * cols + cols + c];
             }
         };
-    // v of all groups, in order (every group gets it)
+    // v of all groups: a wavefront's four, then the wavefronts (every group gets it)
     const auto join = [&](float (&v)[2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int off = kSumCols; off < 64; off <<= 1) v[k] += __shfl_xor(v[k], off, 64);
         __syncthreads();
-        red[0][grp][lane] = v[0];
-        red[1][grp][lane] = v[1];
+        if ((threadIdx.x & 63) < kSumCols) {
+            red[0][threadIdx.x >> 6][lane] = v[0];
+            red[1][threadIdx.x >> 6][lane] = v[1];
+        }
         __syncthreads();
         v[0] = v[1] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kSumGroups; ++k) {
+        for (int k = 0; k < kSumWaves; ++k) {
             v[0] += red[0][k][lane];
             v[1] += red[1][k][lane];
         }
@@ -498,23 +534,31 @@ __global__ __launch_bounds__(64 * kSumGroups) void residual_norm_sum_kernel(Sums
     }
     const float gamma = s.gamma_a && in ? s.gamma_a[c] : 1.0f, beta = s.beta_a && in ? s.beta_a[c] : 0.0f;
     float all[2] = {0.0f, 0.0f};
-    const auto add = [&](uint32_t g, const float (&w)[2], bool write) __attribute__((always_inline)) {
+    const auto add = [&](uint32_t g, float gate, const float (&w)[2], bool write) __attribute__((always_inline)) {
         if (!in) return;
         if (s.dgate && write) s.dgate[int64_t(g) * cols + c] = gamma * w[0] + beta * w[1];
-        const float gate = s.gate ? s.gate[int64_t(g) * cols + c] : 1.0f;
         all[0] += gate * w[0];
         all[1] += gate * w[1];
     };
     if (s.chunks >= uint32_t(kSumGroups)) {
         for (uint32_t g = 0; g < s.groups; ++g) {
             run(s.part_a + int64_t(g) * s.chunks * 2 * cols, grp, s.chunks, kSumGroups, v);
+            const float gate = s.gate && in ? s.gate[int64_t(g) * cols + c] : 1.0f;
             join(v);
-            add(g, v, grp == 0);
+            add(g, gate, v, grp == 0);
         }
     } else {
-        for (uint32_t g = grp; g < s.groups; g += kSumGroups) {
-            run(s.part_a + int64_t(g) * s.chunks * 2 * cols, 0, s.chunks, 1, v);
-            add(g, v, true);
+        for (uint32_t g0 = grp; g0 < s.groups; g0 += kAtOnce * kSumGroups) {
+            float w[kAtOnce][2], gate[kAtOnce];  // loads of several gates in flight
+#pragma unroll
+            for (uint32_t u = 0; u < kAtOnce; ++u) {
+                const uint32_t g = min(g0 + u * kSumGroups, s.groups - 1);
+                gate[u] = s.gate && in ? s.gate[int64_t(g) * cols + c] : 1.0f;
+                run(s.part_a + int64_t(g) * s.chunks * 2 * cols, 0, s.chunks, 1, w[u]);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kAtOnce; ++u)
+                if (g0 + u * kSumGroups < s.groups) add(g0 + u * kSumGroups, gate[u], w[u], true);
         }
         join(all);
     }
@@ -611,7 +655,7 @@ int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a, const float
                  IONN_ERR_ARG, "ionn_residual_norm_fwd: y and n may be a or x, but not overlap them or each other otherwise");
     const int64_t share = gate && gate_rows > 0 && gate_rows < rows ? gate_rows : rows;
     const Forward f{a, x, y, n, {norm_a, gamma_a, beta_a, mean_a, rstd_a}, {norm_y, gamma_y, beta_y, mean_y, rstd_y},
-                    gate, rows, uint32_t(share), int(cols), float(alpha), float(eps), absmax_n};
+                    gate, rows, uint32_t(share), int(cols), float(alpha), float(eps), absmax_n, bytes >= kStreamBytes};
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
         constexpr int VE = 16 / sizeof(T);
@@ -695,7 +739,7 @@ int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a, const 
                          {norm_a, gamma_a, beta_a, const_cast<float *>(mean_a), const_cast<float *>(rstd_a)},
                          {norm_y, gamma_y, nullptr, const_cast<float *>(mean_y), const_cast<float *>(rstd_y)},
                          gate, rows, uint32_t(share), runs.chunks, runs.chunk_rows, runs.units(), int(cols), float(alpha),
-                         part_a, part_y, dgate};
+                         part_a, part_y, dgate, bytes >= kStreamBytes};
         with_dtype(dtype, [&](auto tag) {
             using T = decltype(tag);
             constexpr int VE = 16 / sizeof(T);
@@ -705,16 +749,22 @@ int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a, const 
                 blocks = (runs.units() + each - 1) / each;
                 if (blocks > kMaxGroups) blocks = kMaxGroups;
                 const dim3 grid{unsigned(blocks)}, block{unsigned(kBlock)};
-                if (runs.whole()) residual_norm_bwd_kernel<T, VE, TPR, NV, true><<<grid, block, 0, st>>>(b);
-                else residual_norm_bwd_kernel<T, VE, TPR, NV, false><<<grid, block, 0, st>>>(b);
+                const auto launch = [&](auto whole, auto shift) {
+                    residual_norm_bwd_kernel<T, VE, TPR, NV, decltype(whole)::value, decltype(shift)::value>
+                        <<<grid, block, 0, st>>>(b);
+                };
+                const bool shift = norm_a == IONN_NORM_LAYER || norm_y == IONN_NORM_LAYER;
+                if (runs.whole()) shift ? launch(IntC<1>{}, IntC<1>{}) : launch(IntC<1>{}, IntC<0>{});
+                else shift ? launch(IntC<0>{}, IntC<1>{}) : launch(IntC<0>{}, IntC<0>{});
             });
         });
         if (int rc = check_launch("ionn_residual_norm_bwd")) return rc;
     }
     if (sums_a || sums_y) {  // (of no rows: zeros)
         const Sums s{part_a, part_y, gate, gamma_a, beta_a, dgate, dgamma_a, dbeta_a, dgamma_y, dbeta_y,
-                     runs.groups, runs.chunks, uint32_t(blocks), int(cols), runs.whole(), sums_a, sums_y};
-        residual_norm_sum_kernel<<<dim3(unsigned((cols + 63) / 64), 2), dim3(64 * kSumGroups), 0, st>>>(s);
+                     runs.groups, runs.chunks, uint32_t(blocks), int(cols), runs.whole(), sums_a, sums_y,
+                     norm_a == IONN_NORM_LAYER || norm_y == IONN_NORM_LAYER};
+        residual_norm_sum_kernel<<<dim3(unsigned((cols + kSumCols - 1) / kSumCols), 2), dim3(kSumCols * kSumGroups), 0, st>>>(s);
         return check_launch("ionn_residual_norm_bwd");
     }
     return IONN_OK;
