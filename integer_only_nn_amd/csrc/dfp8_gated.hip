@@ -31,6 +31,7 @@ namespace {
 using namespace dfp8;
 
 constexpr int kThreads = 256;
+constexpr int kRoundGroups = 2048;
 
 // ---- forward -------------------------------------------------------------------
 
@@ -189,8 +190,9 @@ __global__ __launch_bounds__(kThreads) void gated_sums_kernel(const T *__restric
     }
 }
 
-// Workgroups below n_round round the errors, (strip, chunk) as above; those from
-// it on add up the chunks' column sums, 64 columns at a time, every fourth chunk
+// Workgroups below n_round round the errors, each every n_round-th (strip, chunk)
+// as above (each reads all maxima, so there are at most kRoundGroups); those from it
+// on add up the chunks' column sums, 64 columns at a time, every fourth chunk
 // per wavefront.
 template <class T, int ACT>
 __global__ __launch_bounds__(kThreads) void gated_round_kernel(
@@ -225,12 +227,7 @@ __global__ __launch_bounds__(kThreads) void gated_round_kernel(
         if (status) *status = dfp8_status(m, E);
     }
     const int lanes = 1 << lanes_log, per_wave = 64 >> lanes_log, step = (kThreads / 64) * per_wave;
-    const int chunk = int(blockIdx.x) / strips, strip = int(blockIdx.x) - chunk * strips;
-    const int c = (strip * lanes + (lane & (lanes - 1))) * VE;
-    if (c >= H) return;
-    const int valid = H - c;
-    const int64_t r1 = min(B, int64_t(chunk + 1) * chunk_rows);
-    auto put = [&](const Piece<T, VE> &p, int64_t r) __attribute__((always_inline)) {
+    auto put = [&](const Piece<T, VE> &p, int64_t r, int c, int valid) __attribute__((always_inline)) {
         uint32_t qg[VE], qu[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
@@ -243,18 +240,23 @@ __global__ __launch_bounds__(kThreads) void gated_round_kernel(
         store_bytes(z, qg, VE, valid);
         store_bytes(z + H, qu, VE, valid);
     };
-    int64_t r = int64_t(chunk) * chunk_rows + wave * per_wave + (lane >> lanes_log);
-    for (; r + step < r1; r += 2 * step) {  // two rows' loads in flight
-        Piece<T, VE> p[2];
+    for (int unit = int(blockIdx.x); unit < nparts; unit += n_round) {
+        const int chunk = unit / strips, c = ((unit - chunk * strips) * lanes + (lane & (lanes - 1))) * VE, valid = H - c;
+        if (valid <= 0) continue;
+        const int64_t r1 = min(B, int64_t(chunk + 1) * chunk_rows);
+        int64_t r = int64_t(chunk) * chunk_rows + wave * per_wave + (lane >> lanes_log);
+        for (; r + step < r1; r += 2 * step) {  // two rows' loads in flight
+            Piece<T, VE> p[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) p[k].load(dY, Z, r + k * step, H, c, valid);
+            for (int k = 0; k < 2; ++k) p[k].load(dY, Z, r + k * step, H, c, valid);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) put(p[k], r + k * step);
-    }
-    for (; r < r1; r += step) {
-        Piece<T, VE> p;
-        p.load(dY, Z, r, H, c, valid);
-        put(p, r);
+            for (int k = 0; k < 2; ++k) put(p[k], r + k * step, c, valid);
+        }
+        for (; r < r1; r += step) {
+            Piece<T, VE> p;
+            p.load(dY, Z, r, H, c, valid);
+            put(p, r, c, valid);
+        }
     }
 }
 
@@ -273,7 +275,7 @@ size_t error_bytes(int64_t B, int64_t H) {
 void launch_errors(const void *dY, const void *Z, int act, int dtype, int64_t B, int64_t H, int8_t *dZ8, int32_t *edZ,
                    float *gb, int32_t *status, void *workspace, hipStream_t st) {
     const ActLayout a = act_layout(B, H, dtype_size(dtype));
-    const int nparts = a.strips * a.chunks;
+    const int nparts = a.strips * a.chunks, n_round = nparts < kRoundGroups ? nparts : kRoundGroups;
     uint32_t *maxima = static_cast<uint32_t *>(workspace);
     float *sums = gb ? reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                                  ((size_t(nparts) * sizeof(uint32_t) + 15) & ~size_t(15)))
@@ -289,8 +291,8 @@ void launch_errors(const void *dY, const void *Z, int act, int dtype, int64_t B,
             constexpr int ACT = decltype(ac)::value;
             gated_sums_kernel<T, ACT><<<dim3(unsigned(a.strips), unsigned(a.chunks)), dim3(kThreads), 0, st>>>(
                 y, z, B, int(H), lanes_log, a.rows, maxima, sums);
-            gated_round_kernel<T, ACT><<<dim3(unsigned(nparts) + n_sum), dim3(kThreads), 0, st>>>(
-                y, z, B, int(H), lanes_log, a.strips, a.rows, nparts, maxima, nparts, sums, a.chunks, dZ8, edZ, gb,
+            gated_round_kernel<T, ACT><<<dim3(unsigned(n_round) + n_sum), dim3(kThreads), 0, st>>>(
+                y, z, B, int(H), lanes_log, a.strips, a.rows, n_round, maxima, nparts, sums, a.chunks, dZ8, edZ, gb,
                 status);
         });
     });

@@ -503,6 +503,9 @@ bool size_ok(int64_t rows, int64_t cols) {
            up(rows, 256) * up(cols, 256) <= kMaxElements;
 }
 
+// Whether n floats at a and m at b have one in common.
+bool overlap(const float *a, int64_t n, const float *b, int64_t m) { return a < b + m && b < a + n; }
+
 // Takes the matrices from l on that share their launches; returns their number.
 int take_batch(int L, const int64_t *rows, const int64_t *cols, int l, Mat *mats) {
     int k = 0;
@@ -607,6 +610,18 @@ int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype, fl
                      "ionn_muon_step: matrix %d must be aligned to its element size", l);
         IONN_REQUIRE(!scale || (scale[l] >= -3.0e38 && scale[l] <= 3.0e38), IONN_ERR_RANGE,
                      "ionn_muon_step: scale %d is %g", l, scale ? scale[l] : 0.0);
+    }
+    for (int l = 0; l < L; ++l) {
+        const int64_t n = rows[l] * cols[l];
+        const float *g = static_cast<const float *>(G[l]);
+        IONN_REQUIRE(!overlap(P[l], n, M[l], n) && !overlap(M[l], n, g, (n * int64_t(dtype_size(g_dtype)) + 3) / 4),
+                     IONN_ERR_ARG, "ionn_muon_step: matrix %d overlaps its momentum, or that its gradient", l);
+        for (int k = 0; k < l; ++k) {  // (they are worked side by side)
+            const int64_t m = rows[k] * cols[k];
+            IONN_REQUIRE(!overlap(P[l], n, P[k], m) && !overlap(M[l], n, M[k], m) && !overlap(P[l], n, M[k], m) &&
+                             !overlap(M[l], n, P[k], m),
+                         IONN_ERR_ARG, "ionn_muon_step: matrices %d and %d overlap", k, l);
+        }
     }
     const size_t need = ionn_muon_workspace_bytes(L, rows, cols);
     IONN_REQUIRE(workspace && aligned(workspace, 256) && workspace_bytes >= need, IONN_ERR_WORKSPACE,

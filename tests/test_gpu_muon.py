@@ -167,8 +167,9 @@ def test_nothing_else_is_written():
     assert (P[n + 1:] == 5).all() and P[0] == 5 and (M[n + 3:] == 5).all() and (M[:3] == 5).all() and (ws[need:] == 77).all()
 
 
-def test_the_result_does_not_depend_on_the_workspace():
-    d = _case(300, 500)
+@pytest.mark.parametrize("rows,cols", [(300, 500), (33, 65), (900, 1000), (2048, 2048), (2304, 2310)])
+def test_the_result_does_not_depend_on_the_workspace(rows, cols):
+    d = _case(rows, cols)
     out = []
     for fill in (0, 0xff):
         P, M = to_dev(d["P"]), to_dev(d["M"])

@@ -22,7 +22,7 @@ def test_step():
     need = lib.ionn_muon_workspace_bytes(1, i64(8), i64(8))
     assert need > 0
 
-    def f(L=1, p=arr(0x1000), g=arr(0x1000), dt=0, m=arr(0x1000), r=i64(8), c=i64(8), lr=0.1, mu=0.9, nes=1, eps=1e-7, wd=0.0,
+    def f(L=1, p=arr(0x1000), g=arr(0x3000), dt=0, m=arr(0x2000), r=i64(8), c=i64(8), lr=0.1, mu=0.9, nes=1, eps=1e-7, wd=0.0,
           k=5, sc=None, lrd=None, gs=None, top=None, ws=P(0x10000), wb=need):
         return lib.ionn_muon_step(L, p, g, dt, m, r, c, lr, mu, nes, eps, wd, k, sc, lrd, gs, top, ws, wb, None)
     assert f(L=0) == SHAPE and f(r=i64(0)) == SHAPE and f(c=i64(-1)) == SHAPE and f(r=i64(1 << 15), c=i64(1 << 14)) == SHAPE
@@ -33,6 +33,15 @@ def test_step():
     assert f(mu=1.0) == RANGE and f(mu=-0.1) == RANGE and f(mu=NAN) == RANGE and f(eps=-1.0) == RANGE and f(lr=INF) == RANGE
     assert f(wd=NAN) == RANGE and f(k=0) == RANGE and f(k=33) == RANGE and f(sc=(ctypes.c_double * 1)(NAN)) == RANGE
     assert f(ws=None) == WS and f(wb=need - 1) == WS and f(ws=P(0x10080)) == WS
+    assert f(m=arr(0x1000)) == ARG and f(m=arr(0x10fc)) == ARG and f(g=arr(0x20fc)) == ARG and f(g=arr(0x1f82), dt=1) == ARG
+    assert f(m=arr(0x1100), ws=None) == WS and f(g=arr(0x1f80), dt=1, ws=None) == WS  # next to each other
+    two = lambda a, b: (ctypes.c_void_p * 2)(a, b)  # noqa: E731
+    twice = dict(L=2, g=two(0x8000, 0x9000), r=(ctypes.c_int64 * 2)(8, 8), c=(ctypes.c_int64 * 2)(8, 8), ws=None)
+    assert f(p=two(0x1000, 0x1000), m=two(0x2000, 0x3000), **twice) == ARG
+    assert f(p=two(0x1000, 0x10f0), m=two(0x2000, 0x3000), **twice) == ARG
+    assert f(p=two(0x1000, 0x4000), m=two(0x2000, 0x2000), **twice) == ARG
+    assert f(p=two(0x1000, 0x2000), m=two(0x2000, 0x3000), **twice) == ARG
+    assert f(p=two(0x1000, 0x1100), m=two(0x2000, 0x2100), **twice) == WS
 
 
 def test_workspace_of_a_list_is_that_of_its_largest_part():
