@@ -226,9 +226,14 @@ __host__ __device__ __forceinline__ Work work_of(const Mat &a, int product, int 
     const int tm = w.rows / SIDE, tn = w.cols / SIDE;
     w.tiles = w.tri ? tm * (tm + 1) / 2 : tm * tn;
     w.S = w.K < 64 ? 1 : w.K / 64;
+    // wide blocks, but places without a tile in the last one are a lane's idle workgroups
+    // (36 tiles in blocks of 8: five of 1000 x 1000 798 us, in blocks of 4 694)
+    w.width = 8;
+    while (w.width > 1 && 32 * (-w.tiles & (w.width - 1)) > w.tiles) w.width /= 2;
     w.chunk = chunk;
     w.slots = (chunk + w.S - 1) / w.S + 1;
-    w.groups = int((int64_t(w.tiles) * w.S + chunk - 1) / chunk);
+    w.lanes = int((int64_t(w.tiles + w.width - 1) / w.width * w.S + chunk - 1) / chunk);
+    w.groups = (w.lanes + 7) / 8 * 8 * w.width;
     return w;
 }
 
@@ -247,10 +252,7 @@ __global__ __launch_bounds__(g256::NT, 1) void product256_kernel(Mat a, int prod
     __shared__ __attribute__((aligned(1024))) int8_t sA1[g256::TILE_BYTES];
     __shared__ __attribute__((aligned(1024))) int8_t sB1[g256::TILE_BYTES];
     const Work w = work_of<256>(a, product, chunk);
-    // neighbouring runs on one XCD
-    int g = int(blockIdx.x);
-    if (w.groups % 8 == 0) g = (g % 8) * (w.groups / 8) + g / 8;
-    muon::pieces<256>(w, g, [&](int ti, int tj, int k0, int k1, float *to) {
+    muon::pieces<256>(w, int(blockIdx.x), [&](int ti, int tj, int k0, int k1, float *to) {
         muon::piece256(w, ti, tj, k0, k1, to, sA0, sB0, sA1, sB1);
     });
 }
@@ -359,11 +361,12 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(Table t, Hyper h, int 
     f.load(a, product, r0, c0);
     v4f v[4] = {};
     const int block = (part * F + 2 * i + (wave >> 1)) * F + 2 * j + (wave & 1);
-    const int first = tile * w.S / chunk, end = ((tile + 1) * w.S - 1) / chunk;
+    const int run = tile / w.width, q8 = tile - run * w.width;  // the tile's block and place in it
+    const int first = run * w.S / chunk, end = ((run + 1) * w.S - 1) / chunk;
     for (int g = first; g <= end; ++g) {
-        const int slot = tile - g * chunk / w.S;
-        const v4f *p =
-            reinterpret_cast<const v4f *>(w.part + (int64_t(g) * w.slots + slot) * (SIDE * SIDE)) + block * 256 + lane;
+        const int slot = run - g * chunk / w.S;
+        const v4f *p = reinterpret_cast<const v4f *>(w.part + (int64_t(g * w.width + q8) * w.slots + slot) * (SIDE * SIDE)) +
+                       block * 256 + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += p[64 * q];
     }
@@ -473,12 +476,12 @@ Layout lay_out(Mat *mats, int L, char *base) {
         };
         for (int l = 0; l < L; ++l) {
             const Work w = work(l, 1);
-            total += int64_t(w.tiles) * w.S;
+            total += int64_t(w.tiles + w.width - 1) / w.width * w.width * w.S;
         }
         y.chunk[p] = chunk_of(total, y.side == 256 ? 256 : 512);
         for (int l = 0; l < L; ++l) {
             const Work w = work(l, y.chunk[p]);
-            const size_t b = size_t(w.groups) * w.slots * y.side * y.side * sizeof(float);
+            const size_t b = size_t(w.lanes) * w.width * w.slots * y.side * y.side * sizeof(float);
             most[l] = b > most[l] ? b : most[l];
         }
     }
