@@ -11,14 +11,22 @@
 // float16 terms (muon_tile.h): 22 bits, for P and M are float32, and one term
 // alone would leave X off by 1.5e-3 of its size, one of bfloat16 by 1.2e-2
 // (where a few directions dominate, ten times as much).  Scaled by 2^12, which
-// keeps the terms of entries down to 2^-26 of a singular value's size out of
-// float16's subnormal range and the largest (|b| + |c| of B) a factor of 5 below
-// its largest value.
+// keeps the high terms of entries down to 2^-26 of a singular value's size out of
+// float16's subnormal range and the largest entries, 2.8 of b A + c A A, a factor of
+// 5 below its largest value.
 //
 // A product leaves its sums in pieces, and the pass after it adds them, applies
 // the polynomial and writes pairs: for a symmetric matrix both of its halves from
 // the lower tiles, for X both X and X^T, so that each operand is K-major, and at
-// the end P.  Matrices of a batch share every launch.
+// the end P.  Small tiles do both in one launch.  Matrices of a batch share every
+// launch.
+//
+// Measured: 4096 x 4096, bfloat16 gradients, 3.77 ms a step (4.28 on a card of lower
+// clocks): of each of the five rounds 182 us for each symmetric product and 320 for
+// X's (1200 and 1290 TFLOP/s of float16; the library's float16 product reaches
+// 1366), 33 and 47 us for what follows them (201 and 268 MB, at the rate of a copy),
+// and 29 and 47 us for the momentum and the first X.  1024 x 4096 470 us, 512 x 512
+// 92, 64 x 64 56: 17 launches of 3.3 us, of which an empty one takes 2.1.
 #include "muon_tile.h"
 
 #include <climits>
@@ -410,15 +418,15 @@ int64_t up(int64_t a, int64_t to) { return (a + to - 1) / to * to; }
 
 // The side of the tiles that a batch's matrices are worked in, by the sum of m^2 n
 // (a step's operations go with it) and the longest side; in us a step:
-//   32 (of a whole reduction each): 256 x 256 90 against 110 in tiles of 64 and 210
-//     in 128, 512 x 512 105 against 144; three of 512 x 512 (4.0e8) 165 and 143
-//   64 (the same): 1024 x 1024 190 against 308 in tiles of 128, 1536 x 1536 (3.6e9)
-//     509 and 529, four of 1000 x 1000 (4.0e9) 608 and 574
-//   128 (the reduction cut into runs): 2048 x 2048 (8.6e9) 811 against 876 in tiles
-//     of 256; with a long side also few operations, 128 x 32768 488 against 635
-//     in tiles of 32 (128 x 8192: 282 and 210)
-//   256, a matrix at a time: 2304 x 2304 (1.2e10) 1076 against 1320, 4096 x 4096
-//     3823 against 4866
+//   32 (of a whole reduction each): 256 x 256 69 against 106 in tiles of 64 and 215
+//     in 128, 512 x 512 93 against 141; three of 512 x 512 (4.0e8) 157 and 141
+//   64 (the same): 1024 x 1024 194 against 316 in tiles of 128, 1536 x 1536 (3.6e9)
+//     522 and 527, four of 1000 x 1000 (4.0e9) 610 and 611
+//   128 (the reduction cut into runs): 2048 x 2048 (8.6e9) 864 against 949 in tiles
+//     of 256; with a long side also few operations, 128 x 32768 497 against 621
+//     in tiles of 32 (128 x 8192: 298 and 208)
+//   256, a matrix at a time: 2304 x 2304 (1.2e10) 1163 against 1156, 3000 x 3000
+//     2110 against 2272, 4096 x 4096 4279 against 4823
 constexpr double kLarge = 1.15e10;
 double weight_of(const Mat &a) { return double(a.m) * a.m * a.n; }
 int side_of(const Mat *mats, int L) {

@@ -4,7 +4,7 @@
 //
 // A value x is hi + lo, hi = fl16(x), lo = fl16(x - hi): 22 bits.  A product is
 // hi hi + hi lo + lo hi (lo lo is below float32's last bit), three matrix
-// instructions where the float32 ones take the time of eight.  32 values of a row
+// instructions where a float32 product of the library takes the time of nine.  32 values of a row
 // lie as 64 bytes of hi and 64 of lo, so that a 128-byte K step of the int8
 // kernels' loaders (gemm256.h, dfp8_tile128.h) brings both terms of both operands
 // and LDS hands out each fragment once for three products.
@@ -143,8 +143,9 @@ __device__ __forceinline__ void piece128(const Work &w, int ti, int tj, int k0, 
 // each loads its own 32 values of K at a time, straight into LDS that no other
 // wavefront uses (two stages, no barrier), and their sums meet in LDS.  For
 // matrices of which tiles of 128 would be few: a product is then about one trip to
-// memory, and its epilogue is in the same launch.  (Through registers, four steps
-// in flight, 512 x 512 took 106 us a step against 101.)
+// memory, and its epilogue is in the same launch: 784-256-128-10 takes 88 us a step,
+// by tiles of 128 and their pieces 243.  (Through registers, four steps in flight,
+// 512 x 512 took 106 us against the 101 of its time, 92 today.)
 template <int F, int W>
 constexpr int kSmallLds = W * 2 * 2 * 32 * F * 128;
 
