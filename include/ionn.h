@@ -975,7 +975,8 @@ int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
  * device uint32 [L]): max-combined with the float32 bits of |P| after the step,
  * for dfp8_from_float.  L >= 1; P, G, M, rows, cols are HOST arrays; rows, cols
  * >= 1, their product as multiples of 256 at most 2^28; no P or M overlaps
- * another, nor M[l] G[l]; 0 <= momentum < 1; eps >= 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
+ * another of them or a G (gradients may be one tensor); 0 <= momentum < 1; eps >=
+ * 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
  * aligned, ionn_muon_workspace_bytes(L, rows, cols) bytes (0 on invalid sizes). */
 size_t ionn_muon_workspace_bytes(int L, const int64_t *rows, const int64_t *cols);
 /* The side of the tiles that matrix l is worked in, with those that share its

@@ -622,16 +622,16 @@ int ionn_muon_step(int L, float *const *P, const void *const *G, int g_dtype, fl
         IONN_REQUIRE(!scale || (scale[l] >= -3.0e38 && scale[l] <= 3.0e38), IONN_ERR_RANGE,
                      "ionn_muon_step: scale %d is %g", l, scale ? scale[l] : 0.0);
     }
-    for (int l = 0; l < L; ++l) {
+    for (int l = 0; l < L; ++l) {  // (matrices are worked side by side)
         const int64_t n = rows[l] * cols[l];
-        const float *g = static_cast<const float *>(G[l]);
-        IONN_REQUIRE(!overlap(P[l], n, M[l], n) && !overlap(M[l], n, g, (n * int64_t(dtype_size(g_dtype)) + 3) / 4),
-                     IONN_ERR_ARG, "ionn_muon_step: matrix %d overlaps its momentum, or that its gradient", l);
-        for (int k = 0; k < l; ++k) {  // (they are worked side by side)
+        for (int k = 0; k < L; ++k) {
             const int64_t m = rows[k] * cols[k];
-            IONN_REQUIRE(!overlap(P[l], n, P[k], m) && !overlap(M[l], n, M[k], m) && !overlap(P[l], n, M[k], m) &&
-                             !overlap(M[l], n, P[k], m),
-                         IONN_ERR_ARG, "ionn_muon_step: matrices %d and %d overlap", k, l);
+            const float *g = static_cast<const float *>(G[k]);
+            const int64_t gm = (m * int64_t(dtype_size(g_dtype)) + 3) / 4;
+            IONN_REQUIRE((k == l || (!overlap(P[l], n, P[k], m) && !overlap(M[l], n, M[k], m))) && !overlap(P[l], n, M[k], m),
+                         IONN_ERR_ARG, "ionn_muon_step: matrix or momentum %d overlaps one of %d", l, k);
+            IONN_REQUIRE(!overlap(P[l], n, g, gm) && !overlap(M[l], n, g, gm), IONN_ERR_ARG,
+                         "ionn_muon_step: matrix or momentum %d overlaps gradient %d", l, k);
         }
     }
     const size_t need = ionn_muon_workspace_bytes(L, rows, cols);

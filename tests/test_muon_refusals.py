@@ -44,6 +44,20 @@ def test_step():
     assert f(p=two(0x1000, 0x1100), m=two(0x2000, 0x2100), **twice) == WS
 
 
+def test_gradients_apart_from_what_the_step_writes():
+    def f(p, m, g, dt=0):
+        two = lambda v: (ctypes.c_void_p * 2)(*v)  # noqa: E731
+        s = (ctypes.c_int64 * 2)(8, 8)
+        return lib.ionn_muon_step(2, two(p), two(g), dt, two(m), s, s, 0.1, 0.9, 1, 1e-7, 0.0, 5, None, None, None, None, None, 0, None)
+    p, m = (0x1000, 0x1100), (0x2000, 0x2100)
+    for g in ((0x1000, 0x8000), (0x8000, 0x10fc), (0x8000, 0x2000), (0x21fc, 0x8000), (0x0f04, 0x8000)):
+        assert f(p, m, g) == ARG
+    assert f(p, m, (0x0f82, 0x8000), 1) == ARG
+    for g in ((0x8000, 0x8000), (0x0f00, 0x1200), (0x1f00, 0x2200)):  # a shared gradient; next to each other
+        assert f(p, m, g) == WS
+    assert f(p, m, (0x0f80, 0x2200), 1) == WS
+
+
 def test_workspace_of_a_list_is_that_of_its_largest_part():
     one = ops.ionn_muon_workspace_bytes([(4096, 4096)])
     assert one > 4096 * 4096 * 16
