@@ -16,6 +16,12 @@
 // epilogue.  The gradients' products are a Linear layer's of 2 H errors as they
 // stand.
 //
+// Where larger tiles would be faster but for rows that are not whole 16-byte
+// pieces, a product's operands are first copied into rows that are (in the
+// workspace): 8192 x 4095 -> 4095, bfloat16, 266 us forward and 621 backward,
+// straight in tiles of 64 743 and 1834; 2047 x 2047 -> 2047 33 and 78 against 53 and
+// 139.
+//
 // The errors are two passes over dY, g and u, bound by HBM: one that takes the
 // maximum and the column sums, one that rounds (the exponent needs the maximum
 // of the whole tensor first, and a float32 copy of dZ would cost more bytes than
@@ -40,13 +46,87 @@ constexpr int kRoundGroups = 2048;
 
 // ---- forward -------------------------------------------------------------------
 
+int64_t pitch_of(int64_t n) { return (n + 15) & ~int64_t(15); }
+bool large(Path p) { return p == TILE256 || p == TILE128; }
+
+// What copying operands of that many bytes takes, us.
+double copy_us(int64_t bytes) { return 4.0 + double(bytes) / 5.0e6; }
+
 // A Linear layer's plan for the 2 H rows of W; its tiles are counted in outputs.
-Plan gated_plan(int64_t B, int64_t IN, int64_t H) {
-    Plan p = make_plan<true, true>(B, 2 * H, IN, true);
+// pitch: of the copies of X and W, 0 where they are taken as they are.
+struct GatedPlan : Plan {
+    int64_t pitch;
+};
+GatedPlan gated_plan(int64_t B, int64_t IN, int64_t H) {
+    GatedPlan p{make_plan<true, true>(B, 2 * H, IN, true), 0};
+    if (p.path == TILE && IN % 16) {
+        const Plan c = make_plan<true, true>(B, 2 * H, IN, true, pitch_of(IN), pitch_of(IN));
+        // (tiles of 64 take a fifth to a third longer than expected where rows are off
+        // four bytes: 8192 x 1001 -> 2001 103 us against 63 with copies, 3000 x 1001 ->
+        // 999 23 and 21; 2048 x 1000 -> 1020 13 and 17, 8192 x 1000 -> 2000 78 and 65)
+        const double slow = IN % 4 ? 1.3 : 1.0;
+        if (large(c.path) && c.us + copy_us((B + 2 * H) * pitch_of(IN)) < slow * p.us) p = GatedPlan{c, pitch_of(IN)};
+    }
     if (p.path == ROWS) p.cols = 1;
     p.tiles = ceil_div(B, 64) * ceil_div(H, 32);
     return p;
 }
+
+// A tensor's rows in a copy of another pitch (a multiple of 16, less than 16 above
+// cols), zeros behind them.  cols >= 16, rows * pitch < 2^31.
+struct Rows {
+    const int8_t *from;
+    int8_t *to;
+    uint32_t cols, pitch, pieces;  // pieces of 16 bytes in all
+};
+struct Copies {
+    Rows r[3];
+    uint32_t first[3];  // workgroup
+};
+constexpr int kPiecesEach = 2;  // of a thread (8: 1000 x 1023 -> 2049 in tiles of 128 18.8 us against 18.0)
+
+__global__ __launch_bounds__(kThreads) void copy_rows_kernel(Copies c) {
+    typedef v4i loose __attribute__((aligned(1)));
+    const int i = (blockIdx.x >= c.first[1]) + (blockIdx.x >= c.first[2]);
+    const Rows &t = c.r[i];
+    const uint32_t id0 = (blockIdx.x - c.first[i]) * (kThreads * kPiecesEach) + threadIdx.x, per = t.pitch / 16;
+    v4i v[kPiecesEach];
+    uint32_t past[kPiecesEach];
+#pragma unroll
+    for (int k = 0; k < kPiecesEach; ++k) {
+        const uint32_t id = min(id0 + k * kThreads, t.pieces - 1), row = id / per, at = 16 * (id - row * per);
+        const uint32_t from = min(at, t.cols - 16);  // the row's last 16 bytes, shifted
+        past[k] = at - from;
+        v[k] = *reinterpret_cast<const loose *>(t.from + uint64_t(row) * t.cols + from);
+    }
+#pragma unroll
+    for (int k = 0; k < kPiecesEach; ++k) {
+        const uint32_t id = id0 + k * kThreads;
+        if (id < t.pieces) reinterpret_cast<v4i *>(t.to)[id] = shift_piece(v[k], int(past[k]));
+    }
+}
+
+// Copies of tensors into rows of pitch_of(cols) bytes, one after the other.
+struct Copier {
+    Copies c{};
+    int n = 0;
+    uint32_t groups = 0;
+    int8_t *to;
+    explicit Copier(void *at) : to(static_cast<int8_t *>(at)) {}
+    const int8_t *add(const int8_t *from, int64_t rows, int64_t cols) {
+        const uint32_t pitch = uint32_t(pitch_of(cols)), pieces = uint32_t(rows * pitch / 16);
+        c.r[n] = Rows{from, to, uint32_t(cols), pitch, pieces};
+        c.first[n++] = groups;
+        groups += uint32_t(ceil_div(pieces, kThreads * kPiecesEach));
+        int8_t *p = to;
+        to += rows * pitch;
+        return p;
+    }
+    void launch(hipStream_t st) {
+        for (int i = n; i < 3; ++i) c.first[i] = UINT32_MAX;
+        if (groups) copy_rows_kernel<<<dim3(groups), dim3(kThreads), 0, st>>>(c);
+    }
+};
 
 template <class T>
 void launch_gated(const Plan &pl, Product p, hipStream_t st) {
@@ -303,6 +383,41 @@ void launch_errors(const void *dY, const void *Z, int act, int dtype, int64_t B,
     });
 }
 
+// The gradients' products and which of their operands are copied.
+struct BackwardPlan {
+    BackwardSizes s;
+    bool copy_Z, copy_X, copy_W;
+    size_t copy_bytes() const {
+        return (copy_Z ? size_t(s.B) * s.ldz : 0) + (copy_X ? size_t(s.B) * s.ldx : 0) + (copy_W ? size_t(s.OUT) * s.ldw : 0);
+    }
+};
+BackwardPlan backward_plan(int64_t B, int64_t IN, int64_t H) {
+    const int64_t OUT = 2 * H;
+    BackwardPlan p{{B, IN, OUT, OUT, IN, IN}, false, false, false};
+    const bool z = OUT % 16 != 0, in = IN % 16 != 0;
+    if (!z && !in) return p;
+    Plan d, g, dc, gc;
+    backward_plans(p.s, d, g);
+    backward_plans({B, IN, OUT, pitch_of(OUT), pitch_of(IN), pitch_of(IN)}, dc, gc);
+    const int64_t bz = z ? B * pitch_of(OUT) : 0, bx = in ? B * pitch_of(IN) : 0, bw = in ? OUT * pitch_of(IN) : 0;
+    bool for_d = d.path == TILE && large(dc.path), for_g = g.path == TILE && large(gc.path);
+    // (with copies for both: 1025 x 4095 -> 1001 55 us against 78, 2000 x 3001 -> 501 55
+    // and 68; for one alone there is less to gain: 300 x 4095 -> 8192 152 without, 159
+    // with, 1024 x 2050 -> 2050 80 and 88)
+    const double slow = IN % 4 || OUT % 4 ? 1.15 : 1.0;
+    if (!(for_d && for_g && dc.us + gc.us + copy_us(bz + bx + bw) < slow * (d.us + g.us))) {
+        for_d = for_d && dc.us + copy_us(bz + bw) < d.us;
+        for_g = for_g && gc.us + copy_us(bz + bx) < g.us;
+    }
+    p.copy_Z = z && (for_d || for_g);
+    p.copy_X = in && for_g;
+    p.copy_W = in && for_d;
+    if (p.copy_Z) p.s.ldz = pitch_of(OUT);
+    if (p.copy_X) p.s.ldx = pitch_of(IN);
+    if (p.copy_W) p.s.ldw = pitch_of(IN);
+    return p;
+}
+
 bool gated_sizes_ok(int64_t B, int64_t IN, int64_t H) {
     return H >= 0 && H <= kMaxSide / 2 && sizes_ok(B, IN, 2 * H) && tiles_ok(B, 2 * H);
 }
@@ -322,7 +437,8 @@ extern "C" {
 
 size_t dfp8_gated_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t H) {
     if (!gated_sizes_ok(B, IN, H) || B == 0 || H == 0) return 0;
-    return part_bytes(gated_plan(B, IN, H), B, 2 * H);
+    const GatedPlan p = gated_plan(B, IN, H);
+    return p.pitch ? size_t(B + 2 * H) * p.pitch : part_bytes(p, B, 2 * H);
 }
 
 int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const int32_t *eW, const float *bias, int act,
@@ -345,18 +461,26 @@ int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const in
     IONN_REQUIRE(need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need), IONN_ERR_WORKSPACE,
                  "dfp8_gated_fwd: needs a 16-byte aligned workspace of %zu bytes", need);
     const Epi ep{eX, eW, bias, nullptr, Z, Y, absmax_Y, act};
-    const Plan plan = gated_plan(B, IN, H);
+    const GatedPlan plan = gated_plan(B, IN, H);
     Product p = make_product(plan, X, IN, W, IN, ep, B, H, IN, workspace);
     const int64_t most = path_of(plan, X, W) == ROWS ? ceil_div(H, 16) : int64_t(p.blocks);
     IONN_REQUIRE(most <= max_groups(path_of(plan, X, W) == ROWS ? kRowWaves * 64 : NT), IONN_ERR_SHAPE,
                  "dfp8_gated_fwd: B=%lld H=%lld have too many tiles", (long long)B, (long long)H);
+    if (plan.pitch) {
+        Copier c(workspace);
+        p.A = c.add(X, B, IN);
+        p.B = c.add(W, 2 * H, IN);
+        p.lda = p.ldb = plan.pitch;
+        c.launch(as_stream(stream));
+    }
     with_dtype(dtype, [&](auto tag) { launch_gated<decltype(tag)>(plan, p, as_stream(stream)); });
     return check_launch("dfp8_gated_fwd");
 }
 
 size_t dfp8_gated_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t H) {
     if (!gated_sizes_ok(B, IN, H) || B == 0 || H == 0) return 0;
-    return error_bytes(B, H) + (IN > 0 ? backward_part_bytes(B, IN, 2 * H) : 0);
+    const BackwardPlan p = backward_plan(B, IN, H);
+    return error_bytes(B, H) + (IN > 0 ? backward_part_bytes(p.s) + p.copy_bytes() : 0);
 }
 
 int dfp8_gated_bwd(const void *dY, const void *Z, int act, int dtype, const int8_t *X, const int32_t *eX,
@@ -390,12 +514,19 @@ int dfp8_gated_bwd(const void *dY, const void *Z, int act, int dtype, const int8
         zero_bytes(gb, 8 * H, st);
         return check_launch("dfp8_gated_bwd");
     }
-    const BackwardProducts p{dZ8, X, W, edZ, eX, eW, dX, G, B, IN, 2 * H, static_cast<char *>(workspace) + error_bytes(B, H)};
+    const BackwardPlan plan = backward_plan(B, IN, H);
+    char *parts = static_cast<char *>(workspace) + error_bytes(B, H);
+    BackwardProducts p{dZ8, X, W, edZ, eX, eW, dX, G, plan.s, parts};
+    Copier copies(parts + (IN > 0 ? backward_part_bytes(plan.s) : 0));
+    if (plan.copy_Z && (dX || G)) p.dZ8 = copies.add(dZ8, B, 2 * H);
+    if (plan.copy_X && G) p.X = copies.add(X, B, IN);
+    if (plan.copy_W && dX) p.W = copies.add(W, 2 * H, IN);
     IONN_REQUIRE(IN == 0 || backward_launches(p), IONN_ERR_SHAPE,
                  "dfp8_gated_bwd: B=%lld IN=%lld H=%lld have too many tiles", (long long)B, (long long)IN, (long long)H);
     launch_errors(dY, Z, act, dtype, B, H, dZ8, edZ, gb, status_out, workspace, st);
     if (int rc = check_launch("dfp8_gated_bwd")) return rc;
     if (IN == 0) return IONN_OK;
+    copies.launch(st);
     launch_backward_products(p, dtype, st);
     return check_launch("dfp8_gated_bwd");
 }

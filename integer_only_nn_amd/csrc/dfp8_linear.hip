@@ -105,16 +105,18 @@ struct Pair {
     Plan pd, pg;
     Product d, g;
 };
+Plan plan_of_dX(const BackwardSizes &s) { return make_plan<true, false>(s.B, s.IN, s.OUT, false, s.ldz, s.ldw); }
+Plan plan_of_G(const BackwardSizes &s) { return make_plan<false, false>(s.OUT, s.IN, s.B, false, s.ldz, s.ldx); }
 Pair make_pair(const BackwardProducts &p) {
-    const int64_t B = p.B, IN = p.IN, OUT = p.OUT;
+    const int64_t B = p.s.B, IN = p.s.IN, OUT = p.s.OUT;
     Pair r;
-    r.pd = make_plan<true, false>(B, IN, OUT, false);
-    r.pg = make_plan<false, false>(OUT, IN, B, false);
+    r.pd = plan_of_dX(p.s);
+    r.pg = plan_of_G(p.s);
     const Epi ed{p.edZ, p.eW, nullptr, nullptr, nullptr, p.dX, nullptr, IONN_ACT_NONE};
     const Epi eg{p.edZ, p.eX, nullptr, nullptr, nullptr, p.G, nullptr, IONN_ACT_NONE};
     char *parts = static_cast<char *>(p.parts);
-    r.d = make_product(r.pd, p.dZ8, OUT, p.W, IN, ed, B, IN, OUT, parts);
-    r.g = make_product(r.pg, p.dZ8, OUT, p.X, IN, eg, OUT, IN, B, parts + part_bytes(r.pd, B, IN));
+    r.d = make_product(r.pd, p.dZ8, p.s.ldz, p.W, p.s.ldw, ed, B, IN, OUT, parts);
+    r.g = make_product(r.pg, p.dZ8, p.s.ldz, p.X, p.s.ldx, eg, OUT, IN, B, parts + part_bytes(r.pd, B, IN));
     if (!p.dX) r.d.blocks = 0;
     if (!p.G) r.g.blocks = 0;
     return r;
@@ -137,9 +139,13 @@ void zero_bytes(void *p, int64_t n, hipStream_t st) {
     zero_bytes_kernel<<<dim3(unsigned(b < 2048 ? b : 2048)), dim3(256), 0, st>>>(static_cast<uint8_t *>(p), n);
 }
 
-size_t backward_part_bytes(int64_t B, int64_t IN, int64_t OUT) {
-    return part_bytes(make_plan<true, false>(B, IN, OUT, false), B, IN) +
-           part_bytes(make_plan<false, false>(OUT, IN, B, false), OUT, IN);
+size_t backward_part_bytes(const BackwardSizes &s) {
+    return part_bytes(plan_of_dX(s), s.B, s.IN) + part_bytes(plan_of_G(s), s.OUT, s.IN);
+}
+
+void backward_plans(const BackwardSizes &s, Plan &dX, Plan &G) {
+    dX = plan_of_dX(s);
+    G = plan_of_G(s);
 }
 
 bool backward_launches(const BackwardProducts &p) {
@@ -203,7 +209,7 @@ int dfp8_linear_path(int product, int64_t B, int64_t IN, int64_t OUT) {
 size_t dfp8_linear_bwd_workspace_bytes(int64_t B, int64_t IN, int64_t OUT) {
     if (!sizes_ok(B, IN, OUT) || B == 0 || OUT == 0) return 0;
     size_t n = act_workspace_bytes(B, OUT);
-    if (IN > 0) n += backward_part_bytes(B, IN, OUT);
+    if (IN > 0) n += backward_part_bytes({B, IN, OUT, OUT, IN, IN});
     return n;
 }
 
@@ -240,7 +246,7 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype, const int
         zero_bytes(gb, OUT * 4, st);
         return check_launch("dfp8_linear_bwd");
     }
-    const BackwardProducts p{dZ8, X, W, edZ, eX, eW, dX, G, B, IN, OUT,
+    const BackwardProducts p{dZ8, X, W, edZ, eX, eW, dX, G, {B, IN, OUT, OUT, IN, IN},
                              static_cast<char *>(workspace) + act_workspace_bytes(B, OUT)};
     IONN_REQUIRE(IN == 0 || backward_launches(p), IONN_ERR_SHAPE,
                  "dfp8_linear_bwd: B=%lld IN=%lld OUT=%lld have too many tiles", (long long)B, (long long)IN,

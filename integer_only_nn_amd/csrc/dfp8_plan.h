@@ -30,15 +30,17 @@ struct Plan {
     int64_t tiles;
     int split;
     int rows, cols;  // ROWS: groups of 16 rows and of 16 outputs in a workgroup
+    double us;       // of tiles: the time that is expected
 };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // By the sizes alone (the workspace query knows no addresses); operands whose
-// address does not suit TILE256 and TILE128 take TILE.
+// address does not suit TILE256 and TILE128 take TILE.  a_pitch, b_pitch: bytes from
+// an operand's row to the next, 0 for rows that follow each other.
 template <bool A_KM, bool B_KM>
-Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
-    Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1, 0, 0};
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward, int64_t a_pitch = 0, int64_t b_pitch = 0) {
+    Plan p{TILE, ceil_div(M, 64) * ceil_div(N, 64), 1, 0, 0, 0.0};
     const int64_t a_side = A_KM ? K : M, b_side = B_KM ? K : N;  // contiguous
     // Straight into matrix operands: the smallest tile that a grid of one
     // workgroup per compute unit covers, for these products are bound by one
@@ -72,7 +74,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
         p.path = TINY;
         return p;
     }
-    const int64_t lda = a_side, ldb = b_side;
+    const int64_t lda = a_pitch ? a_pitch : a_side, ldb = b_pitch ? b_pitch : b_side;
     // The tile size that is expected to end first; in us, fitted to
     // measurements: a round of 256 x 256 tiles, one per compute unit, takes 23 (15
     // without an activation) and K / 110; 128 x 128 tiles, two at a time on a
@@ -81,15 +83,16 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool forward) {
     // 2048^3 22.5, 17.6 and 35; 2048 x 4096 x 4096 67, 42 and 54; 4096^3 128, 78
     // and 70.  With both gradients: 512^3 12, 19 and 35; 4096 x 1024 x 4096 110, 81
     // (74 in one grid) and 121.
+    const double k = double(K);
+    p.us = (forward ? 5.0 : 2.5) + double(M) * double(N) * k / 65536.0 / (forward ? 6800.0 : 6500.0);
     if (tile256_fits<A_KM, B_KM>(nullptr, lda, nullptr, ldb, M, N, K)) {
         const int64_t tiles256 = ceil_div(M, 256) * ceil_div(N, 256), tiles128 = ceil_div(M, 128) * ceil_div(N, 128);
-        const double rounds = double(ceil_div(tiles256, 256)), each = double(ceil_div(tiles128, 256)), k = double(K);
-        const double t64 = (forward ? 5.0 : 2.5) + double(M) * double(N) * k / 65536.0 / (forward ? 6800.0 : 6500.0);
+        const double rounds = double(ceil_div(tiles256, 256)), each = double(ceil_div(tiles128, 256));
         const double t128 = forward ? 3.5 + 2.6 * each + k * (0.0022 + 0.0031 * each)
                                     : 2.5 + 1.8 * each + k * (0.0018 + 0.0031 * each);
         const double t256 = rounds * ((forward ? 23.0 : 15.0) + k / 110.0);
-        if (t256 < t64 && t256 < t128) p.path = TILE256;
-        else if (t128 < t64) p.path = TILE128;
+        if (t256 < p.us && t256 < t128) p.path = TILE256, p.us = t256;
+        else if (t128 < p.us) p.path = TILE128, p.us = t128;
         if (p.path != TILE) return p;
     }
     // few tiles over a long reduction: ranges of at least four steps, about
@@ -145,14 +148,20 @@ inline bool tiles_ok(int64_t M, int64_t N) { return 2 * ceil_div(M, 64) * ceil_d
 // The two gradients' products of a backward pass (dfp8_linear.hip), from the
 // error dZ8, edZ that is in place: dX (nullable) [B][IN] and G (nullable)
 // [OUT][IN] of type dtype.  IN >= 1.
-size_t backward_part_bytes(int64_t B, int64_t IN, int64_t OUT);
+struct BackwardSizes {
+    int64_t B, IN, OUT;
+    int64_t ldz, ldx, ldw;  // bytes from a row of dZ8, X, W to the next
+};
+size_t backward_part_bytes(const BackwardSizes &s);
 struct BackwardProducts {
     const int8_t *dZ8, *X, *W;
     const int32_t *edZ, *eX, *eW;
     void *dX, *G;
-    int64_t B, IN, OUT;
-    void *parts;  // backward_part_bytes(B, IN, OUT) bytes, 16-byte aligned
+    BackwardSizes s;
+    void *parts;  // backward_part_bytes(s) bytes, 16-byte aligned
 };
+// How the two products are planned.
+void backward_plans(const BackwardSizes &s, Plan &dX, Plan &G);
 // Whether their launches are within what the runtime takes.
 bool backward_launches(const BackwardProducts &p);
 void launch_backward_products(const BackwardProducts &p, int dtype, hipStream_t st);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from integer_only_nn_amd import _lib, ops
-from test_gpu_dfp8_gated import WAYS
+from test_gpu_dfp8_gated import COPIES, WAYS
 
 lib = _lib.lib()
 OK, ARG, SHAPE, RANGE, ALIGN, UNSUP, HIP, WS = range(8)
@@ -22,6 +22,16 @@ def test_sizes_take_their_ways(B, IN, H):
 def test_every_way_is_taken():
     assert set(WAYS.values()) == {"rows", "tiles 256", "tiles 128", "tiles", "narrow"}
     assert ops.dfp8_gated_fwd_workspace_bytes(300, 9001, 300) > 0  # ranges of the reduction
+
+
+@pytest.mark.parametrize("B,IN,H", list(COPIES))
+def test_sizes_whose_rows_are_copied(B, IN, H):
+    whole = lambda n: (n + 15) // 16 * 16  # noqa: E731
+    size = {"Z": B * whole(2 * H), "X": B * whole(IN), "W": 2 * H * whole(IN)}
+    fwd, bwd = COPIES[B, IN, H]
+    assert ops.dfp8_gated_fwd_workspace_bytes(B, IN, H) == sum(size[t] for t in fwd)
+    errors = ops.dfp8_gated_bwd_workspace_bytes(B, 0, H)
+    assert ops.dfp8_gated_bwd_workspace_bytes(B, IN, H) - errors == sum(size[t] for t in bwd)
 
 
 def test_fwd():

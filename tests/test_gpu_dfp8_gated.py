@@ -34,6 +34,13 @@ WAYS = {
     (4096, 4096, 2048): "tiles 256", (4090, 2064, 2041): "tiles 256", (3901, 4080, 1929): "tiles 256",
 }
 
+# (B, IN, H) whose rows are not whole 16-byte pieces -> the tensors copied for larger tiles: forward, backward
+COPIES = {
+    (2043, 2027, 1011): ("XW", "ZXW"), (4090, 2063, 2041): ("XW", "ZXW"), (700, 4001, 2000): ("XW", "XW"),
+    (1222, 2803, 533): ("", "ZXW"), (2048, 2032, 1017): ("", "Z"), (1470, 1249, 1592): ("", "X"), (4335, 823, 952): ("XW", "W"),
+    (300, 4095, 8192): ("XW", ""), (8192, 1000, 2000): ("XW", "XW"), (2048, 1000, 1020): ("", ""), (1024, 2050, 2050): ("", ""),
+}
+
 
 def _case(B, IN, H, bias=True, seed=0):
     rng = np.random.default_rng(seed + 7 * B + 3 * IN + H)
@@ -81,6 +88,12 @@ def test_forward(B, IN, H, name):
         _check_forward(_case(B, IN, H, bias=i != 1), kind, name, save_z=i != 2, absmax=i != 3)
 
 
+@pytest.mark.parametrize("B,IN,H", [s for s, c in COPIES.items() if c[0] and s[0] < 4096])
+@pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "silu"), ("f16", "gelu")])
+def test_forward_of_copied_rows(B, IN, H, name, kind):
+    _check_forward(_case(B, IN, H, bias=name != "f16"), kind, name, save_z=name != "bf16")
+
+
 def test_forward_empty_sizes():
     _check_forward(_case(4, 0, 6), "gelu", "f32")  # IN = 0: z = bias
     for B, H in ((0, 6), (4, 0)):
@@ -104,7 +117,8 @@ def test_forward_not_finite_values_stay_in_their_place():
         assert int(host(top)[0]) & 0x7fffffff > 0x7f800000  # a NaN counts above every number
 
 
-@pytest.mark.parametrize("B,IN,H", [(70, 256, 256), (2041, 2032, 1016), (4090, 2064, 2041), (1001, 1023, 1025), (300, 9001, 300)])
+@pytest.mark.parametrize("B,IN,H", [(70, 256, 256), (2041, 2032, 1016), (4090, 2064, 2041), (1001, 1023, 1025), (300, 9001, 300),
+                                    (2043, 2027, 1011)])
 def test_operands_that_start_anywhere(B, IN, H):
     d = _case(B, IN, H)
     want = _forward(d, "silu", "f16")[0]
@@ -188,6 +202,39 @@ def test_backward(B, IN, H, name):
 @pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "silu"), ("f16", "gelu")])
 def test_backward_larger(B, IN, H, name, kind):
     _check_backward(_backward(B, IN, H, kind, name), kind, name)
+
+
+@pytest.mark.parametrize("B,IN,H", [s for s, c in COPIES.items() if c[1] and s[0] < 8192])
+@pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "silu"), ("f16", "gelu_tanh")])
+def test_backward_of_copied_rows(B, IN, H, name, kind):
+    _check_backward(_backward(B, IN, H, kind, name), kind, name)
+
+
+@pytest.mark.parametrize("B,IN,H", [(2043, 2027, 1011), (2048, 2032, 1017), (4335, 823, 952)])
+def test_copied_rows_one_gradient_and_any_workspace(B, IN, H):
+    """dX or G alone; nothing depends on what the workspace held, and nothing behind it is written."""
+    g = torch.Generator(device=dev()).manual_seed(5)
+    ints = lambda *s: torch.randint(-128, 128, s, dtype=torch.int8, device=dev(), generator=g)  # noqa: E731
+    X, W = ints(B, IN), ints(2 * H, IN)
+    dY, Z = (torch.randn(B, n, device=dev(), generator=g).bfloat16() for n in (H, 2 * H))
+    need = {"bwd": ops.dfp8_gated_bwd_workspace_bytes(B, IN, H), "fwd": ops.dfp8_gated_fwd_workspace_bytes(B, IN, H)}
+
+    def run(names, byte):
+        ws = torch.full((max(need.values()) + 64,), byte, dtype=torch.uint8, device=dev())
+        out = {k: torch.full(s, 7.0, dtype=torch.bfloat16, device=dev()) for k, s in
+               (("Y", (B, H)), ("dX", (B, IN)), ("G", (2 * H, IN))) if k in names}
+        q, e = torch.empty(B, 2 * H, dtype=torch.int8, device=dev()), _e(0)
+        say("copied rows", B, IN, H, names)
+        if "Y" in names:
+            ops.dfp8_gated_fwd(X, _e(-6), W, _e(-12), out["Y"], workspace=ws[:need["fwd"]])
+            assert (ws[need["fwd"]:] == byte).all()
+        ops.dfp8_gated_bwd(dY, Z, "silu", X, _e(-6), W, _e(-12), q, e, dX=out.get("dX"), G=out.get("G"), workspace=ws[:need["bwd"]])
+        assert (ws[max(need.values()):] == byte).all()
+        return out
+    want = run(("Y", "dX", "G"), 0)
+    for names, byte in ((("dX",), 0xff), (("G",), 0x7f), (("Y", "dX", "G"), 0x80)):
+        for k, v in run(names, byte).items():
+            assert torch.equal(v, want[k]), k
 
 
 def test_backward_outputs_are_optional():
