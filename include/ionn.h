@@ -769,7 +769,8 @@ int dfp8_linear_bwd(const void *dY, const void *Z, int act, int dtype,
  * Z (nullable): dtype [B][2 H], receives z for the backward pass (apart from Y).
  * absmax_Y and the rest as in dfp8_linear_fwd with OUT = 2 H: H in [0, 2^29],
  * 0 <= IN <= IONN_DFP8_MAX_REDUCTION.  workspace: 16-byte aligned,
- * dfp8_gated_fwd_workspace_bytes(B, IN, H) bytes (may be 0). */
+ * dfp8_gated_fwd_workspace_bytes(B, IN, H) bytes (may be 0; of large products
+ * whose rows are not whole 16-byte pieces, X and W once more). */
 size_t dfp8_gated_fwd_workspace_bytes(int64_t B, int64_t IN, int64_t H);
 int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W,
                    const int32_t *eW, const float *bias, int act, void *Z,

@@ -47,14 +47,30 @@ __device__ __forceinline__ void put_vec(T *p, const float (&x)[VE], int valid, b
     __builtin_nontemporal_store(v, reinterpret_cast<typename Vec<T, VE>::loose *>(p));
 }
 
-// Sums of v over the TPR threads that share a row (whole wavefronts); every one
-// of them gets them.  buf: the wavefronts' sums, twice over, so that one barrier
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// The sum over an aligned group of N lanes, in each of them.
+template <int N>
+__device__ __forceinline__ float group_sum(float v) {
+    v += moved<0xb1>(v);   // lane ^ 1
+    v += moved<0x4e>(v);   // lane ^ 2
+    v += moved<0x141>(v);  // the other four of eight
+    if (N >= 16) v += moved<0x140>(v);  // the other eight of sixteen
+    if (N >= 32) v += __shfl_xor(v, 16, 64);
+    if (N >= 64) v += __shfl_xor(v, 32, 64);
+    return v;
+}
+
+// Sums of v over the TPR threads that share a row (a part of a wavefront, or whole
+// ones); every one of them gets them.  buf: the wavefronts' sums, twice over, so that one barrier
 // per call suffices (ph alternates).
 template <int TPR, int V>
 __device__ __forceinline__ void row_sums(float (&v)[V], float (*buf)[V][TPR / 64 + 1], int &ph) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = wave_sum(v[k]);
-    if (TPR == 64) return;
+    for (int k = 0; k < V; ++k) v[k] = group_sum<(TPR < 64 ? TPR : 64)>(v[k]);
+    if (TPR <= 64) return;
     float(*b)[TPR / 64 + 1] = buf[ph];
     ph ^= 1;
     if ((threadIdx.x & 63) == 0) {
@@ -137,7 +153,15 @@ __device__ __forceinline__ void normalise(float (&v)[NV][VE], int kind, float ep
         for (int e = 0; e < VE; ++e) v[i][e] *= rstd;
 }
 
-constexpr int fwd_threads(int tpr) { return tpr == 64 ? 256 : tpr; }
+constexpr int fwd_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
+
+// The row of this thread among a workgroup's (scalar where a wavefront has one row, so
+// that addresses are but for the column).
+template <int TPR>
+__device__ __forceinline__ int row_group() {
+    const int g = int(threadIdx.x) / TPR;
+    return TPR < 64 ? g : __builtin_amdgcn_readfirstlane(g);
+}
 
 template <class T, int VE, int TPR, int NV>
 __global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(Forward f) {
@@ -149,8 +173,7 @@ __global__ __launch_bounds__(fwd_threads(TPR)) void residual_norm_fwd_kernel(For
     T *y = static_cast<T *>(f.y), *n = static_cast<T *>(f.n);
     const int t = threadIdx.x % TPR, cols = f.cols;
     const int64_t step = int64_t(gridDim.x) * kRows;
-    // (a wavefront has one row: addresses are scalar but for the column)
-    int64_t r = int64_t(blockIdx.x) * kRows + __builtin_amdgcn_readfirstlane(int(threadIdx.x) / TPR);
+    int64_t r = int64_t(blockIdx.x) * kRows + row_group<TPR>();
     int ph = 0;
     uint32_t top = 0;
     typename Vec<T, VE>::type ra[NV], rx[NV];
@@ -253,7 +276,7 @@ struct Backward {
     bool stream;
 };
 
-constexpr int bwd_threads(int tpr) { return tpr == 64 ? 512 : tpr; }
+constexpr int bwd_threads(int tpr) { return tpr <= 64 ? 512 : tpr; }
 
 // h := the normalised rows of v (zeros past the end).
 template <class T, int VE, int TPR, int NV>
@@ -290,18 +313,20 @@ __device__ __forceinline__ void project(float (&d)[NV][VE], const float (&h)[NV]
 
 // WHOLE: a unit is a gate's rows, taken by one of a workgroup's row groups.  SHIFT:
 // one of the norms is a layer norm, so that the sums S1 and dbeta_y are needed
-// (without their registers two workgroups of 512 threads share a compute unit).
+// (without their registers two workgroups of 512 threads share a compute unit;
+// two vectors a thread do not fit that many registers: 8192 x 4096 float32, layer
+// norms, 173 us, and 280 where they are made to).
 template <class T, int VE, int TPR, int NV, bool WHOLE, bool SHIFT>
-__global__ __launch_bounds__(bwd_threads(TPR), NV * VE <= 8 && !(WHOLE && SHIFT) ? 4 : 1) void residual_norm_bwd_kernel(Backward b) {
+__global__ __launch_bounds__(bwd_threads(TPR), NV == 1 && !(WHOLE && SHIFT) ? 4 : 1) void residual_norm_bwd_kernel(Backward b) {
     constexpr int kRows = bwd_threads(TPR) / TPR;
     typedef Cols<VE, TPR, NV> Vector;
     __shared__ float buf[2][SHIFT ? 2 : 1][TPR / 64 + 1];
-    __shared__ float fold[kRows > 1 ? kRows * NV * VE * TPR : 1];
+    constexpr int kFolds = TPR < 64 ? bwd_threads(TPR) / 64 : kRows;  // rows of sums that a workgroup folds
+    __shared__ float fold[kFolds > 1 ? kFolds * NV * VE * TPR : 1];
     const T *dy = static_cast<const T *>(b.dy), *dn = static_cast<const T *>(b.dn);
     const T *a = static_cast<const T *>(b.a), *y = static_cast<const T *>(b.y);
     T *da = static_cast<T *>(b.da), *dx = static_cast<T *>(b.dx);
-    // (a wavefront has one row: addresses are scalar but for the column)
-    const int t = threadIdx.x % TPR, rg = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / TPR), cols = b.cols;
+    const int t = threadIdx.x % TPR, rg = row_group<TPR>(), cols = b.cols;
     const float n = float(cols);
     int ph = 0;
     // S: Sh, S1 of the run at hand; Y: dgamma_y, dbeta_y of all runs; A (WHOLE): dgamma_a, dbeta_a of all runs
@@ -315,16 +340,24 @@ __global__ __launch_bounds__(bwd_threads(TPR), NV * VE <= 8 && !(WHOLE && SHIFT)
 #pragma unroll
             for (int e = 0; e < VE; ++e) Y[k].v[i][e] = A[WHOLE ? k : 0].v[i][e] = 0.0f;
 
-    // the row groups of a workgroup one after the other, to two rows of partial sums
+    // the row groups of a workgroup (those of a wavefront first) one after the other, to two rows of partial sums
     const auto leave = [&](Vector *s, float *to) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < kSums; ++k) {
-            if (kRows > 1) {
+            if (kFolds > 1) {
+                const int at = TPR < 64 ? int(threadIdx.x) >> 6 : rg;
+#pragma unroll
+                for (int off = TPR; off < 64; off <<= 1)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) s[k].v[i][e] += __shfl_xor(s[k].v[i][e], off, 64);
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) fold[((rg * NV + i) * VE + e) * TPR + t] = s[k].v[i][e];
+                    for (int e = 0; e < VE; ++e)
+                        if (TPR >= 64 || (threadIdx.x & 63) < TPR) fold[((at * NV + i) * VE + e) * TPR + t] = s[k].v[i][e];
                 __syncthreads();
             }
             if (rg > 0) continue;
@@ -336,7 +369,7 @@ __global__ __launch_bounds__(bwd_threads(TPR), NV * VE <= 8 && !(WHOLE && SHIFT)
                 for (int e = 0; e < VE; ++e) {
                     o[e] = s[k].v[i][e];
 #pragma unroll
-                    for (int g = 1; g < kRows; ++g) o[e] += fold[((g * NV + i) * VE + e) * TPR + t];
+                    for (int g = 1; g < kFolds; ++g) o[e] += fold[((g * NV + i) * VE + e) * TPR + t];
                 }
                 if (c < cols) store_vec<float, VE>(to + int64_t(k) * cols + c, o, cols - c);
             }
@@ -568,20 +601,30 @@ __global__ __launch_bounds__(kSumCols *kSumGroups) void residual_norm_sum_kernel
     }
 }
 
-// f(threads per row, vectors per thread) for a row of cols columns: one wavefront
-// per row while that takes few vectors a lane (no barrier), then the fewest
-// threads that hold it in eight columns each.
-template <int VE, bool BWD, class F>
+// f(columns of a vector, threads per row, vectors per thread) for a row of cols columns: a part of a
+// wavefront for short rows (32768 x 64 bfloat16 forward 9 us, in a wavefront a row 30;
+// 25088 x 256 12 and 26), one while that takes few vectors a lane (no barrier), then the
+// fewest threads that hold it in eight columns each.  Backward, short rows of 16-bit
+// types are held in four columns each, for eight and the vectors' sums are more than
+// the registers of two workgroups on a compute unit (32768 x 64 12.7 against 19.5 us).
+template <class T, bool BWD, class F>
 void with_shape(int64_t cols, F &&f) {
-    const int64_t v = (cols + VE - 1) / VE;
+    constexpr int VE = 16 / sizeof(T), kShort = BWD ? 4 : VE;
     constexpr bool kWide = VE == 8 && !BWD;
-    if (v <= 64) f(IntC<64>{}, IntC<1>{});
-    else if (v <= 128) f(IntC<kWide ? 128 : 64>{}, IntC<kWide ? 1 : 2>{});
-    else if (v <= 256) f(IntC<256>{}, IntC<1>{});
-    else if (v <= 512) f(IntC<VE == 8 ? 512 : 256>{}, IntC<VE == 8 ? 1 : 2>{});
-    else if (v <= 1024) f(IntC<VE == 8 ? 1024 : 512>{}, IntC<VE == 8 ? 1 : 2>{});
-    else if (v <= 2048) f(IntC<1024>{}, IntC<2>{});
-    else if constexpr (VE == 4) f(IntC<1024>{}, IntC<4>{});
+    const IntC<VE> ve;
+    const IntC<kShort> few;
+    const int64_t v = (cols + VE - 1) / VE, s = (cols + kShort - 1) / kShort;
+    if (s <= 8) return f(few, IntC<8>{}, IntC<1>{});
+    if (s <= 16) return f(few, IntC<16>{}, IntC<1>{});
+    if (s <= 32) return f(few, IntC<32>{}, IntC<1>{});
+    if (s <= 64) return f(few, IntC<64>{}, IntC<1>{});
+    if (v <= 64) return f(ve, IntC<64>{}, IntC<1>{});
+    if (v <= 128) return f(ve, IntC<kWide ? 128 : 64>{}, IntC<kWide ? 1 : 2>{});
+    if (v <= 256) return f(ve, IntC<256>{}, IntC<1>{});
+    if (v <= 512) return f(ve, IntC<VE == 8 ? 512 : 256>{}, IntC<VE == 8 ? 1 : 2>{});
+    if (v <= 1024) return f(ve, IntC<VE == 8 ? 1024 : 512>{}, IntC<VE == 8 ? 1 : 2>{});
+    if (v <= 2048) return f(ve, IntC<1024>{}, IntC<2>{});
+    if constexpr (VE == 4) f(ve, IntC<1024>{}, IntC<4>{});
 }
 
 // How the rows are cut for the backward pass.
@@ -658,9 +701,8 @@ int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a, const float
                     gate, rows, uint32_t(share), int(cols), float(alpha), float(eps), absmax_n, bytes >= kStreamBytes};
     with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
-        constexpr int VE = 16 / sizeof(T);
-        with_shape<VE, false>(cols, [&](auto tpr, auto nv) {
-            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = fwd_threads(TPR);
+        with_shape<T, false>(cols, [&](auto ve, auto tpr, auto nv) {
+            constexpr int VE = decltype(ve)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = fwd_threads(TPR);
             // as many workgroups as are resident at once: rows are dealt out evenly
             int64_t blocks = (rows + kBlock / TPR - 1) / (kBlock / TPR);
             const int64_t most = int64_t(device_cus()) * (kBlock < 1024 ? 1024 / kBlock : 1);
@@ -742,9 +784,8 @@ int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a, const 
                          part_a, part_y, dgate, bytes >= kStreamBytes};
         with_dtype(dtype, [&](auto tag) {
             using T = decltype(tag);
-            constexpr int VE = 16 / sizeof(T);
-            with_shape<VE, true>(cols, [&](auto tpr, auto nv) {
-                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = bwd_threads(TPR);
+            with_shape<T, true>(cols, [&](auto ve, auto tpr, auto nv) {
+                constexpr int VE = decltype(ve)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = bwd_threads(TPR);
                 const int64_t each = runs.whole() ? kBlock / TPR : 1;
                 blocks = (runs.units() + each - 1) / each;
                 if (blocks > kMaxGroups) blocks = kMaxGroups;

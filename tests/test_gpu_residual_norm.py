@@ -133,6 +133,19 @@ def test_forward(rows, cols, name):
         _check_forward(_case(rows, cols, name, ka, ky, gate_rows, alpha=(1.0, 0.5, -2.0)[i % 3]), name)
 
 
+# several rows in a wavefront: parts of 8, 16 and 32 threads, gates that end among a wavefront's rows, more
+# gates than workgroups, rows behind the last that fill no part, a second round of rows
+SHORT = [(1, 2, 0), (77, 5, 3), (1003, 31, 5), (1003, 33, 1), (700, 63, 300), (700, 65, 0), (130, 127, 7), (2001, 129, 2),
+         (61, 255, 60), (40000, 24, 600), (40000, 9, 70)]
+
+
+@pytest.mark.parametrize("rows,cols,gate_rows", SHORT)
+@pytest.mark.parametrize("name", list(TYPES))
+def test_forward_of_short_rows(rows, cols, gate_rows, name):
+    for ka, ky in (("layer", "rms"), ("rms", "layer"), ("none", "rms")):
+        _check_forward(_case(rows, cols, name, ka, ky, gate_rows or None, alpha=0.5), name)
+
+
 @pytest.mark.parametrize("name", list(TYPES))
 def test_forward_of_the_first_norm(name):
     """No block yet: the norm of the stream alone."""
@@ -307,6 +320,13 @@ def test_backward(rows, cols, name):
         d = _errors(_case(rows, cols, name, ka, ky, gate_rows, alpha=(1.0, 0.5, -2.0)[i % 3]), name,
                     dy=ky == "none" or i % 2 == 0)
         _check_backward(d, name)
+
+
+@pytest.mark.parametrize("rows,cols,gate_rows", SHORT)
+@pytest.mark.parametrize("name", list(TYPES))
+def test_backward_of_short_rows(rows, cols, gate_rows, name):
+    for ka, ky in (("layer", "rms"), ("rms", "rms"), ("none", "layer")):
+        _check_backward(_errors(_case(rows, cols, name, ka, ky, gate_rows or None, alpha=0.5), name), name)
 
 
 # a gate for few rows: more gates than workgroups, whole ones in a row group each; many runs of a few gates
