@@ -303,7 +303,7 @@ def test_repeatable_and_on_another_stream():
     assert torch.equal(Y, want)
 
 
-@pytest.mark.parametrize("B,IN,H", [(16, 300, 100), (2048, 2048, 1024), (300, 9001, 300)])
+@pytest.mark.parametrize("B,IN,H", [(16, 300, 100), (2048, 2048, 1024), (300, 9001, 300), (2043, 2027, 1011)])
 def test_captured_and_replayed(B, IN, H):
     g = torch.Generator(device=dev()).manual_seed(5)
     ints = lambda *s: torch.randint(-128, 128, s, device=dev(), generator=g, dtype=torch.int8)  # noqa: E731
