@@ -6,7 +6,7 @@ import itertools
 import numpy as np
 import pytest
 
-from integer_only_nn_amd import _lib
+from integer_only_nn_amd import _lib, ops
 from oracle import floats as of
 
 lib = _lib.lib()
@@ -88,3 +88,11 @@ def test_oracle_gradient_against_differences(ka, ky):
             diff = (loss({**d, k: hi}) - loss({**d, k: lo})) / (2 * h)
             # third derivatives of rows of deviation 0.3 and more: below 1000 times the terms
             assert abs(diff - g[name][at]) <= scale * 1000 * h * h, (k, at)
+
+
+def test_workspace_serves_a_call_without_a_gate():
+    """gate_rows does not count without a gate, whatever the workspace was asked for with."""
+    for rows, cols in ((1, 5), (300, 64), (8192, 700), (40000, 24)):
+        for gate_rows in (1, 3, 70, 299, 300, 8000, 50000):
+            assert (ops.ionn_residual_norm_bwd_workspace_bytes(rows, cols, gate_rows)
+                    >= ops.ionn_residual_norm_bwd_workspace_bytes(rows, cols))
