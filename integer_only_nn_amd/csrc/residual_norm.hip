@@ -604,7 +604,9 @@ __global__ __launch_bounds__(kSumCols *kSumGroups) void residual_norm_sum_kernel
 // f(columns of a vector, threads per row, vectors per thread) for a row of cols columns: a part of a
 // wavefront for short rows (32768 x 64 bfloat16 forward 9 us, in a wavefront a row 30;
 // 25088 x 256 12 and 26), one while that takes few vectors a lane (no barrier), then the
-// fewest threads that hold it in eight columns each.  Backward, short rows of 16-bit
+// fewest wavefronts, of some numbers, that hold it in eight columns each (4096 x 5120
+// bfloat16 in 640 threads a row 49 us forward and 57 backward, in 1024 59 and 74; 8192 x
+// 2560 in 320 53 and 48, in 512 53 and 53).  Backward, short rows of 16-bit
 // types are held in four columns each, for eight and the vectors' sums are more than
 // the registers of two workgroups on a compute unit (32768 x 64 12.7 against 19.5 us).
 template <class T, bool BWD, class F>
@@ -620,8 +622,19 @@ void with_shape(int64_t cols, F &&f) {
     if (s <= 64) return f(few, IntC<64>{}, IntC<1>{});
     if (v <= 64) return f(ve, IntC<64>{}, IntC<1>{});
     if (v <= 128) return f(ve, IntC<kWide ? 128 : 64>{}, IntC<kWide ? 1 : 2>{});
+    if constexpr (kWide) {
+        if (v <= 192) return f(ve, IntC<192>{}, IntC<1>{});
+    }
     if (v <= 256) return f(ve, IntC<256>{}, IntC<1>{});
+    if constexpr (VE == 8) {
+        if (v <= 320) return f(ve, IntC<320>{}, IntC<1>{});
+        if (v <= 384) return f(ve, IntC<384>{}, IntC<1>{});
+    }
     if (v <= 512) return f(ve, IntC<VE == 8 ? 512 : 256>{}, IntC<VE == 8 ? 1 : 2>{});
+    if constexpr (VE == 8) {
+        if (v <= 640) return f(ve, IntC<640>{}, IntC<1>{});
+        if (v <= 768) return f(ve, IntC<768>{}, IntC<1>{});
+    }
     if (v <= 1024) return f(ve, IntC<VE == 8 ? 1024 : 512>{}, IntC<VE == 8 ? 1 : 2>{});
     if (v <= 2048) return f(ve, IntC<1024>{}, IntC<2>{});
     if constexpr (VE == 4) f(ve, IntC<1024>{}, IntC<4>{});

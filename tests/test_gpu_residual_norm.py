@@ -146,6 +146,19 @@ def test_forward_of_short_rows(rows, cols, gate_rows, name):
         _check_forward(_case(rows, cols, name, ka, ky, gate_rows or None, alpha=0.5), name)
 
 
+# rows of three, five, six, ten and twelve wavefronts, full and not (16-bit types)
+WIDE = [(70, 1500, 9), (70, 2560, 70), (33, 2300, 1), (20, 3000, 7), (600, 5120, 1), (40, 5000, 0), (9, 6000, 2), (6, 6144, 6)]
+
+
+@pytest.mark.parametrize("rows,cols,gate_rows", WIDE)
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_rows_of_some_wavefronts(rows, cols, gate_rows, name):
+    for ka, ky in (("layer", "rms"), ("rms", "layer"), ("rms", "rms")):
+        d = _case(rows, cols, name, ka, ky, gate_rows or None, alpha=0.5)
+        _check_forward(d, name)
+        _check_backward(_errors(d, name), name)
+
+
 @pytest.mark.parametrize("name", list(TYPES))
 def test_forward_of_the_first_norm(name):
     """No block yet: the norm of the stream alone."""
