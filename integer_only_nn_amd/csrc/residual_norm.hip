@@ -15,7 +15,7 @@
 // (forward), a, y, dy and dn read and da and dx written once (backward), and HBM
 // bounds both.  A row lies in registers, up to eight columns a thread, and the
 // next row's loads are in flight while a row's sums are taken.  Measured: forward 8192
-// x 4096 bf16 51 us (5.2 TB/s, a large copy reaches 5.1); backward 84 us in the first
+// x 4096 bf16 48 us (5.6 TB/s, a large copy reaches 5.1); backward 84 us in the first
 // pass (4.8 TB/s) and 8 in the second; 25088 x 256 float32 with 128 gates 28 and 5.
 //
 // The backward pass needs only four column sums for its five vectors: S1 = sum t
