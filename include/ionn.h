@@ -876,10 +876,11 @@ int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a,
  *   dgamma_y[c] = sum_r dn * h_y,        dbeta_y[c] = sum_r dn
  * y: as the forward stored it; the statistics: as it left them.  Every output is
  * nullable; da and dx may be dy, dn, a or y, but not each other.  The vectors'
- * gradients are float32, summed in an order that the sizes fix (0 for rows = 0);
- * beta_a is read for dgate.  workspace: 16-byte aligned,
- * ionn_residual_norm_bwd_workspace_bytes(rows, cols, gate_rows) bytes (needed
- * where a vector's gradient is asked for; gate_rows = 0 without a gate). */
+ * gradients are float32, summed in an order that the sizes fix (rows = 0: zeros,
+ * dgate's for the one gate of all rows); beta_a is read for dgate.  workspace:
+ * 16-byte aligned, ionn_residual_norm_bwd_workspace_bytes(rows, cols, gate_rows)
+ * bytes (needed where a vector's gradient is asked for; gate_rows = 0 without a
+ * gate). */
 size_t ionn_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t cols,
                                               int64_t gate_rows);
 int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a,

@@ -131,13 +131,13 @@ __global__ void zero_bytes_kernel(uint8_t *p, int64_t n) {
 
 }  // namespace
 
-namespace dfp8 {
-
 void zero_bytes(void *p, int64_t n, hipStream_t st) {
     if (p == nullptr || n <= 0) return;
     const int64_t b = (n + 255) / 256;
     zero_bytes_kernel<<<dim3(unsigned(b < 2048 ? b : 2048)), dim3(256), 0, st>>>(static_cast<uint8_t *>(p), n);
 }
+
+namespace dfp8 {
 
 size_t backward_part_bytes(const BackwardSizes &s) {
     return part_bytes(plan_of_dX(s), s.B, s.IN) + part_bytes(plan_of_G(s), s.OUT, s.IN);

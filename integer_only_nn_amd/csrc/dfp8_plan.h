@@ -166,8 +166,5 @@ void backward_plans(const BackwardSizes &s, Plan &dX, Plan &G);
 bool backward_launches(const BackwardProducts &p);
 void launch_backward_products(const BackwardProducts &p, int dtype, hipStream_t st);
 
-// Zeros to n bytes at p (nullable).
-void zero_bytes(void *p, int64_t n, hipStream_t st);
-
 }  // namespace dfp8
 }  // namespace ionn

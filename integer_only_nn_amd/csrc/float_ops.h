@@ -20,6 +20,10 @@ inline size_t dtype_size(int dtype) { return dtype == IONN_F32 ? 4 : 2; }
 // larger ones without a word and runs the rest of their division by 2^32.
 constexpr int64_t max_groups(int threads) { return int64_t(0xffffffffu) / threads; }
 
+// Zeros to n bytes at p (nullable): the gradients of an empty batch, and of an
+// empty layer (dfp8_linear.hip).
+void zero_bytes(void *p, int64_t n, hipStream_t st);
+
 // Calls f with a value of the element type of `dtype` (checked before).
 template <class F>
 inline void with_dtype(int dtype, F &&f) {

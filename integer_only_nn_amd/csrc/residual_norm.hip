@@ -796,38 +796,40 @@ int ionn_residual_norm_bwd(const void *dy, const void *dn, const void *a, const 
     IONN_REQUIRE(!(sums_a || sums_y) || need == 0 || (workspace && aligned(workspace, 16) && workspace_bytes >= need),
                  IONN_ERR_WORKSPACE, "ionn_residual_norm_bwd: needs a 16-byte aligned workspace of %zu bytes", need);
     hipStream_t st = as_stream(stream);
-    const Runs runs = some ? runs_of(rows, cols, share) : Runs{0, 0, 0, 0};
+    if (!some) {  // (no rows: one gate of all of them)
+        for (float *v : {dgamma_a, dbeta_a, dgate, dgamma_y, dbeta_y}) zero_bytes(v, cols * 4, st);
+        return check_launch("ionn_residual_norm_bwd");
+    }
+    const Runs runs = runs_of(rows, cols, share);
     int64_t blocks = 0;
     float *part_a = sums_a ? static_cast<float *>(workspace) : nullptr;
     float *part_y = nullptr;
-    if (some) {
-        if (sums_y)
-            part_y = static_cast<float *>(workspace) + size_t(runs.whole() ? uint32_t(kMaxGroups) : runs.units()) * 2 * cols;
-        const Backward b{dy, dn, a, y, da, dx,
-                         {norm_a, gamma_a, beta_a, const_cast<float *>(mean_a), const_cast<float *>(rstd_a)},
-                         {norm_y, gamma_y, nullptr, const_cast<float *>(mean_y), const_cast<float *>(rstd_y)},
-                         gate, rows, uint32_t(share), runs.chunks, runs.chunk_rows, runs.units(), int(cols), float(alpha),
-                         part_a, part_y, dgate, bytes >= kStreamBytes};
-        with_dtype(dtype, [&](auto tag) {
-            using T = decltype(tag);
-            with_shape<T, true>(cols, [&](auto ve, auto tpr, auto nv) {
-                constexpr int VE = decltype(ve)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = bwd_threads(TPR);
-                const int64_t each = runs.whole() ? kBlock / TPR : 1;
-                blocks = (runs.units() + each - 1) / each;
-                if (blocks > kMaxGroups) blocks = kMaxGroups;
-                const dim3 grid{unsigned(blocks)}, block{unsigned(kBlock)};
-                const auto launch = [&](auto whole, auto shift) {
-                    residual_norm_bwd_kernel<T, VE, TPR, NV, decltype(whole)::value, decltype(shift)::value>
-                        <<<grid, block, 0, st>>>(b);
-                };
-                const bool shift = norm_a == IONN_NORM_LAYER || norm_y == IONN_NORM_LAYER;
-                if (runs.whole()) shift ? launch(IntC<1>{}, IntC<1>{}) : launch(IntC<1>{}, IntC<0>{});
-                else shift ? launch(IntC<0>{}, IntC<1>{}) : launch(IntC<0>{}, IntC<0>{});
-            });
+    if (sums_y)
+        part_y = static_cast<float *>(workspace) + size_t(runs.whole() ? uint32_t(kMaxGroups) : runs.units()) * 2 * cols;
+    const Backward b{dy, dn, a, y, da, dx,
+                     {norm_a, gamma_a, beta_a, const_cast<float *>(mean_a), const_cast<float *>(rstd_a)},
+                     {norm_y, gamma_y, nullptr, const_cast<float *>(mean_y), const_cast<float *>(rstd_y)},
+                     gate, rows, uint32_t(share), runs.chunks, runs.chunk_rows, runs.units(), int(cols), float(alpha),
+                     part_a, part_y, dgate, bytes >= kStreamBytes};
+    with_dtype(dtype, [&](auto tag) {
+        using T = decltype(tag);
+        with_shape<T, true>(cols, [&](auto ve, auto tpr, auto nv) {
+            constexpr int VE = decltype(ve)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value, kBlock = bwd_threads(TPR);
+            const int64_t each = runs.whole() ? kBlock / TPR : 1;
+            blocks = (runs.units() + each - 1) / each;
+            if (blocks > kMaxGroups) blocks = kMaxGroups;
+            const dim3 grid{unsigned(blocks)}, block{unsigned(kBlock)};
+            const auto launch = [&](auto whole, auto shift) {
+                residual_norm_bwd_kernel<T, VE, TPR, NV, decltype(whole)::value, decltype(shift)::value>
+                    <<<grid, block, 0, st>>>(b);
+            };
+            const bool shift = norm_a == IONN_NORM_LAYER || norm_y == IONN_NORM_LAYER;
+            if (runs.whole()) shift ? launch(IntC<1>{}, IntC<1>{}) : launch(IntC<1>{}, IntC<0>{});
+            else shift ? launch(IntC<0>{}, IntC<1>{}) : launch(IntC<0>{}, IntC<0>{});
         });
-        if (int rc = check_launch("ionn_residual_norm_bwd")) return rc;
-    }
-    if (sums_a || sums_y) {  // (of no rows: zeros)
+    });
+    if (int rc = check_launch("ionn_residual_norm_bwd")) return rc;
+    if (sums_a || sums_y) {
         const Sums s{part_a, part_y, gate, gamma_a, beta_a, dgate, dgamma_a, dbeta_a, dgamma_y, dbeta_y,
                      runs.groups, runs.chunks, runs.last, uint32_t(blocks), int(cols), runs.whole(), sums_a, sums_y,
                      norm_a == IONN_NORM_LAYER || norm_y == IONN_NORM_LAYER};
