@@ -100,9 +100,10 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float logistic2(float x) { return __builtin_amdgcn_rcpf(1.0f + exp2_fast(x)); }
 // The factor z of a product with a vanishing one, kept finite: the limits at
 // z = -inf (0) and, in the derivatives, at +inf (1) come out instead of
-// inf * 0.  A NaN passes through the other factor.
+// inf * 0.  A NaN passes through the other factor.  (200: there it has vanished in
+// every activation; silu's, exp(z), is the last to leave float32's range, at -88.)
 __device__ __forceinline__ float above(float z) { return fmaxf(z, -200.0f); }
-__device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -30.0f, 30.0f); }
+__device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f); }
 
 // exp(-x^2 / 2) and, of it, Phi(-x); x >= 0.
 __device__ __forceinline__ float normal_exp(float x) { return exp2_fast(x * x * (-0.5f * kLog2e)); }
