@@ -780,7 +780,8 @@ int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W,
 
 /* Its backward pass, for the error dY of Y:
  *   dZ = (dY * u * act'(g) | dY * act(g))   (not stored; float32, and float64
- *     for dtype IONN_F32 with IONN_ACT_NONE or IONN_ACT_RELU)
+ *     for dtype IONN_F32 with IONN_ACT_NONE or IONN_ACT_RELU, where a value
+ *     that float32 would round to infinity counts as that)
  *   gb[o] = sum_b dZ[b][o]                  (float32, a fixed order)
  *   dZ8, edZ = DFP-8 of dZ, one exponent for both halves
  *   dX = fl(dZ8 . W) * 2^(edZ + eW),  G = fl(dZ8^T . X) * 2^(edZ + eX)

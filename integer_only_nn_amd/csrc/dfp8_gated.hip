@@ -195,6 +195,17 @@ __device__ __forceinline__ uint32_t mantissa_of(double x, int negE) {
     return uint32_t(__double_as_longlong(y + 6755399441055744.0));  // 1.5 * 2^52
 }
 
+// Magnitude bits for the largest error's exponent.  Rounding a float64 product to
+// float32 can take it to the next power of two ((1 + 2^-23) (2 - 2^-22) = 2 - 2^-45),
+// so a value rounded up gives the bits below it, of its own power of two; what is
+// beyond float32's numbers stays infinite.
+__device__ __forceinline__ uint32_t top_bits(float x) { return mag_bits(x); }
+__device__ __forceinline__ uint32_t top_bits(double x) {
+    const float f = float(x);
+    const uint32_t b = mag_bits(f);
+    return b - uint32_t(b > 1u && b < 0x7f800000u && fabs(double(f)) > fabs(x));
+}
+
 __device__ __forceinline__ uint32_t block_max(uint32_t v) {
     __shared__ uint32_t red[kThreads / 64];
     v = wave_max_u32(v);
@@ -239,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void gated_sums_kernel(const T *__restric
                 s[0][e] += float(dg);
                 s[1][e] += float(du);
                 // (past a row's end all three are 0, and so are both errors)
-                m = max(m, max(mag_bits(float(dg)), mag_bits(float(du))));
+                m = max(m, max(top_bits(dg), top_bits(du)));
             }
         };
         int64_t r = int64_t(blockIdx.y) * chunk_rows + wave * per_wave + (lane >> lanes_log);

@@ -1,0 +1,36 @@
+"""GPU: the gated layer where a call's edges lie: errors next to a power of two."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import dev, host, say
+from integer_only_nn_amd import ops
+from oracle import floats as of
+from test_gpu_dfp8_linear import _e, _typed, _ws
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", ["none", "relu"])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -20, 2.0 ** 60, 2.0 ** -100])
+@pytest.mark.parametrize("half", ["gate", "up"])
+def test_largest_error_next_to_a_power_of_two(kind, scale, half):
+    """(1 + 2^-23) (2 - 2^-22) = 2 - 2^-45, which float32 rounds to 2: the exponent
+    is that of the product itself (errors behind none and relu are float64)."""
+    rng = np.random.default_rng(3)
+    for B, H, sign in ((1, 1, 1.0), (7, 33, -1.0), (70, 1030, 1.0)):
+        dY, Z = scale * rng.uniform(-1, 1, (B, H)), rng.uniform(0.1, 1, (B, 2 * H))
+        dY, Z = dY.astype(np.float32).astype(np.float64), Z.astype(np.float32).astype(np.float64)
+        r, c = B // 2, H // 3
+        dY[r, c] = sign * scale * (1 + 2.0 ** -23)
+        # u behind the gate's error, g behind the up half's
+        Z[r, c], Z[r, H + c] = (1.0, 2 - 2.0 ** -22) if half == "gate" else (2 - 2.0 ** -22, 1.0)
+        dz = of.gated_error(dY, Z, kind)
+        assert np.abs(dz).max() == scale * (2 - 2.0 ** -45)
+        q, e, st = torch.empty(B, 2 * H, dtype=torch.int8, device=dev()), _e(99), _e(99)
+        say("gated bwd next to a power of two", B, H, kind, scale, half)
+        ops.dfp8_gated_bwd(_typed(dY, "f32"), _typed(Z, "f32"), kind, torch.empty(B, 0, dtype=torch.int8, device=dev()), None,
+                           None, None, q, e, status_out=st, workspace=_ws(ops.dfp8_gated_bwd_workspace_bytes(B, 0, H)))
+        want, exponent = of.dfp8(dz)
+        assert int(host(e)[0]) == exponent and int(host(st)[0]) == 0
+        np.testing.assert_array_equal(host(q), want)
