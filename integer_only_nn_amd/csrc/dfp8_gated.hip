@@ -67,7 +67,7 @@ GatedPlan gated_plan(int64_t B, int64_t IN, int64_t H) {
         const double slow = IN % 4 ? 1.3 : 1.0;
         if (large(c.path) && c.us + copy_us((B + 2 * H) * pitch_of(IN)) < slow * p.us) p = GatedPlan{c, pitch_of(IN)};
     }
-    if (p.path == ROWS) p.cols = 1;
+    if (p.path == ROWS) p.cols = 2;  // a group of gate rows and one of up rows
     p.tiles = ceil_div(B, 64) * ceil_div(H, 32);
     return p;
 }
@@ -474,16 +474,17 @@ int dfp8_gated_fwd(const int8_t *X, const int32_t *eX, const int8_t *W, const in
     const Epi ep{eX, eW, bias, nullptr, Z, Y, absmax_Y, act};
     const GatedPlan plan = gated_plan(B, IN, H);
     Product p = make_product(plan, X, IN, W, IN, ep, B, H, IN, workspace);
-    const int64_t most = path_of(plan, X, W) == ROWS ? ceil_div(H, 16) : int64_t(p.blocks);
-    IONN_REQUIRE(most <= max_groups(path_of(plan, X, W) == ROWS ? kRowWaves * 64 : NT), IONN_ERR_SHAPE,
-                 "dfp8_gated_fwd: B=%lld H=%lld have too many tiles", (long long)B, (long long)H);
+    Copier copies(workspace);
     if (plan.pitch) {
-        Copier c(workspace);
-        p.A = c.add(X, B, IN);
-        p.B = c.add(W, 2 * H, IN);
+        p.A = copies.add(X, B, IN);
+        p.B = copies.add(W, 2 * H, IN);
         p.lda = p.ldb = plan.pitch;
-        c.launch(as_stream(stream));
     }
+    Product both = p;  // its tiles are those of the 2 H rows of W
+    both.N = int(2 * H);
+    IONN_REQUIRE(launches(plan, both), IONN_ERR_SHAPE, "dfp8_gated_fwd: B=%lld H=%lld have too many tiles", (long long)B,
+                 (long long)H);
+    copies.launch(as_stream(stream));
     with_dtype(dtype, [&](auto tag) { launch_gated<decltype(tag)>(plan, p, as_stream(stream)); });
     return check_launch("dfp8_gated_fwd");
 }

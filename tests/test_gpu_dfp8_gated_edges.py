@@ -1,4 +1,5 @@
-"""GPU: the gated layer where a call's edges lie: errors next to a power of two."""
+"""GPU: the gated layer where a call's edges lie: errors next to a power of two,
+outputs of more tiles of 64 than a grid has."""
 import numpy as np
 import pytest
 import torch
@@ -34,3 +35,20 @@ def test_largest_error_next_to_a_power_of_two(kind, scale, half):
         want, exponent = of.dfp8(dz)
         assert int(host(e)[0]) == exponent and int(host(st)[0]) == 0
         np.testing.assert_array_equal(host(q), want)
+
+
+def test_forward_of_more_outputs_than_tiles_of_64():
+    """2^24 tiles of 64 x 32 outputs and more, which larger tiles take."""
+    B, IN, H = (1 << 20) + 70, 512, 1 << 15
+    assert ops.dfp8_linear_path("fwd", B, IN, 2 * H) == "tiles 128"
+    say("gated fwd", B, IN, H)
+    g = torch.Generator(device=dev()).manual_seed(2)
+    X = torch.randint(-128, 128, (B, IN), dtype=torch.int8, device=dev(), generator=g)
+    W = torch.randint(-128, 128, (2 * H, IN), dtype=torch.int8, device=dev(), generator=g)
+    Y = torch.empty(B, H, dtype=torch.bfloat16, device=dev())
+    ops.dfp8_gated_fwd(X, _e(-6), W, _e(-11), Y, act="silu", workspace=_ws(ops.dfp8_gated_fwd_workspace_bytes(B, IN, H)))
+    for first in (0, 12345, B // 2, B - 64):
+        rows = slice(first, first + 64)
+        y = torch.empty(64, H, dtype=torch.bfloat16, device=dev())
+        ops.dfp8_gated_fwd(X[rows], _e(-6), W, _e(-11), y, act="silu", workspace=_ws(ops.dfp8_gated_fwd_workspace_bytes(64, IN, H)))
+        assert torch.equal(Y[rows], y), first
