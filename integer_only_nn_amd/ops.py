@@ -614,6 +614,14 @@ def _same(cond, what):
         raise ValueError(f"shape mismatch: {what}")
 
 
+def _reduced(X, W):
+    """Columns of a layer's input and weights; 0 where neither is given (no gradient of either is asked for)."""
+    for t in (X, W):
+        if t is not None:
+            return t.shape[1]
+    return 0
+
+
 def _space(workspace):
     """Address and bytes of a workspace (None: NULL and 0)."""
     if workspace is None:
@@ -661,10 +669,10 @@ def dfp8_linear_bwd_workspace_bytes(B, IN, OUT):
 
 def dfp8_linear_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None, workspace=None, status_out=None,
                     stream=None):
-    """Z may be None for no activation; X and eX are read for G, W and eW for dX."""
+    """Z may be None for no activation; X and eX are read for G, W and eW for dX (and may be None without)."""
     ys, dt = dY.shape, dY.dtype
     B, OUT = ys
-    IN = (X if X is not None else W).shape[1]
+    IN = _reduced(X, W)
     xs, gs = (B, IN), (OUT, IN)
     ws, nws = _space(workspace)
     rc = lib().dfp8_linear_bwd(_m(dY, dt, ys, "dY"), _m(Z, dt, ys, "Z"), _act(act), _dtype(dY, "dY"),
@@ -700,10 +708,10 @@ def dfp8_gated_bwd_workspace_bytes(B, IN, H):
 
 def dfp8_gated_bwd(dY, Z, act, X, eX, W, eW, dZ8, edZ, dX=None, G=None, gb=None, workspace=None, status_out=None,
                    stream=None):
-    """X and eX are read for G, W and eW for dX."""
+    """X and eX are read for G, W and eW for dX (and may be None without)."""
     ys, dt = dY.shape, dY.dtype
     B, H = ys
-    IN = (X if X is not None else W).shape[1]
+    IN = _reduced(X, W)
     xs, zs, gs = (B, IN), (B, 2 * H), (2 * H, IN)
     ws, nws = _space(workspace)
     rc = lib().dfp8_gated_bwd(_m(dY, dt, ys, "dY"), _m(Z, dt, zs, "Z"), _act(act), _dtype(dY, "dY"),

@@ -1,5 +1,5 @@
 """GPU: the gated layer where a call's edges lie: errors next to a power of two,
-outputs of more tiles of 64 than a grid has."""
+outputs of more tiles of 64 than a grid has, calls for the error alone."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,8 @@ import torch
 from gpu_helpers import dev, host, say
 from integer_only_nn_amd import ops
 from oracle import floats as of
-from test_gpu_dfp8_linear import _e, _typed, _ws
+from test_gpu_dfp8_gated import _backward
+from test_gpu_dfp8_linear import _e, _np, _typed, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,24 @@ def test_forward_of_more_outputs_than_tiles_of_64():
         y = torch.empty(64, H, dtype=torch.bfloat16, device=dev())
         ops.dfp8_gated_fwd(X[rows], _e(-6), W, _e(-11), y, act="silu", workspace=_ws(ops.dfp8_gated_fwd_workspace_bytes(64, IN, H)))
         assert torch.equal(Y[rows], y), first
+
+
+@pytest.mark.parametrize("name,kind", [("f32", "relu"), ("bf16", "silu")])
+def test_the_error_alone(name, kind):
+    """Without dX and G neither X nor W is read, in the gated layer and in the Linear layer."""
+    B, H = 70, 50
+    whole = _backward(B, 40, H, kind, name)
+    dY, Z = _typed(whole["dY"], name), _typed(whole["Z"], name)
+    q, e, gb = torch.empty(B, 2 * H, dtype=torch.int8, device=dev()), _e(99), torch.empty(2 * H, device=dev())
+    ops.dfp8_gated_bwd(dY, Z, kind, None, None, None, None, q, e, gb=gb, workspace=_ws(ops.dfp8_gated_bwd_workspace_bytes(B, 0, H)))
+    np.testing.assert_array_equal(host(q), whole["dZ8"])
+    np.testing.assert_array_equal(_np(gb), whole["gb"])
+    assert int(host(e)[0]) == whole["e"]
+    z = Z[:, :H].contiguous()
+    ws = _ws(ops.dfp8_linear_bwd_workspace_bytes(B, 40, H))
+    got = []
+    for X in (None, torch.ones(B, 40, dtype=torch.int8, device=dev())):
+        q, e, gb = torch.empty(B, H, dtype=torch.int8, device=dev()), _e(99), torch.empty(H, device=dev())
+        ops.dfp8_linear_bwd(dY, z, kind, X, _e(0), None, None, q, e, gb=gb, workspace=ws)
+        got.append((q, e, gb))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
