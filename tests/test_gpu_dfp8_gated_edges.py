@@ -1,5 +1,6 @@
 """GPU: the gated layer where a call's edges lie: errors next to a power of two,
-outputs of more tiles of 64 than a grid has, calls for the error alone."""
+outputs of more tiles of 64 than a grid has, calls for the error alone, and what
+lies behind a backward pass's workspace."""
 import numpy as np
 import pytest
 import torch
@@ -7,8 +8,8 @@ import torch
 from gpu_helpers import dev, host, say
 from integer_only_nn_amd import ops
 from oracle import floats as of
-from test_gpu_dfp8_gated import _backward
-from test_gpu_dfp8_linear import _e, _np, _typed, _ws
+from test_gpu_dfp8_gated import COPIES, _backward
+from test_gpu_dfp8_linear import TYPES, _e, _np, _typed, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,19 @@ def test_the_error_alone(name, kind):
         ops.dfp8_linear_bwd(dY, z, kind, X, _e(0), None, None, q, e, gb=gb, workspace=ws)
         got.append((q, e, gb))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("B,IN,H", [s for s, c in COPIES.items() if c[1]] + [(513, 1281, 769), (4000, 70, 130), (40, 9001, 300)])
+def test_backward_keeps_to_its_workspace(B, IN, H):
+    g = torch.Generator(device=dev()).manual_seed(5)
+    ints = lambda *s: torch.randint(-128, 128, s, dtype=torch.int8, device=dev(), generator=g)  # noqa: E731
+    X, W = ints(B, IN), ints(2 * H, IN)
+    need = ops.dfp8_gated_bwd_workspace_bytes(B, IN, H)
+    ws = torch.full((need + (1 << 20),), 0x5a, dtype=torch.uint8, device=dev())
+    for name, kind in (("f32", "none"), ("bf16", "silu")):
+        dY, Z = (torch.randn(B, n, device=dev(), generator=g).to(TYPES[name]) for n in (H, 2 * H))
+        new = lambda *s, t=TYPES[name]: torch.empty(s, dtype=t, device=dev())  # noqa: E731
+        say("gated bwd", B, IN, H, name)
+        ops.dfp8_gated_bwd(dY, Z, kind, X, _e(-6), W, _e(-12), new(B, 2 * H, t=torch.int8), _e(0), dX=new(B, IN), G=new(2 * H, IN),
+                           gb=new(2 * H, t=torch.float32), workspace=ws[:need])
+        assert (ws[need:] == 0x5a).all()
