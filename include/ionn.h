@@ -970,10 +970,11 @@ int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
  *     X^T in the place of X)
  *   P = P * (1 - lr * weight_decay) - lr * scale[l] * X
  * P, M: float32 [rows[l]][cols[l]]; G: the same of type g_dtype.  The products'
- * operands are held as pairs of float16 terms (22 bits) and summed in float32, so
- * X is right to about 1e-6 of its size.  A u of zeros leaves X = 0; one that is
- * not finite everywhere makes the whole of P not a number.  scale (nullable, HOST
- * [L]): sqrt(max(1, rows / cols)).  lr_dev (nullable, device float) gives lr when
+ * operands are held as pairs of float16 terms (22 bits, steps of 2^-36 at least)
+ * and summed in float32, so X is right to about 1e-6 of its size; where |u| is below
+ * eps / 1000 the steps show, and below 2^-37 an element of u / (|u| + eps) counts as
+ * 0.  A u of zeros leaves X = 0; one that is not finite everywhere makes the whole
+ * of P not a number.  scale (nullable, HOST [L]): sqrt(max(1, rows / cols)).  lr_dev (nullable, device float) gives lr when
  * the kernels run; grad_scale (nullable, device float): 1.  absmax_P (nullable,
  * device uint32 [L]): max-combined with the float32 bits of |P| after the step,
  * for dfp8_from_float.  L >= 1; P, G, M, rows, cols are HOST arrays; rows, cols

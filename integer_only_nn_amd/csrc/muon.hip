@@ -14,6 +14,8 @@
 // keeps the high terms of entries down to 2^-26 of a singular value's size out of
 // float16's subnormal range and the largest entries, 2.8 of b A + c A A, a factor of
 // 5 below its largest value.
+// Steps are 2^-36 at least all the same: an X of 1e-3 (|u| a thousandth of eps), 2048 x
+// 2048, is off by 9e-6 of itself, one of 1e-6 by 9e-3.
 //
 // A product leaves its sums in pieces, and the pass after it adds them, applies
 // the polynomial and writes pairs: for a symmetric matrix both of its halves from
