@@ -27,10 +27,11 @@
 // of the whole tensor first, and a float32 copy of dZ would cost more bytes than
 // computing it again).
 //
-// Measured: 8192 x 4096 -> 4096, bfloat16, silu: forward with z 261 us (2105 TOP/s;
-// the library's int8 product reaches 2134), the errors' passes 53 and 52 us (205 and
-// 273 MB), the two gradients' products 212 and 215; one row 5.6 us (W at 5.9 TB/s);
-// 256 x 784 -> 256, float32, 3.6 forward and 4.2 + 4.9 + 5.4 backward.
+// Measured: 8192 x 4096 -> 4096, bfloat16, silu: forward with z 265 us (2075 TOP/s;
+// the library's int8 product reaches 2141), the errors' passes 53 and 52 us (205 and
+// 273 MB), the two gradients' products 216 and 214; one row 7.9 us (W at 4.3 TB/s; 5.6
+// where the XCDs' L2 hold most of it); 256 x 784 -> 256, float32, 3.5 forward and 4.8 +
+// 4.7 + 5.2 backward.
 #include <type_traits>
 
 #include "dfp8_convert.h"

@@ -23,11 +23,11 @@
 // the end P.  Small tiles do both in one launch.  Matrices of a batch share every
 // launch.
 //
-// Measured: 4096 x 4096, bfloat16 gradients, 3.77 ms a step (4.28 on a card of lower
-// clocks): of each of the five rounds 182 us for each symmetric product and 320 for
-// X's (1200 and 1290 TFLOP/s of float16; the library's float16 product reaches
-// 1366), 33 and 47 us for what follows them (168 to 268 MB, at the rate of a copy),
-// and 29 and 47 us for the momentum and the first X.  1024 x 4096 470 us, 512 x 512
+// Measured: 4096 x 4096, bfloat16 gradients, 3.84 ms a step (3.77 to 4.28 by the card's
+// clocks): of each of the five rounds 171 us for each symmetric product and 307 for
+// X's (1280 and 1340 TFLOP/s of float16; the library's float16 product reaches
+// 1373), 31 and 49 us for what follows them (168 to 268 MB, at the rate of a copy),
+// and 29 and 49 us for the momentum and the first X.  1024 x 4096 470 us, 512 x 512
 // 92, 64 x 64 56: 17 launches of 3.3 us, of which an empty one takes 2.1.
 #include "muon_tile.h"
 

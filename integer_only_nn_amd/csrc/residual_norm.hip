@@ -13,10 +13,12 @@
 // of each `gate_rows` rows.  As single operations they would move the stream
 // through memory once each; together a and x are read and y and n written once
 // (forward), a, y, dy and dn read and da and dx written once (backward), and HBM
-// bounds both.  A row lies in registers, up to eight columns a thread, and the
-// next row's loads are in flight while a row's sums are taken.  Measured: forward 8192
-// x 4096 bf16 48 us (5.6 TB/s, a large copy reaches 5.1); backward 84 us in the first
-// pass (4.8 TB/s) and 8 in the second; 25088 x 256 float32 with 128 gates 28 and 5.
+// bounds both.  A row lies in registers, up to eight columns a thread (sixteen in
+// rows above 8192, where the forward pass reads its vectors again for every row, and
+// in the backward pass of 16-bit rows of 513 to 1024), and the next row's loads are in
+// flight while a row's sums are taken.  Measured, inputs out of the caches: forward 8192 x 4096 bf16 56 us (4.8 TB/s, a large copy reaches 5.2; 49
+// where some of them are in); backward 84 us in the first pass (4.8 TB/s) and 8 in the
+// second; 25088 x 256 float32 with 128 gates 32 and 9.
 //
 // The backward pass needs only four column sums for its five vectors: S1 = sum t
 // and Sh = sum t h_a of the rows that share a gate give that gate's gradient
@@ -33,10 +35,14 @@ constexpr int64_t kMaxCols = 16384;
 constexpr int kMaxGroups = 512;  // workgroups of the backward pass
 
 // store_vec, past the caches where `stream`: tensors larger than an XCD's L2.  2048
-// x 2048 bf16 forward 10.2 against 12.5 us, 8192 x 4096 51.1 against 55.1, backward
-// 92.5 and 94.1, 25088 x 256 float32 backward 35.8 and 39.3; smaller ones take as
+// x 2048 bf16 forward 12.5 against 13.8 us, 8192 x 4096 49.4 against 55.2, backward
+// 90.5 and 92.2, 25088 x 256 float32 backward 37.5 and 39.5; smaller ones take as
 // long either way (1024 x 1024 8.8 and 13.8 us) and stay where the next kernel finds
-// them.
+// them.  With the kernel that reads them next (n to DFP-8; da's conversion in the
+// Linear layer's backward pass) much of the lead goes: 2048 x 2048 16.6 and 17.9,
+// backward 30.2 and 29.8, 25088 x 256 29.7 and 29.0, 53.8 and 52.9, and the largest,
+// which the last-level cache would have held, are behind: 8192 x 4096 75.0 and 71.6,
+// 125.4 and 120.8.
 constexpr size_t kStreamBytes = size_t(4) << 20;
 template <class T, int VE>
 __device__ __forceinline__ void put_vec(T *p, const float (&x)[VE], int valid, bool stream) {
@@ -604,11 +610,12 @@ __global__ __launch_bounds__(kSumCols *kSumGroups) void residual_norm_sum_kernel
 // f(columns of a vector, threads per row, vectors per thread) for a row of cols columns: a part of a
 // wavefront for short rows (32768 x 64 bfloat16 forward 9 us, in a wavefront a row 30;
 // 25088 x 256 12 and 26), one while that takes few vectors a lane (no barrier), then the
-// fewest wavefronts, of some numbers, that hold it in eight columns each (4096 x 5120
-// bfloat16 in 640 threads a row 49 us forward and 57 backward, in 1024 59 and 74; 8192 x
-// 2560 in 320 53 and 48, in 512 53 and 53).  Backward, short rows of 16-bit
-// types are held in four columns each, for eight and the vectors' sums are more than
-// the registers of two workgroups on a compute unit (32768 x 64 12.7 against 19.5 us).
+// fewest wavefronts, of some numbers, that hold it in eight columns each, 16 wavefronts
+// of sixteen columns above 8192 (4096 x 5120 bfloat16 in 640 threads a row 49 us forward
+// and 57 backward, in 1024 59 and 74; 8192 x 2560 in 320 53 and 48, in 512 53 and 53).
+// Backward, short rows of 16-bit types are held in four columns each, for eight and
+// the vectors' sums are more than the registers of two workgroups on a compute unit
+// (32768 x 64 12.7 against 19.5 us).
 template <class T, bool BWD, class F>
 void with_shape(int64_t cols, F &&f) {
     constexpr int VE = 16 / sizeof(T), kShort = BWD ? 4 : VE;
