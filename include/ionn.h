@@ -854,9 +854,10 @@ int ionn_layer_norm_bwd(const void *dy, const void *x, const float *mean,
  * [ceil(rows / gate_rows)][cols], gate_rows rows share a gate (0, or rows and
  * more: all); mean_* (layer norms only), rstd_* (nullable): float [rows], written
  * for the backward pass.  a NULL: y = alpha * x (the norm before the first
- * block).  y NULL or n NULL: not written (without n nor are
- * its norm's other results); n NULL where norm_y is IONN_NORM_NONE.  y and n may be a or x.  absmax_n as in dfp8_linear_fwd.
- * rows >= 0 and below 2^31, 0 <= cols <= 16384; eps >= 0; alpha finite. */
+ * block).  y NULL or n NULL: not written (without n nor are its norm's other
+ * results); n NULL where norm_y is IONN_NORM_NONE.  y and n may be a or x.
+ * absmax_n as in dfp8_linear_fwd.  rows >= 0 and below 2^31, 0 <= cols <= 16384;
+ * eps >= 0; alpha finite. */
 enum { IONN_NORM_NONE = 0, IONN_NORM_LAYER = 1, IONN_NORM_RMS = 2 };
 int ionn_residual_norm_fwd(const void *a, const void *x, int norm_a,
                            const float *gamma_a, const float *beta_a,
@@ -970,17 +971,18 @@ int ionn_adamw_step_carried(int L, float *const *P, const void *const *G,
  *     X^T in the place of X)
  *   P = P * (1 - lr * weight_decay) - lr * scale[l] * X
  * P, M: float32 [rows[l]][cols[l]]; G: the same of type g_dtype.  The products'
- * operands are held as pairs of float16 terms (22 bits, steps of 2^-36 at least)
- * and summed in float32, so X is right to about 1e-6 of its size; where |u| is below
- * eps / 1000 the steps show, and below 2^-37 an element of u / (|u| + eps) counts as
- * 0.  A u of zeros leaves X = 0; one that is not finite everywhere makes the whole
- * of P not a number.  scale (nullable, HOST [L]): sqrt(max(1, rows / cols)).  lr_dev (nullable, device float) gives lr when
- * the kernels run; grad_scale (nullable, device float): 1.  absmax_P (nullable,
+ * operands are held as pairs of float16 terms (22 bits, steps of 2^-36 at
+ * least) and summed in float32, so X is right to about 1e-6 of its size; where
+ * |u| is below eps / 1000 the steps show, and below 2^-37 an element of u /
+ * (|u| + eps) counts as 0.  A u of zeros leaves X = 0; one that is not finite
+ * everywhere makes the whole of P not a number.  scale (nullable, HOST [L]):
+ * sqrt(max(1, rows / cols)).  lr_dev (nullable, device float) gives lr when the
+ * kernels run; grad_scale (nullable, device float): 1.  absmax_P (nullable,
  * device uint32 [L]): max-combined with the float32 bits of |P| after the step,
  * for dfp8_from_float.  L >= 1; P, G, M, rows, cols are HOST arrays; rows, cols
  * >= 1, their product as multiples of 256 at most 2^28; no P or M overlaps
- * another of them or a G (gradients may be one tensor); 0 <= momentum < 1; eps >=
- * 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
+ * another of them or a G (gradients may be one tensor); 0 <= momentum < 1; eps
+ * >= 0; lr and weight_decay finite; ns_steps in [1, 32].  workspace: 256-byte
  * aligned, ionn_muon_workspace_bytes(L, rows, cols) bytes (0 on invalid sizes). */
 size_t ionn_muon_workspace_bytes(int L, const int64_t *rows, const int64_t *cols);
 /* The side of the tiles that matrix l is worked in, with those that share its
